@@ -21,6 +21,8 @@ __all__ = [
     "build_segments", "shrink", "expand", "apply_layer", "apply_layer_noalloc", "decode_layer",
     "decode_layer_launches", "layer_shrink", "layer_expand", "pack_table", "STATIC_SCRATCH_BYTES",
     "status_string", "MAX_RANK", "host_lib", "LinearIO", "LinearQ4IO", "Q4_GROUP", "MASK_INT8_ITEMS", "module_mask",
+    "LinearI8IO", "linear_i8_workspace_bytes", "GroupedIO", "grouped_layer", "grouped_workspace_bytes", "pack_weights",
+    "WEIGHT_ENTRY_DTYPE", "I8_MAX_IN",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +34,10 @@ MODULES = ("q", "k", "v", "o", "gate", "up", "down")
 # lora_adapter_entry_t, 32 bytes
 TABLE_ENTRY_DTYPE = np.dtype([("A", "<u8"), ("B", "<u8"), ("rank", "<i4"), ("scale", "<f4"), ("format", "<i4"),
                               ("reserved", "<i4")])
+# lora_weight_entry_t, 32 bytes
+WEIGHT_ENTRY_DTYPE = np.dtype([("W", "<u8"), ("Ws", "<u8"), ("ldw", "<i8"), ("reserved", "<i8")])
+assert WEIGHT_ENTRY_DTYPE.itemsize == 32
+I8_MAX_IN = 131072  # LORA_I8_MAX_IN
 FORMAT_BF16, FORMAT_INT8_ROWS = 0, 1  # lora_factor_format_t
 assert TABLE_ENTRY_DTYPE.itemsize == 32
 
@@ -60,6 +66,18 @@ class _LinQ4IO(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("Wq", ctypes.c_void_p), ("ldwq", ctypes.c_int64),
                 ("Ws", ctypes.c_void_p), ("lds", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
                 ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32)]
+
+
+class _LinI8IO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("Wq", ctypes.c_void_p), ("ldwq", ctypes.c_int64),
+                ("Ws", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32)]
+
+
+class _GroupedIO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("rows_per_x", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -108,6 +126,18 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = st
             f.argtypes = [ctypes.POINTER(_LinQ4IO), u32, i32, vp, vp, i32, _Seg, i32, vp, sz, vp]
+        for name in ("lora_linear_layer_i8", "lora_linear_shrink_i8", "lora_linear_expand_i8"):
+            f = getattr(L, name)
+            f.restype = st
+            f.argtypes = [ctypes.POINTER(_LinI8IO), u32, i32, vp, vp, i32, _Seg, i32, vp, sz, vp]
+        L.lora_linear_i8_workspace_bytes.restype = sz
+        L.lora_linear_i8_workspace_bytes.argtypes = [i32, i32, i32, i64, i32]
+        L.lora_grouped_workspace_bytes.restype = sz
+        L.lora_grouped_workspace_bytes.argtypes = [i32, i32, i64, i32]
+        L.lora_grouped_layer.restype = st
+        L.lora_grouped_layer.argtypes = [ctypes.POINTER(_GroupedIO), u32, i32, vp, i32, _Seg, vp]
+        L.lora_grouped_layer_i8.restype = st
+        L.lora_grouped_layer_i8.argtypes = [ctypes.POINTER(_GroupedIO), u32, i32, vp, i32, _Seg, vp, sz, vp]
         L.lora_form_batch.restype = st
         L.lora_form_batch.argtypes = [vp, i32, vp, ctypes.c_float, i32, i32, i32, i32, vp, vp]
         _lib = L
@@ -262,41 +292,69 @@ class LinearQ4IO:
         self.d_out = int(Wq.shape[0] if d_out is None else d_out)
 
 
+class LinearI8IO:
+    """One projection for linear_layer with an int8 base: x [rows, >= d_in]
+    bf16, Wq int8 [d_out, >= d_in] (row stride a multiple of 16), Ws float32
+    [d_out] (the scale of each output), y [rows, >= d_out] bf16 (written).
+    Rows of x are quantised in the call."""
+
+    def __init__(self, x, Wq, Ws, y, d_in=None, d_out=None):
+        self.x, self.Wq, self.Ws, self.y = x, Wq, Ws, y
+        self.d_in = int(x.shape[1] if d_in is None else d_in)
+        self.d_out = int(Wq.shape[0] if d_out is None else d_out)
+
+
+def linear_i8_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, sum_d_in: int, n_modules: int) -> int:
+    return int(lib().lora_linear_i8_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules))
+
+
 def linear_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, sum_d_in: int, n_modules: int) -> int:
     return int(lib().lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules))
+
+
+_LINEAR_KINDS = {LinearIO: (_LinIO, ""), LinearQ4IO: (_LinQ4IO, "_q4"), LinearI8IO: (_LinI8IO, "_i8")}
 
 
 def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws, stream=None, module_mask=None,
                  _fn="lora_linear_layer"):
     """Base projection + delta of every projection in ``ios`` ({name:
-    LinearIO}, or {name: LinearQ4IO} for 4-bit base weights); see
-    lora_linear_layer and lora_linear_layer_q4."""
+    LinearIO}, or {name: LinearQ4IO} for 4-bit or {name: LinearI8IO} for int8
+    base weights); see lora_linear_layer, lora_linear_layer_q4 and
+    lora_linear_layer_i8."""
     import torch
     _need(row_adapter, torch.int32, "row_adapter", 1)
-    q4 = any(isinstance(io, LinearQ4IO) for io in ios.values())
-    arr = ((_LinQ4IO if q4 else _LinIO) * 7)()
+    kind = next((k for k in _LINEAR_KINDS if any(isinstance(io, k) for io in ios.values())), LinearIO)
+    struct, suffix = _LINEAR_KINDS[kind]
+    arr = (struct * 7)()
     mask = 0
     for i, name in enumerate(MODULES):
         io = ios.get(name)
         if io is None:
             continue
-        if isinstance(io, LinearQ4IO) != q4:
-            raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO")
-        for t, what in ((io.x, "x"), (io.y, "y")) + (() if q4 else ((io.W, "W"),)):
+        if not isinstance(io, kind):
+            raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every "
+                            "projection LinearI8IO")
+        for t, what in ((io.x, "x"), (io.y, "y")) + (((io.W, "W"),) if kind is LinearIO else ()):
             _need(t, torch.bfloat16, f"{name}.{what}", 2)
         if io.x.shape[0] < num_rows or io.y.shape[0] < num_rows:
             raise ValueError(f"{name}: fewer rows than num_rows")
-        if q4:
+        if kind is LinearQ4IO:
             _need(io.Wq, torch.uint8, f"{name}.Wq", 2)
             _need(io.Ws, torch.float32, f"{name}.Ws", 2)
             arr[i] = _LinQ4IO(io.x.data_ptr(), io.x.stride(0), io.Wq.data_ptr(), io.Wq.stride(0), io.Ws.data_ptr(),
                               io.Ws.stride(0), io.y.data_ptr(), io.y.stride(0), io.d_in, io.d_out)
+        elif kind is LinearI8IO:
+            _need(io.Wq, torch.int8, f"{name}.Wq", 2)
+            _need(io.Ws, torch.float32, f"{name}.Ws", 1)
+            if io.Wq.shape[0] < io.d_out or io.Ws.shape[0] < io.d_out:
+                raise ValueError(f"{name}: fewer weight rows or scales than d_out")
+            arr[i] = _LinI8IO(io.x.data_ptr(), io.x.stride(0), io.Wq.data_ptr(), io.Wq.stride(0), io.Ws.data_ptr(),
+                              io.y.data_ptr(), io.y.stride(0), io.d_in, io.d_out)
         else:
             arr[i] = _LinIO(io.x.data_ptr(), io.x.stride(0), io.W.data_ptr(), io.W.stride(0), io.y.data_ptr(),
                             io.y.stride(0), io.d_in, io.d_out)
         mask |= 1 << i
-    if q4:
-        _fn += "_q4"
+    _fn += suffix
     _check(getattr(lib(), _fn)(arr, mask if module_mask is None else module_mask, num_rows, _ptr(row_adapter),
                                _ptr(table), num_slots, seg.c(), max_rank, _ptr(ws),
                                ws.numel() * ws.element_size(), _stream(stream)), _fn)
@@ -324,6 +382,68 @@ def pack_table(A_ptrs, B_ptrs, ranks, scales, formats=None) -> np.ndarray:
     if formats is not None:
         t["format"] = np.asarray(formats, np.int32)
     return t
+
+
+class GroupedIO:
+    """One projection for grouped_layer: x [ceil(rows / rows_per_x), >= d_in]
+    and y [rows, >= d_out], bf16; row b of the batch reads x row
+    b // rows_per_x.  The weights come from the device table."""
+
+    def __init__(self, x, y, d_in=None, d_out=None, rows_per_x: int = 1):
+        self.x, self.y = x, y
+        self.d_in = int(x.shape[1] if d_in is None else d_in)
+        self.d_out = int(y.shape[1] if d_out is None else d_out)
+        self.rows_per_x = int(rows_per_x)
+
+
+def pack_weights(W_ptrs, ldw, Ws_ptrs=None) -> np.ndarray:
+    """Host bytes of a table of lora_weight_entry_t; arrays of shape
+    [num_slots, 7]: device addresses of the weights (0: none), elements per
+    row, and for int8 weights the addresses of their output scales."""
+    W = np.asarray(W_ptrs, np.uint64)
+    t = np.zeros(W.shape, WEIGHT_ENTRY_DTYPE)
+    t["W"] = W
+    t["ldw"] = np.asarray(ldw, np.int64)
+    if Ws_ptrs is not None:
+        t["Ws"] = np.asarray(Ws_ptrs, np.uint64)
+    return t
+
+
+def grouped_workspace_bytes(num_rows: int, num_slots: int, sum_d_in: int, n_modules: int) -> int:
+    return int(lib().lora_grouped_workspace_bytes(num_rows, num_slots, sum_d_in, n_modules))
+
+
+def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, module_mask=None, int8=False):
+    """Dense products grouped by slot of every projection in ``ios`` ({name:
+    GroupedIO}): y[b] = W_a . x[b // rows_per_x] for the rows in a segment,
+    W_a from the device table ``weights`` (pack_weights).  int8: the table's
+    weights are int8 with output scales, rows of x are quantised in the call
+    and ``ws`` is needed.  See lora_grouped_layer and lora_grouped_layer_i8."""
+    import torch
+    arr = (_GroupedIO * 7)()
+    mask = 0
+    for i, name in enumerate(MODULES):
+        io = ios.get(name)
+        if io is None:
+            continue
+        _need(io.x, torch.bfloat16, f"{name}.x", 2)
+        _need(io.y, torch.bfloat16, f"{name}.y", 2)
+        if io.rows_per_x < 1:
+            raise ValueError(f"{name}: rows_per_x must be >= 1")
+        if io.x.shape[0] < -(-num_rows // io.rows_per_x) or io.y.shape[0] < num_rows:
+            raise ValueError(f"{name}: fewer rows than num_rows")
+        arr[i] = _GroupedIO(io.x.data_ptr(), io.x.stride(0), io.y.data_ptr(), io.y.stride(0), io.d_in, io.d_out,
+                            io.rows_per_x, 0)
+        mask |= 1 << i
+    if module_mask is not None:
+        mask = module_mask
+    if int8:
+        _check(lib().lora_grouped_layer_i8(arr, mask, num_rows, _ptr(weights), num_slots, seg.c(), _ptr(ws),
+                                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+               "lora_grouped_layer_i8")
+    else:
+        _check(lib().lora_grouped_layer(arr, mask, num_rows, _ptr(weights), num_slots, seg.c(), _stream(stream)),
+               "lora_grouped_layer")
 
 
 def build_segments(row_adapter, num_slots: int, seg: Segments, ws, stream=None):

@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "liblora_gemv.so")
 INCLUDE = os.path.join(ROOT, "include")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["api.hip", "segments.hip", "kernels.hip", "batch_former.cpp", "status.cpp"]
+SOURCES = ["api.hip", "segments.hip", "kernels.hip", "gemm.hip", "batch_former.cpp", "status.cpp"]
 # the host-only calls (lora_form_batch, lora_status_string), built apart with
 # the host compiler under AddressSanitizer and UndefinedBehaviorSanitizer
 HOST_SOURCES = ["batch_former.cpp", "status.cpp"]

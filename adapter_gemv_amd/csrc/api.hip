@@ -263,6 +263,21 @@ lora_status_t layer_phase(bool do_shrink, bool do_expand, const lora_module_io_t
   return st;
 }
 
+// Bytes of a row of int8 values (a multiple of 16), and of the quantised rows
+// of sum_d_in inputs in n matrices with their scales.
+int i8_pitch(int d_in) { return (d_in + 15) & ~15; }
+size_t quant_ws_bytes(int64_t num_rows, int64_t sum_d_in, int n) {
+  const size_t per = (size_t)(sum_d_in + 16 * (int64_t)n) * (size_t)num_rows;
+  return per + (size_t)n * ((size_t)num_rows * 4 + 512);
+}
+
+// The end of the v planes of a fused layer call's workspace (a multiple of
+// 256): the int8 form's quantised rows follow.
+size_t linear_v_end(int num_rows, int max_rank, int64_t sum_d_in, int n_modules) {
+  const size_t part = (partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255;
+  return (part + (size_t)n_modules * num_rows * partial_row_stride(max_rank) * 4 + 255) & ~(size_t)255;
+}
+
 }  // namespace
 
 extern "C" {
@@ -275,6 +290,21 @@ size_t lora_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_ran
 // The fused layer's workspace: the shrink's partials, then one v plane
 // [num_rows][rs] per projection (256-byte aligned); at least the segment
 // builder's.
+size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank, int64_t sum_d_in,
+                                      int32_t n_modules) {
+  const size_t base = lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules);
+  if (base == 0) return 0;
+  const size_t need = linear_v_end(num_rows, max_rank, sum_d_in, n_modules) + quant_ws_bytes(num_rows, sum_d_in, n_modules);
+  return need > base ? need : base;
+}
+
+size_t lora_grouped_workspace_bytes(int32_t num_rows, int32_t num_slots, int64_t sum_d_in, int32_t n_modules) {
+  if (num_rows < 0 || num_slots < 1 || sum_d_in < 0 || n_modules < 1 || n_modules > LORA_NUM_MODULES) return 0;
+  const size_t a = quant_ws_bytes(num_rows, sum_d_in, n_modules);
+  const size_t b = segments_ws_bytes(num_rows, num_slots);
+  return a > b ? a : b;
+}
+
 size_t lora_linear_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank, int64_t sum_d_in,
                                    int32_t n_modules) {
   if (num_rows < 0 || num_slots < 1 || max_rank < 1 || max_rank > LORA_MAX_RANK || sum_d_in < 0 || n_modules < 1 ||
@@ -563,7 +593,7 @@ struct LinearArgs {
   int64_t ldx;
   const void *W;   // bf16 [d_out][ldw] elements, or 4-bit [d_out][ldw] bytes
   int64_t ldw;
-  const float *Ws; // 4-bit: group scales [d_out][ldws]
+  const float *Ws; // 4-bit: group scales [d_out][ldws]; int8: scales [d_out]
   int64_t ldws;
   void *y;
   int64_t ldy;
@@ -594,6 +624,86 @@ lora_status_t check_linear(const lora_linear_q4_io_t &m, LinearArgs *a) {
   return LORA_OK;
 }
 
+lora_status_t check_linear(const lora_linear_i8_io_t &m, LinearArgs *a) {
+  if (!m.x || !m.y || !m.Wq || !m.Ws) return LORA_ERR_NULL;
+  if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.ldwq < m.d_in || m.d_in > LORA_I8_MAX_IN)
+    return LORA_ERR_SHAPE;
+  if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || (m.ldwq & 15) || !aligned16(m.x) ||
+      !aligned16(m.y) || !aligned16(m.Wq) || !aligned16(m.Ws))
+    return LORA_ERR_ALIGN;
+  if (m.ldwq > (int64_t)0xFFFFFF00 / m.d_out) return LORA_ERR_SHAPE;
+  *a = LinearArgs{m.x, m.ldx, m.Wq, m.ldwq, static_cast<const float *>(m.Ws), 0, m.y, m.ldy, m.d_in, m.d_out};
+  return LORA_OK;
+}
+
+// ---- the products of gemm_items.h
+
+// One input matrix of a call to quantise, and where its rows go in ws; the
+// projections that share it (same pointer, ldx and d_in) share its rows.
+struct QuantInputs {
+  QuantDesc d{};
+  int n = 0;
+  size_t used = 0;
+  int add(const void *x, int64_t ldx, int d_in, int64_t rows, void *ws) {
+    for (int i = 0; i < n; ++i)
+      if (d.in[i].x == x && d.in[i].ldx == ldx && d.in[i].d_in == d_in && d.in[i].rows == rows) return i;
+    auto &in = d.in[n];
+    in.x = static_cast<const uint16_t *>(x);
+    in.ldx = ldx;
+    in.d_in = d_in;
+    in.rows = (int)rows;
+    in.pitch = i8_pitch(d_in);
+    auto take = [&](size_t bytes) {
+      void *p = static_cast<char *>(ws) + used;
+      used += (bytes + 255) & ~(size_t)255;
+      return p;
+    };
+    in.q = static_cast<int8_t *>(take((size_t)rows * in.pitch));
+    in.s = static_cast<float *>(take((size_t)rows * 4));
+    return n++;
+  }
+};
+
+// The tile configuration of a product (index into gemm_tile): the smallest
+// row tile that holds the rows a block can expect, and the largest tile only
+// where it still gives every compute unit a block.
+int pick_gemm(int64_t rows, int64_t groups, const int *d_out, int n) {
+  const int64_t per = (rows + groups - 1) / groups;
+  for (int cfg = 0; cfg < kGemmTiles - 2; ++cfg)
+    if (per <= gemm_tile(cfg).rows) return cfg;
+  const GemmTile t = gemm_tile(kGemmTiles - 1);
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) blocks += (rows / t.rows) * ((d_out[i] + t.cols - 1) / t.cols);
+  return blocks >= 256 ? kGemmTiles - 1 : kGemmTiles - 2;
+}
+
+// Number the blocks of n projections (g.mod[0..n), longest d_in first: a
+// block's work grows with it and blocks are dispatched in order), fill in what
+// is common and launch.  row_tiles: row tiles of a projection (grouped: the
+// most the segments can give).
+lora_status_t gemm_launch(GemmDesc &g, int n, int64_t row_tiles, int num_rows, int num_slots,
+                          const lora_segments_t &seg, GemmKind kind, int cfg, hipStream_t s) {
+  std::stable_sort(g.mod, g.mod + n, [](const GemmModule &a, const GemmModule &b) { return a.d_in > b.d_in; });
+  const GemmTile tile = gemm_tile(cfg);
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    g.mod[i].n_tiles = (g.mod[i].d_out + tile.cols - 1) / tile.cols;
+    g.mod[i].block_base = (int)blocks;
+    blocks += row_tiles * g.mod[i].n_tiles;
+    if (blocks > 0x7fffffff) return LORA_ERR_SHAPE;
+  }
+  g.n_active = n;
+  g.num_rows = num_rows;
+  g.num_slots = num_slots;
+  g.max_seg = segment_bound(num_rows, num_slots, seg);
+  g.perm = seg.perm;
+  g.seg_offsets = seg.seg_offsets;
+  g.seg_adapter = seg.seg_adapter;
+  g.num_segments = seg.num_segments;
+  g.status = seg.status;
+  return launched(launch_gemm(g, kind, cfg, (int)blocks, s));
+}
+
 // Base projection + delta: the grouped shrink and the partials summed into one
 // v plane per projection (original row order) (do_shrink), then the fused
 // kernel (do_fused).  IO: lora_linear_io_t (bf16 base) or lora_linear_q4_io_t.
@@ -602,6 +712,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
                            const int32_t *row_adapter, const lora_adapter_entry_t *table, int32_t num_slots,
                            lora_segments_t seg, int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
   constexpr bool kQ4 = std::is_same<IO, lora_linear_q4_io_t>::value;
+  constexpr bool kI8 = std::is_same<IO, lora_linear_i8_io_t>::value;
   if (!io || !table) return LORA_ERR_NULL;
   lora_status_t st = check_segments(seg);
   if (st != LORA_OK) return st;
@@ -625,7 +736,8 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
     sum_d_in += m.d_in;
     ++n;
   }
-  const size_t need = lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n);
+  const size_t need = kI8 ? lora_linear_i8_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n)
+                          : lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n);
   if (!ws) return LORA_ERR_NULL;
   if (!aligned16(ws)) return LORA_ERR_ALIGN;
   if (ws_bytes < need) return LORA_ERR_WORKSPACE;
@@ -635,6 +747,16 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
   hipStream_t s = static_cast<hipStream_t>(stream);
   float *vplanes = reinterpret_cast<float *>(static_cast<char *>(ws) +
                                              ((partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255));
+  QuantInputs quant;
+  int quant_of[LORA_NUM_MODULES] = {};
+  if constexpr (kI8) {  // the int8 rows of x, behind the v planes
+    void *qws = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
+    for (int i = 0; i < n; ++i) quant_of[i] = quant.add(la[i].x, la[i].ldx, la[i].d_in, num_rows, qws);
+    if (do_shrink) {
+      st = launched(launch_quantize(quant.d, quant.n, s));
+      if (st != LORA_OK) return st;
+    }
+  }
   if (do_shrink) {
     // 1. v partials of every projection (segment-grouped: each adapter's A once)
     st = launch_phase(true, ms, n, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws, nullptr, 0, s);
@@ -648,6 +770,38 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
     if (st != LORA_OK) return st;
   }
   if (!do_fused) return LORA_OK;
+  if constexpr (kI8) {
+    GemmDesc g{};
+    int outs[LORA_NUM_MODULES];
+    for (int i = 0; i < n; ++i) outs[i] = la[i].d_out;
+    const int cfg = pick_gemm(num_rows, 1, outs, n);
+    const GemmTile tile = gemm_tile(cfg);
+    g.row_tiles = (num_rows + tile.rows - 1) / tile.rows;
+    for (int i = 0; i < n; ++i) {
+      const auto &in = quant.d.in[quant_of[i]];
+      GemmModule &gm = g.mod[i];
+      gm.x = in.q;
+      gm.ldx = in.pitch;
+      gm.xs = in.s;
+      gm.x_bytes = (uint32_t)((int64_t)num_rows * in.pitch);
+      gm.W = static_cast<const uint8_t *>(la[i].W);
+      gm.ldw = la[i].ldw;
+      gm.Ws = la[i].Ws;
+      gm.y = static_cast<uint16_t *>(la[i].y);
+      gm.ldy = la[i].ldy;
+      gm.v = vplanes + (int64_t)i * num_rows * rs;
+      gm.kbytes = in.pitch;
+      gm.d_in = la[i].d_in;
+      gm.d_out = la[i].d_out;
+      gm.col = ms[i].col;
+      gm.rows_per_x = 1;
+    }
+    g.rs = rs;
+    g.max_rank = max_rank;
+    g.ids = row_adapter;
+    g.table = table;
+    return gemm_launch(g, n, g.row_tiles, num_rows, num_slots, seg, kLinearI8, cfg, s);
+  } else {
   // 3. base projection + delta.  A block's work grows with its module's
   // d_in, and the blocks are dispatched in order, so the modules are numbered
   // longest first: a module of a long d_in (a down projection, 3.5x the
@@ -693,6 +847,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
   f.seg_adapter = seg.seg_adapter;
   f.max_seg = segment_bound(num_rows, num_slots, seg);
   return launched(launch_fused(f, kQ4, (int)blocks, s));
+  }
 }
 
 }  // namespace
@@ -741,6 +896,114 @@ lora_status_t lora_linear_expand_q4(const lora_linear_q4_io_t *io, uint32_t modu
                                     size_t ws_bytes, void *stream) {
   return linear_phase(false, true, io, module_mask, num_rows, row_adapter, table, num_slots, seg, max_rank, ws,
                       ws_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks, the quantiser (int8) and the launch of the grouped products.
+lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
+                           const lora_weight_entry_t *weights, int32_t num_slots, const lora_segments_t &seg, void *ws,
+                           size_t ws_bytes, void *stream) {
+  if (!io || !weights) return LORA_ERR_NULL;
+  lora_status_t st = check_segments(seg);
+  if (st != LORA_OK) return st;
+  if (module_mask == 0 || module_mask >= (1u << LORA_NUM_MODULES)) return LORA_ERR_MODULE;
+  if (num_rows < 0 || num_slots < 1) return LORA_ERR_SHAPE;
+  GemmDesc g{};
+  QuantInputs quant;
+  int outs[LORA_NUM_MODULES];
+  int n = 0;
+  int64_t sum_d_in = 0;
+  for (int c = 0; c < LORA_NUM_MODULES; ++c) {
+    if (!(module_mask & (1u << c))) continue;
+    const lora_grouped_io_t &m = io[c];
+    if (!m.x || !m.y) return LORA_ERR_NULL;
+    if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.rows_per_x < 1) return LORA_ERR_SHAPE;
+    if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || !aligned16(m.x) || !aligned16(m.y))
+      return LORA_ERR_ALIGN;
+    if (i8 && m.d_in > LORA_I8_MAX_IN) return LORA_ERR_SHAPE;
+    const int64_t x_rows = ((int64_t)num_rows + m.rows_per_x - 1) / m.rows_per_x;
+    if (!fits_u32(x_rows, m.ldx) || !fits_u32(num_rows, m.ldy)) return LORA_ERR_SHAPE;
+    GemmModule &gm = g.mod[n];
+    gm.x = m.x;
+    gm.ldx = m.ldx * 2;
+    gm.x_bytes = (uint32_t)(x_rows * m.ldx * 2);
+    gm.kbytes = m.d_in * 2;
+    if (i8) {
+      const auto &in = quant.d.in[quant.add(m.x, m.ldx, m.d_in, x_rows, ws)];
+      gm.x = in.q;
+      gm.ldx = gm.kbytes = in.pitch;
+      gm.xs = in.s;
+      gm.x_bytes = (uint32_t)(x_rows * in.pitch);
+    }
+    gm.y = static_cast<uint16_t *>(m.y);
+    gm.ldy = m.ldy;
+    gm.d_in = m.d_in;
+    gm.d_out = outs[n] = m.d_out;
+    gm.col = c;
+    gm.rows_per_x = m.rows_per_x;
+    sum_d_in += m.d_in;
+    ++n;
+  }
+  if (i8) {
+    void *scratch = nullptr;
+    st = check_ws(ws, ws_bytes, lora_grouped_workspace_bytes(num_rows, num_slots, sum_d_in, n), &scratch);
+    if (st != LORA_OK) return st;
+  }
+  if (num_rows == 0) return LORA_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (i8) {
+    st = launched(launch_quantize(quant.d, quant.n, s));
+    if (st != LORA_OK) return st;
+  }
+  g.weights = weights;
+  const int groups = segment_bound(num_rows, num_slots, seg);
+  const int cfg = pick_gemm(num_rows, groups, outs, n);
+  const int rt = gemm_tile(cfg).rows;
+  // every segment's last tile may be partial
+  const int64_t row_tiles = std::min<int64_t>(num_rows, (int64_t)num_rows / rt + groups);
+  return gemm_launch(g, n, row_tiles, num_rows, num_slots, seg, i8 ? kGroupedI8 : kGroupedBf16, cfg, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status_t lora_linear_layer_i8(const lora_linear_i8_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                   const int32_t *row_adapter, const lora_adapter_entry_t *table, int32_t num_slots,
+                                   lora_segments_t seg, int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
+  return linear_phase(true, true, io, module_mask, num_rows, row_adapter, table, num_slots, seg, max_rank, ws,
+                      ws_bytes, stream);
+}
+
+lora_status_t lora_linear_shrink_i8(const lora_linear_i8_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                    const int32_t *row_adapter, const lora_adapter_entry_t *table,
+                                    int32_t num_slots, lora_segments_t seg, int32_t max_rank, void *ws,
+                                    size_t ws_bytes, void *stream) {
+  return linear_phase(true, false, io, module_mask, num_rows, row_adapter, table, num_slots, seg, max_rank, ws,
+                      ws_bytes, stream);
+}
+
+lora_status_t lora_linear_expand_i8(const lora_linear_i8_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                    const int32_t *row_adapter, const lora_adapter_entry_t *table,
+                                    int32_t num_slots, lora_segments_t seg, int32_t max_rank, void *ws,
+                                    size_t ws_bytes, void *stream) {
+  return linear_phase(false, true, io, module_mask, num_rows, row_adapter, table, num_slots, seg, max_rank, ws,
+                      ws_bytes, stream);
+}
+
+lora_status_t lora_grouped_layer(const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                 const lora_weight_entry_t *weights, int32_t num_slots, lora_segments_t seg,
+                                 void *stream) {
+  return grouped_call(false, io, module_mask, num_rows, weights, num_slots, seg, nullptr, 0, stream);
+}
+
+lora_status_t lora_grouped_layer_i8(const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                    const lora_weight_entry_t *weights, int32_t num_slots, lora_segments_t seg,
+                                    void *ws, size_t ws_bytes, void *stream) {
+  return grouped_call(true, io, module_mask, num_rows, weights, num_slots, seg, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

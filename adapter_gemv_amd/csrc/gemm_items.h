@@ -1,0 +1,575 @@
+// Base products on the matrix cores, from int8 or bf16 rows:
+//   * the int8 base projection with the adapter delta (lora_linear_layer_i8):
+//       y[b] = bf16( s_b * Ws[n] * sum_k q_b[k] Wq[n][k] + scale_a B_a.v[b] )
+//     with q_b, s_b the row quantised to int8 (quantize_rows_kernel) and
+//     v[b] = A_a.x[b] from the grouped shrink;
+//   * the dense products grouped by slot (lora_grouped_layer, _i8):
+//       y[b] = bf16( W_a . x[b / rows_per_x] ),  a = the row's slot.
+//
+// One block computes RT rows x NC output columns over the whole input range.
+// A product of 16-byte pieces looks the same to memory and LDS for either
+// type (64 bytes of k per matrix-core step: 32 bf16 or 64 int8 values), so one
+// body serves both and only the matrix-core instruction differs.
+//   * x and W go to LDS by direct loads (no registers in between), S stages of
+//     KB bytes per row in a ring, S - 1 of them in flight.  The 16-byte pieces
+//     of a row are stored at piece ^ (row mod 8), so that the 8 rows an
+//     operand read touches per cycle fall into different banks; the loads
+//     write LDS in lane order, so the lanes fetch the pieces in that order.
+//   * The loads are issued by inline assembly: they return nothing to
+//     registers, and the compiler, which does not know which stage a load
+//     fills, would wait for all of them before every LDS read.  A wave waits
+//     for its own loads of the stage by count (they complete in order), then
+//     the block's barrier covers the other waves' loads.  One barrier per
+//     stage: passing it also means that every wave has read the stage before,
+//     whose place the next loads take.
+//   * W is the matrix-core A operand and x the B operand, so a lane holds 4
+//     consecutive outputs of one row and stores them as 8 bytes.
+//   * The waves form a WR x WC x WK grid over rows, columns and the k of a
+//     stage; with WK > 1 (few rows and columns per block, so that short
+//     batches still fill the device) the partial sums meet in LDS, added in
+//     wave order.
+// Sums are exact in int32 for int8 and in fp32 for bf16; the order of the
+// additions is fixed, so results are bit-reproducible.
+#pragma once
+
+#include "device_common.h"
+
+namespace lora {
+
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+
+template <bool I8_, int RT_, int NC_, int WR_, int WC_, int WK_, int KB_, int S_, int EU_>
+struct GemmCfg {
+  static constexpr bool I8 = I8_;
+  static constexpr int RT = RT_, NC = NC_;             // rows and columns of a block
+  static constexpr int WR = WR_, WC = WC_, WK = WK_;   // wave grid: rows, columns, k
+  static constexpr int KB = KB_, S = S_;               // bytes of k per stage, stages
+  static constexpr int EU = EU_;                       // waves per SIMD it is compiled for
+  static constexpr int NW = WR * WC * WK, THREADS = NW * 64;
+  static constexpr int MT = RT / WR / 16, NT = NC / WC / 16;  // 16 x 16 tiles of a wave
+  static constexpr int NTE = NT >= WK ? NT / WK : 1;   // column tiles a wave finishes (epilogue)
+  static constexpr int PIECES = KB / 16;
+  static constexpr int XL = RT * KB / 1024 / NW, WL = NC * KB / 1024 / NW;  // loads per wave and stage
+  static constexpr int XBYTES = RT * KB, STAGE = (RT + NC) * KB;
+  static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
+  static constexpr int LDS = S * STAGE > RED ? S * STAGE : RED;
+  static_assert(XL >= 1 && WL >= 1 && XL * NW * 1024 == RT * KB && WL * NW * 1024 == NC * KB, "loads per wave");
+  static_assert(KB % (64 * WK) == 0 && KB >= 128, "k steps per wave");
+  static_assert((S - 1) * (XL + WL) < 64, "the load counter holds the stages in flight");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+__device__ __forceinline__ const GemmDesc &gemm_desc() {
+  return *(const GemmDesc *)(const void *)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+// A buffer resource as four scalar words (for the inline-assembly loads).
+__device__ __forceinline__ u32x4 rsrc_words(const void *base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)base;
+  return u32x4{(uint32_t)uniform((int)(uint32_t)a), (uint32_t)uniform((int)((uint32_t)(a >> 32) & 0xffffu)),
+               (uint32_t)uniform((int)bytes), (uint32_t)kBufferWord3};
+}
+
+// 16 bytes per lane from r + voff + soff straight to LDS at lds + 16 * lane
+// (out-of-range lanes write zeros).  Counted by vmcnt; waits are the caller's.
+__device__ __forceinline__ void dma16(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "memory");
+}
+
+// Wait until at most N of this wave's loads are outstanding and its LDS reads
+// are done, then for the block.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+// Segments of at most max_seg, as tiles of RT rows: how many tiles there are,
+// and the segment of one.  Every wave does it for itself, 64 segments a step.
+struct TileOf {
+  int slot, pos0, rows;  // segment's slot, first sorted row of the tile, rows of the tile
+  bool first;            // the segment's first tile
+};
+template <int RT>
+__device__ __forceinline__ int seg_tiles(const GemmDesc &d, int s, int nseg, int *slot, int *o0, int *len) {
+  *slot = -1;
+  *o0 = 0;
+  *len = 0;
+  if (s >= nseg) return 0;
+  *slot = d.seg_adapter[s];
+  *o0 = d.seg_offsets[s];
+  *len = d.seg_offsets[s + 1] - *o0;
+  const bool ok = (unsigned)*slot < (unsigned)d.num_slots && *o0 >= 0 && *len > 0 && *o0 + *len <= d.num_rows;
+  if (!ok) *len = 0;
+  return (*len + RT - 1) / RT;
+}
+__device__ __forceinline__ int wave_scan(int v, int lane) {  // inclusive
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) {
+    const int u = __shfl_up(v, k, 64);
+    if (lane >= k) v += u;
+  }
+  return v;
+}
+template <int RT>
+__device__ __forceinline__ int total_tiles(const GemmDesc &d, int nseg) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int s0 = 0; s0 < nseg; s0 += 64) {
+    int slot, o0, len;
+    total += __builtin_amdgcn_readlane(wave_scan(seg_tiles<RT>(d, s0 + lane, nseg, &slot, &o0, &len), lane), 63);
+  }
+  return total;
+}
+template <int RT>
+__device__ __forceinline__ bool find_tile(const GemmDesc &d, int nseg, int t, TileOf *out) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int s0 = 0; s0 < nseg; s0 += 64) {
+    int slot, o0, len;
+    const int n = seg_tiles<RT>(d, s0 + lane, nseg, &slot, &o0, &len);
+    const int upto = before + wave_scan(n, lane);
+    const uint64_t hit = __ballot(t < upto && n > 0);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const int start = __builtin_amdgcn_readlane(upto - n, l);
+      const int k = t - start;
+      const int length = __builtin_amdgcn_readlane(len, l);
+      out->slot = __builtin_amdgcn_readlane(slot, l);
+      out->pos0 = __builtin_amdgcn_readlane(o0, l) + k * RT;
+      out->rows = min(RT, length - k * RT);
+      out->first = k == 0;
+      return true;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// Order of a module's tiles over its blocks: blocks go to the 8 XCDs in turn,
+// so each XCD takes one contiguous eighth of an order that walks kPatchRows
+// row tiles before it moves to the next column tile; the tiles an XCD works on
+// at one time then share rows and columns in its L2.
+constexpr int kPatchRows = 4;
+__device__ __forceinline__ void tile_order(int local, int row_tiles, int col_tiles, int *rt, int *ct) {
+  const int n = row_tiles * col_tiles;
+  const int xcd = local & 7, i = local >> 3;
+  const int lin = xcd * (n >> 3) + min(xcd, n & 7) + i;
+  const int group = lin / (kPatchRows * col_tiles);
+  const int in = lin - group * kPatchRows * col_tiles;
+  const int gr = min(kPatchRows, row_tiles - group * kPatchRows);
+  *ct = in / gr;
+  *rt = group * kPatchRows + in - *ct * gr;
+}
+
+template <bool I8>
+struct AccOf {
+  typedef f32x4_t type;
+};
+template <>
+struct AccOf<true> {
+  typedef i32x4_t type;
+};
+
+__device__ __forceinline__ f32x4_t mma(u32x4 a, u32x4 b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+__device__ __forceinline__ i32x4_t mma(u32x4 a, u32x4 b, i32x4_t c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0,
+                                               0);
+}
+
+// The delta of one 16-row tile on top of its finished base sums acc[.] (4
+// consecutive outputs of a lane's row per column tile, columns n0 + 16 nt).
+// For each adapter among the 16 rows in turn, B_a's rows are the matrix-core A
+// operand and all 16 rows' v the B operand; the columns of that adapter's rows
+// are then added and the others dropped (selected, not multiplied by zero: a
+// non-finite factor of one row's adapter must not reach the others).  v, fp32,
+// enters as bf16 hi + lo (2^-16 relative).  The next adapter's B is requested
+// before the current one's products.
+// An int8 B (values exact in bf16) comes in the same 16-byte loads: the piece
+// that holds a lane's 8 values, of which it keeps its half; the outputs' scales
+// come with it (1 for bf16), so that no branch stands between a product and
+// the use of its result: there the compiler leaves out the wait states that
+// the matrix cores need (seen as wrong first elements; the assembly shows it).
+struct DeltaRows {
+  int a;                 // this lane's row: slot of its adapter, -1 for none
+  int rank, fmt;
+  const uint8_t *B;
+  V8Split v[2];          // scale * v, columns 32 ks + 8 g ..
+};
+template <int NTE>
+__device__ __forceinline__ void add_delta(const GemmModule &m, const DeltaRows &dr, int n0, f32x4_t (&acc)[NTE]) {
+  const int lane = threadIdx.x & 63, r_in = lane & 15, g = lane >> 4;
+  struct Frag {
+    u32x4 b[NTE][2];
+    f32x4_t s[NTE];
+    int a;
+    bool q8;
+  };
+  uint64_t todo = __ballot(dr.a >= 0) & 0xffffull;
+  auto load = [&](Frag &f) {  // the next adapter among the rows (f.a = -1 at the end)
+    const bool on = todo != 0;
+    const int l = on ? __builtin_ctzll(todo) : 0;
+    f.a = on ? __builtin_amdgcn_readlane(dr.a, l) : -1;
+    todo &= ~__ballot(dr.a == f.a);
+    const int rank = on ? __builtin_amdgcn_readlane(dr.rank, l) : 0;
+    f.q8 = __builtin_amdgcn_readlane(dr.fmt, l) == LORA_FORMAT_INT8_ROWS;
+    const uint8_t *B = (const uint8_t *)(uintptr_t)(
+        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(uintptr_t)dr.B, l) |
+        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uintptr_t)dr.B >> 32), l) << 32));
+    const uint32_t row_bytes = f.q8 ? (uint32_t)ldb8_of(rank) : (uint32_t)((rank + 7) & ~7) * 2;
+    const uint8_t *vals = B + (f.q8 ? q8_values_offset(m.d_out) : 0);
+    const rsrc_t rb = make_rsrc(on ? vals : nullptr, on ? (uint32_t)m.d_out * row_bytes : 0u);
+    const rsrc_t rs = make_rsrc(on && f.q8 ? B : nullptr, on && f.q8 ? q8_values_offset(m.d_out) : 0u);
+#pragma unroll
+    for (int nt = 0; nt < NTE; ++nt) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int n = n0 + nt * 16 + r_in, j = ks * 32 + g * 8;
+        const uint32_t at = f.q8 ? (uint32_t)(j & ~15) : (uint32_t)j * 2;
+        f.b[nt][ks] = buf_ld16_stream(rb, n < m.d_out && j < rank ? (uint32_t)n * row_bytes + at : kOutOfRange, 0);
+      }
+      const int n = n0 + nt * 16 + g * 4;
+      f.s[nt] = __builtin_bit_cast(f32x4_t, buf_ld16(rs, n < m.d_out ? (uint32_t)n * 4 : kOutOfRange, 0));
+    }
+  };
+  auto use = [&](Frag &f) {
+    if (f.q8) {
+#pragma unroll
+      for (int nt = 0; nt < NTE; ++nt)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const u32x4 b = f.b[nt][ks];
+          f.b[nt][ks] = i8x8_to_bf16x8((g & 1) ? u32x2{b.z, b.w} : u32x2{b.x, b.y});
+        }
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NTE; ++nt) f.s[nt] = f32x4_t{1.f, 1.f, 1.f, 1.f};
+    }
+    const bool mine = dr.a == f.a;
+    f32x4_t t[NTE];
+#pragma unroll
+    for (int nt = 0; nt < NTE; ++nt) {
+      t[nt] = mma(f.b[nt][0], dr.v[0].lo, f32x4_t{0.f, 0.f, 0.f, 0.f});
+      t[nt] = mma(f.b[nt][0], dr.v[0].hi, t[nt]);
+      t[nt] = mma(f.b[nt][1], dr.v[1].lo, t[nt]);
+      t[nt] = mma(f.b[nt][1], dr.v[1].hi, t[nt]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NTE; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] = mine ? fmaf(t[nt][i], f.s[nt][i], acc[nt][i]) : acc[nt][i];
+  };
+  Frag cur, nxt;
+  load(cur);
+  while (cur.a >= 0) {
+    load(nxt);
+    use(cur);
+    cur = nxt;
+  }
+}
+
+template <class C, bool GROUPED, bool DELTA>
+__device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
+  typedef typename AccOf<C::I8>::type acc_t;
+  const int t = threadIdx.x, lane = t & 63, w = wave_id();
+  const int r_in = lane & 15, g = lane >> 4;
+  const int wk = w / (C::WR * C::WC), wr = (w / C::WC) % C::WR, wc = w % C::WC;
+
+  int mi = 0;
+#pragma unroll
+  for (int k = 1; k < kMaxModules; ++k)
+    if (k < d.n_active && (int)blockIdx.x >= d.mod[k].block_base) mi = k;
+  const GemmModule m = gemm_desc().mod[mi];
+  const int local = (int)blockIdx.x - m.block_base;
+
+  // the block's rows and columns
+  int row0, rows, ct, slot = 0;
+  const uint8_t *W;
+  const float *Ws;
+  int64_t ldw;
+  if constexpr (GROUPED) {
+    const int nseg = min(uniform(*d.num_segments), d.max_seg);
+    if (blockIdx.x == 0 && w == 0)  // segments that do not fit the batch, counted once per call
+      for (int s = lane; s < nseg; s += 64) {
+        const int a = d.seg_adapter[s], o0 = d.seg_offsets[s], o1 = d.seg_offsets[s + 1];
+        if ((unsigned)a >= (unsigned)d.num_slots || o0 < 0 || o1 <= o0 || o1 > d.num_rows) atomicAdd(d.status, 1);
+      }
+    int rt;
+    if constexpr (C::RT >= 128) {
+      const int total = total_tiles<C::RT>(d, nseg);
+      if (local >= total * m.n_tiles) return;
+      tile_order(local, total, m.n_tiles, &rt, &ct);
+    } else {
+      rt = local / m.n_tiles;
+      ct = local - rt * m.n_tiles;
+    }
+    TileOf tile;
+    if (!find_tile<C::RT>(d, nseg, rt, &tile)) return;
+    row0 = tile.pos0;
+    rows = tile.rows;
+    slot = tile.slot;
+    const lora_weight_entry_t raw = d.weights[(int64_t)slot * kMaxModules + m.col];
+    W = uniform(static_cast<const uint8_t *>(raw.W));
+    Ws = uniform(raw.Ws);
+    const int64_t ld = raw.ldw;
+    ldw = (int64_t)(((uint64_t)(uint32_t)uniform((int)(uint32_t)((uint64_t)ld >> 32)) << 32) |
+                    (uint32_t)uniform((int)(uint32_t)ld));
+    if (W == nullptr) return;  // this slot has no weight for the projection: its rows stay as they are
+    const int elt = C::I8 ? 1 : 2;
+    const bool ok = ((uintptr_t)W & 15) == 0 && ldw >= (C::I8 ? (m.d_in + 15) & ~15 : m.d_in) && ldw % (16 / elt) == 0 &&
+                    ldw <= (int64_t)0xFFFFFF00 / elt / m.d_out &&
+                    (!C::I8 || (Ws != nullptr && ((uintptr_t)Ws & 15) == 0));
+    if (!ok) {
+      if (tile.first && ct == 0 && t == 0) atomicAdd(d.status, 1);
+      return;
+    }
+    ldw *= elt;
+  } else {
+    int rt;
+    if constexpr (C::RT >= 128) {
+      tile_order(local, d.row_tiles, m.n_tiles, &rt, &ct);
+    } else {
+      rt = local / m.n_tiles;
+      ct = local - rt * m.n_tiles;
+    }
+    row0 = rt * C::RT;
+    rows = min(C::RT, d.num_rows - row0);
+    W = m.W;
+    Ws = m.Ws;
+    ldw = m.ldw;
+  }
+  const int n0 = ct * C::NC;
+
+  // ---- this lane's pieces of a stage: offsets of the rows it loads
+  const u32x4 rx = rsrc_words(m.x, m.x_bytes);
+  const u32x4 rw = rsrc_words(W, (uint32_t)(ldw * m.d_out));
+  constexpr int RPI = 1024 / C::KB > 0 ? 1024 / C::KB : 1;  // rows per load instruction
+  static_assert(C::KB <= 1024, "a load instruction covers whole rows");
+  const int lrow = lane / C::PIECES, lslot = lane % C::PIECES;
+  uint32_t xoff[C::XL], woff[C::WL];
+#pragma unroll
+  for (int i = 0; i < C::XL; ++i) {
+    const int r = (i * C::NW + w) * RPI + lrow;
+    const int rr = min(r, rows - 1);  // past the tile: its last row again (never stored)
+    int b = row0 + rr;
+    if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
+    xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & 7)) * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < C::WL; ++i) {
+    const int r = (i * C::NW + w) * RPI + lrow;
+    const int n = min(n0 + r, m.d_out - 1);
+    woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((lslot ^ (r & 7)) * 16);
+  }
+
+  const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+  const int rounds = (m.kbytes + C::KB - 1) / C::KB;
+  const int full = m.kbytes / C::KB;
+  auto issue = [&](int r, uint32_t buf) {
+    const uint32_t soff = (uint32_t)(r * C::KB);
+    const uint32_t at = lds_base + buf + (uint32_t)w * 1024;
+    if (r < full) {
+#pragma unroll
+      for (int i = 0; i < C::XL; ++i) dma16(rx, xoff[i], soff, at + i * C::NW * 1024);
+#pragma unroll
+      for (int i = 0; i < C::WL; ++i) dma16(rw, woff[i], soff, at + C::XBYTES + i * C::NW * 1024);
+    } else {  // the last, partial stage and those past the end: zeros beyond the row
+      const int left = m.kbytes - r * C::KB;
+#pragma unroll
+      for (int i = 0; i < C::XL; ++i) {
+        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & 7);
+        dma16(rx, piece * 16 < left ? xoff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < C::WL; ++i) {
+        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & 7);
+        dma16(rw, piece * 16 < left ? woff[i] + soff : kOutOfRange, 0, at + C::XBYTES + i * C::NW * 1024);
+      }
+    }
+  };
+
+  acc_t acc[C::NT][C::MT];
+#pragma unroll
+  for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = acc_t{0, 0, 0, 0};
+
+  uint32_t put = 0, get = 0;  // ring positions of the next stage to load and to use
+#pragma unroll
+  for (int s = 0; s < C::S - 1; ++s) {
+    issue(s, put);
+    put += C::STAGE;
+  }
+  constexpr int KS = C::KB / 64 / C::WK;  // matrix-core steps of a wave per stage
+  const int xrow = (wr * C::MT * 16 + r_in) * C::KB, wrow = C::XBYTES + (wc * C::NT * 16 + r_in) * C::KB;
+  for (int r = 0; r < rounds; ++r) {
+    stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
+    issue(r + C::S - 1, put);
+    put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
+    const uint8_t *buf = lds + get;
+    get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & 7)) * 16;
+      u32x4 xo[C::MT], wo[C::NT];
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) xo[mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + slot16);
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt) wo[nt] = *(const u32x4 *)(buf + wrow + nt * 16 * C::KB + slot16);
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = mma(wo[nt], xo[mt], acc[nt][mt]);
+    }
+  }
+  stage_barrier<0>();  // nothing in flight to LDS any more, and every wave is done with it
+
+  // ---- sums of the k waves
+  int et0 = 0;  // first column tile this wave finishes
+  acc_t fin[C::NTE][C::MT];
+  if constexpr (C::WK > 1) {
+    acc_t *red = reinterpret_cast<acc_t *>(lds);
+    const int grp = w % (C::WR * C::WC);
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt)
+        red[(((wk * C::WR * C::WC + grp) * C::NT + nt) * C::MT + mt) * 64 + lane] = acc[nt][mt];
+    __syncthreads();
+    et0 = wk * C::NTE;
+    if (et0 >= C::NT) return;
+#pragma unroll
+    for (int e = 0; e < C::NTE; ++e)
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
+        acc_t s = acc_t{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < C::WK; ++k)
+          s += red[(((k * C::WR * C::WC + grp) * C::NT + et0 + e) * C::MT + mt) * 64 + lane];
+        fin[e][mt] = s;
+      }
+  } else {
+#pragma unroll
+    for (int e = 0; e < C::NTE; ++e)
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) fin[e][mt] = acc[e][mt];
+  }
+
+  // ---- scales, delta, rounding, store
+  const int nw0 = n0 + (wc * C::NT + et0) * 16;  // first column of this wave's tiles
+  f32x4_t sw[C::NTE];
+  if constexpr (C::I8) {
+#pragma unroll
+    for (int e = 0; e < C::NTE; ++e) {
+      const int n = nw0 + e * 16 + g * 4;
+      sw[e] = n < m.d_out ? *(const f32x4_t *)(Ws + n) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+  int last_slot = -1;
+  if constexpr (DELTA) {  // segments come in ascending slot order: later slots were dropped by the build
+    const int nseg = min(uniform(*d.num_segments), d.max_seg);
+    last_slot = nseg > 0 ? uniform(d.seg_adapter[nseg - 1]) : -1;
+  }
+#pragma unroll
+  for (int mt = 0; mt < C::MT; ++mt) {
+    const int r = (wr * C::MT + mt) * 16 + r_in;
+    const bool on = r < rows;
+    int b = row0 + min(r, rows - 1);
+    if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1));
+    f32x4_t out[C::NTE];
+    if constexpr (C::I8) {
+      const float sx = m.xs[GROUPED ? b / m.rows_per_x : b];
+#pragma unroll
+      for (int e = 0; e < C::NTE; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[e][i] = (float)fin[e][mt][i] * sx * sw[e][i];
+    } else {
+#pragma unroll
+      for (int e = 0; e < C::NTE; ++e) out[e] = fin[e][mt];
+    }
+    if constexpr (DELTA) {
+      DeltaRows dr;
+      const int a = on ? d.ids[b] : -1;
+      dr.a = -1;
+      dr.rank = dr.fmt = 0;
+      dr.B = nullptr;
+      float scale = 0.f;
+      if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
+        const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + m.col];
+        if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
+          dr.a = a;
+          dr.rank = e.rank;
+          dr.fmt = e.format;
+          dr.B = static_cast<const uint8_t *>(e.B);
+          scale = e.scale;
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        float vv[8];
+        const int j0 = ks * 32 + g * 8;
+        const float *src = m.v + (int64_t)b * d.rs + j0;
+        const bool von = j0 < dr.rank;
+        const f32x4_t lo = von ? *(const f32x4_t *)src : f32x4_t{0.f, 0.f, 0.f, 0.f};
+        const f32x4_t hi = von ? *(const f32x4_t *)(src + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vv[i] = j0 + i < dr.rank ? lo[i] * scale : 0.f;
+          vv[4 + i] = j0 + 4 + i < dr.rank ? hi[i] * scale : 0.f;
+        }
+        dr.v[ks] = split_v8(vv);
+      }
+      add_delta<C::NTE>(m, dr, nw0, out);
+    }
+    if (on) {
+      uint16_t *y = m.y + (int64_t)b * m.ldy;
+#pragma unroll
+      for (int e = 0; e < C::NTE; ++e) {
+        const int n = nw0 + e * 16 + g * 4;
+        if (n < m.d_out)
+          *(u32x2 *)(y + n) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
+      }
+    }
+  }
+}
+
+// Rows of x as int8 with one scale each: s = max|x| / 127, q = rint(127 x /
+// max|x|).  127 x is exact in fp32 for bf16 x, and the quotient of two 8-bit
+// significands times 127 is a tie or at least 2^-9 away from one, so the
+// correctly rounded quotient rounds to the same integer as the real one.  A
+// zero row: q = 0, s = 0.  A row with an infinity or a NaN: s = NaN (its
+// outputs are NaN), q = 0.  A block takes one row (wide: 256 threads) of one
+// distinct input; rows up to kQuantRegs * 2048 values stay in registers
+// between the two passes, longer ones are read again.  [d_in, pitch) gets 0.
+constexpr int kQuantRegs = 4;
+__device__ __forceinline__ float abs_max8(u32x4 p, float m, bool *bad) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = fabsf(bf16_lo(p[i])), b = fabsf(bf16_hi(p[i]));
+    *bad |= !(a <= 3.4e38f) || !(b <= 3.4e38f);
+    m = fmaxf(m, fmaxf(a, b));
+  }
+  return m;
+}
+__device__ __forceinline__ u32x2 quant8(u32x4 p, float amax) {
+  uint32_t o[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = p[h * 2 + i / 2];
+      const float f = (i & 1) ? bf16_hi(u) : bf16_lo(u);
+      v |= ((uint32_t)(int)rintf(f * 127.f / amax) & 0xffu) << (8 * i);
+    }
+    o[h] = v;
+  }
+  return u32x2{o[0], o[1]};
+}
+
+}  // namespace lora

@@ -174,6 +174,70 @@ struct OnePassDesc {
 
 hipError_t launch_onepass(const OnePassDesc &d, int grid, hipStream_t stream);
 
+// ---- Base products on the matrix cores (gemm_items.h): the int8 base
+// projection with its delta, and the dense products grouped by slot.
+struct GemmModule {
+  const void *x;        // bf16 or int8 rows
+  int64_t ldx;          // bytes
+  const float *xs;      // int8: scale of each row of x
+  const uint8_t *W;     // base weight [d_out] rows (not grouped)
+  int64_t ldw;          // bytes
+  const float *Ws;      // int8: scale of each output
+  uint16_t *y;
+  int64_t ldy;
+  const float *v;       // delta: [num_rows][rs], unscaled rank-r vectors
+  uint32_t x_bytes;     // size of x
+  int32_t kbytes;       // bytes of a row of x and W that hold inputs, up to a multiple of 16
+  int32_t d_in;
+  int32_t d_out;
+  int32_t col;          // table column
+  int32_t n_tiles;      // column tiles
+  int32_t block_base;   // first block of this module
+  int32_t rows_per_x;   // grouped: rows of the batch that share one row of x
+};
+
+struct GemmDesc {
+  GemmModule mod[kMaxModules];
+  int32_t n_active;
+  int32_t num_rows;
+  int32_t num_slots;
+  int32_t row_tiles;    // not grouped: row tiles of the batch
+  int32_t max_rank;     // delta
+  int32_t rs;           // delta: floats per row of v
+  int32_t max_seg;
+  const int32_t *ids;   // delta: the rows' slots
+  const int32_t *perm;
+  const int32_t *seg_offsets;
+  const int32_t *seg_adapter;
+  const int32_t *num_segments;
+  int32_t *status;
+  const lora_adapter_entry_t *table;    // delta
+  const lora_weight_entry_t *weights;   // grouped
+};
+
+// Rows of up to kMaxModules distinct inputs to quantise.
+struct QuantDesc {
+  struct {
+    const uint16_t *x;
+    int64_t ldx;       // elements
+    int8_t *q;
+    float *s;
+    int32_t d_in;
+    int32_t pitch;     // bytes of a row of q, a multiple of 16
+    int32_t rows;
+  } in[kMaxModules];
+};
+
+enum GemmKind { kLinearI8 = 0, kGroupedBf16 = 1, kGroupedI8 = 2 };
+// Tile configurations by rows per block; index into gemm_tile().
+struct GemmTile {
+  int rows, cols;
+};
+constexpr int kGemmTiles = 5;
+GemmTile gemm_tile(int cfg);
+hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
+hipError_t launch_quantize(const QuantDesc &d, int n_inputs, hipStream_t stream);
+
 inline int round_up(int a, int b) { return (a + b - 1) / b * b; }
 inline int partial_row_stride(int max_rank) { return round_up(max_rank, 8); }
 

@@ -512,6 +512,171 @@ lora_status_t lora_linear_expand_q4(const lora_linear_q4_io_t *io, uint32_t modu
                                     lora_segments_t seg, int32_t max_rank, void *ws,
                                     size_t ws_bytes, void *stream);
 
+/* One projection of a layer with an int8 base weight, for
+ * lora_linear_layer_i8.  W[n][k] = Ws[n] * Wq[n][k]. */
+typedef struct lora_linear_i8_io {
+  const void *x;  /* device, bf16 [num_rows][ldx]                            */
+  int64_t ldx;
+  const void *Wq; /* device, int8 [d_out][ldwq]                              */
+  int64_t ldwq;   /* bytes per row: >= d_in rounded up to a multiple of 16,
+                     a multiple of 16; bytes [d_in, ldwq) contribute nothing */
+  const void *Ws; /* device, fp32 [d_out]: the scale of each output          */
+  void *y;        /* device, bf16 [num_rows][ldy]: written, W.x + delta      */
+  int64_t ldy;
+  int32_t d_in;   /* up to LORA_I8_MAX_IN                                    */
+  int32_t d_out;
+} lora_linear_i8_io_t;
+
+/* Most inputs of an int8 product: 2^17 products of magnitude at most 127 * 128
+ * stay below 2^31, so the int32 sums are exact. */
+#define LORA_I8_MAX_IN 131072
+
+/*
+ * lora_linear_i8_workspace_bytes -- workspace of lora_linear_layer_i8 for
+ * n_modules projections whose d_in sum to sum_d_in (also enough for
+ * lora_build_segments with the same rows and slots).  0 for bad arguments.
+ */
+size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots,
+                                      int32_t max_rank, int64_t sum_d_in,
+                                      int32_t n_modules);
+
+/*
+ * lora_linear_layer_i8 -- lora_linear_layer with int8 base weights (one scale
+ * per output channel) and the base product in int8: each row of x is
+ * quantised with a scale of its own,
+ *     s_b = max_k |x[b][k]| / 127,   q[b][k] = rint(127 x[b][k] / max|x[b]|)
+ *     y[b][n] = bf16_rne( s_b * Ws[n] * sum_k Wq[n][k] q[b][k]
+ *                         + scale_a * B_a[n] . (A_a . x[b]) ).
+ * q is the exact quotient rounded half to even, the int32 sum is exact, and
+ * the adapter term takes x itself (bf16), not q.  Source: "12. Adapter Serving
+ * and Multi-Tenant Customization", "Interactions with other engine
+ * mechanisms", Quantization (a quantised base with wider adapters, the
+ * contributions accumulated wide); "m07 -- Multi-Adapter (LoRA) Serving", "9.
+ * Bottlenecks and Evolution", item 3 (int8 halves the bytes); one scale per
+ * row and per output channel is this library's reading.  A row of zeros gives
+ * the delta alone; a row that holds an infinity or a NaN gives NaN in all its
+ * outputs, and only there.  Any batch, from one decode row to a prefill: the
+ * tile follows the number of rows.  Projections of a call that share x (same
+ * pointer, ldx and d_in) share its quantised rows.  Launches on `stream`: the
+ * row quantiser, the grouped shrink, the sum of its partials, one product.
+ *
+ *   io           array of LORA_NUM_MODULES entries, read where module_mask
+ *                has a bit: x, Wq, Ws, y 16-byte aligned; d_in, d_out, ldx,
+ *                ldy multiples of 8; Wq below 4 GiB
+ *   ws, ws_bytes at least lora_linear_i8_workspace_bytes(...)
+ *   other arguments as for lora_linear_layer.
+ *
+ * Errors: those of lora_linear_layer; LORA_ERR_NULL for a null Wq or Ws,
+ * LORA_ERR_ALIGN for an ldwq that is not a multiple of 16, LORA_ERR_SHAPE for
+ * ldwq < d_in or d_in > LORA_I8_MAX_IN.
+ */
+lora_status_t lora_linear_layer_i8(const lora_linear_i8_io_t *io, uint32_t module_mask,
+                                   int32_t num_rows, const int32_t *row_adapter,
+                                   const lora_adapter_entry_t *table, int32_t num_slots,
+                                   lora_segments_t seg, int32_t max_rank, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* The two parts of lora_linear_layer_i8, as for lora_linear_shrink and
+ * lora_linear_expand: the shrink part also leaves the quantised rows of x in
+ * the workspace. */
+lora_status_t lora_linear_shrink_i8(const lora_linear_i8_io_t *io, uint32_t module_mask,
+                                    int32_t num_rows, const int32_t *row_adapter,
+                                    const lora_adapter_entry_t *table, int32_t num_slots,
+                                    lora_segments_t seg, int32_t max_rank, void *ws,
+                                    size_t ws_bytes, void *stream);
+lora_status_t lora_linear_expand_i8(const lora_linear_i8_io_t *io, uint32_t module_mask,
+                                    int32_t num_rows, const int32_t *row_adapter,
+                                    const lora_adapter_entry_t *table, int32_t num_slots,
+                                    lora_segments_t seg, int32_t max_rank, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/*
+ * One entry of the device-resident table of dense weights: the whole weight of
+ * one slot for one projection ("m07 ...", "9. Bottlenecks and Evolution": a hot
+ * adapter merged into the weight, W' = W + BA; or the weight of an expert).
+ * A table is an array of these indexed [slot * 7 + module].
+ *   W    device, 16-byte aligned: bf16 [d_out][ldw] (lora_grouped_layer) or
+ *        int8 [d_out][ldw] (lora_grouped_layer_i8; bytes [d_in, ldw) of a row
+ *        contribute nothing).  NULL: the slot has no weight for the
+ *        projection, and its rows of y are left as they are.
+ *   Ws   int8: device fp32 [d_out], 16-byte aligned, the scale of each output;
+ *        bf16: not read.
+ *   ldw  elements per row: bf16 >= d_in and a multiple of 8, int8 >= d_in
+ *        rounded up to a multiple of 16 and a multiple of 16.  A weight stays
+ *        below 4 GiB.
+ * An entry that breaks these rules is a device-data error (see above). 32 bytes.
+ */
+typedef struct lora_weight_entry {
+  const void *W;
+  const float *Ws;
+  int64_t ldw;
+  int64_t reserved; /* set to 0 */
+} lora_weight_entry_t;
+
+/* One projection of a layer for the grouped products. */
+typedef struct lora_grouped_io {
+  const void *x; /* device, bf16 [ceil(num_rows / rows_per_x)][ldx]          */
+  int64_t ldx;
+  void *y;       /* device, bf16 [num_rows][ldy]: rows in a segment written  */
+  int64_t ldy;
+  int32_t d_in;
+  int32_t d_out;
+  int32_t rows_per_x; /* >= 1: row b of the batch reads x row b / rows_per_x
+                         (a token's top-k experts are k rows of one x)       */
+  int32_t reserved;   /* set to 0                                            */
+} lora_grouped_io_t;
+
+/*
+ * lora_grouped_workspace_bytes -- workspace of lora_grouped_layer_i8 for
+ * n_modules projections whose d_in sum to sum_d_in (also enough for
+ * lora_build_segments with the same rows and slots).  0 for bad arguments.
+ */
+size_t lora_grouped_workspace_bytes(int32_t num_rows, int32_t num_slots,
+                                    int64_t sum_d_in, int32_t n_modules);
+
+/*
+ * lora_grouped_layer -- dense products grouped by slot:
+ *     y[b] = bf16_rne( W_a . x[b / rows_per_x] ),   a = the slot of row b,
+ * for every projection in module_mask and every row in a segment; the segments
+ * may have any lengths, and rows in no segment are not touched.  Each slot's
+ * weight is read from the table on the device: adapters merged into their
+ * weights beside the low-rank ones of the same batch, or experts.  Source:
+ * "m07 -- Multi-Adapter (LoRA) Serving", "5. Architecture" and "9. Bottlenecks
+ * and Evolution" (promotion: W' = W + BA for a hot adapter, served as a full
+ * weight); "LoRA, quotas and noisy neighbours", "One weight read, many
+ * adapters" (rows tagged and grouped, each weight read once for its group).
+ * bf16 matrix cores, fp32 sums, one rounding; one launch.
+ *
+ *   io       array of LORA_NUM_MODULES entries, read where module_mask has a
+ *            bit: x, y 16-byte aligned; d_in, d_out, ldx, ldy multiples of 8
+ *   weights  device lora_weight_entry_t [num_slots * 7]
+ *   seg      the segments of the batch (lora_build_segments on the same
+ *            stream before); *seg.status gets one per segment that does not
+ *            fit the batch and one per (segment, projection) whose entry
+ *            cannot be used
+ * No workspace.
+ * Errors: LORA_ERR_NULL, LORA_ERR_SHAPE (sizes, rows_per_x < 1, a matrix of 4
+ * GiB or more), LORA_ERR_ALIGN, LORA_ERR_MODULE (mask 0 or above 0x7f),
+ * LORA_ERR_LAUNCH.
+ */
+lora_status_t lora_grouped_layer(const lora_grouped_io_t *io, uint32_t module_mask,
+                                 int32_t num_rows, const lora_weight_entry_t *weights,
+                                 int32_t num_slots, lora_segments_t seg, void *stream);
+
+/*
+ * lora_grouped_layer_i8 -- lora_grouped_layer with int8 weights (a scale per
+ * output) and each row of x quantised as by lora_linear_layer_i8:
+ *     y[b][n] = bf16_rne( s * Ws_a[n] * sum_k Wq_a[n][k] q[k] ),
+ * q and s of x row b / rows_per_x.  Two launches.
+ *   ws, ws_bytes  at least lora_grouped_workspace_bytes(...), 16-byte aligned
+ * Errors: those of lora_grouped_layer, LORA_ERR_WORKSPACE, and LORA_ERR_SHAPE
+ * for d_in > LORA_I8_MAX_IN.
+ */
+lora_status_t lora_grouped_layer_i8(const lora_grouped_io_t *io, uint32_t module_mask,
+                                    int32_t num_rows, const lora_weight_entry_t *weights,
+                                    int32_t num_slots, lora_segments_t seg, void *ws,
+                                    size_t ws_bytes, void *stream);
+
 /* Most adapters one row may carry in lora_apply_layer_stacked. */
 #define LORA_MAX_STACK 8
 

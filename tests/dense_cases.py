@@ -1,0 +1,111 @@
+"""Inputs and 64-bit references of the int8 base projection and the grouped
+products (no test functions here).  Everything is torch on the CPU; the GPU
+tests move it over.
+
+Tolerances (u = 2^-24, half a step of fp32):
+  * the output's rounding: half a bf16 step, 2^-8 of |y|;
+  * int8 base: the int32 sum is exact; its conversion, the row scale (one
+    division) and the two products round four times: 4 u |base|;
+  * bf16 products: n terms added in fp32 in some order err by at most n u times
+    the sum of their magnitudes (2 n u: an adder of the matrix cores may cut
+    instead of rounding);
+  * delta: the same for A x (n = d_in) and B v (n = rank), and v enters the
+    second product as two bf16 pieces, 2^-16 of its magnitude at most.
+"""
+from __future__ import annotations
+
+import numpy as np
+import torch
+
+U = 2.0 ** -24
+BF = 2.0 ** -8
+MODS = ("q", "k", "v", "o", "gate", "up", "down")
+
+
+def quantise_rows(x):
+    """(q int64, s fp64) of bf16 rows, exact quotients rounded half to even."""
+    x = x.double()
+    amax = x.abs().amax(1) if x.shape[1] else torch.zeros(x.shape[0], dtype=torch.float64)
+    bad = ~torch.isfinite(x).all(1)
+    safe = torch.where((amax > 0) & ~bad, amax, torch.ones_like(amax))
+    q = torch.round(127.0 * torch.where(bad[:, None], torch.zeros_like(x), x) / safe[:, None])
+    s = amax / 127.0
+    s[bad] = float("nan")
+    return q.long(), s
+
+
+def close(got, ref, slack, what):
+    """got (bf16 values), ref and slack fp64 [rows, n]: |got - ref| <= 2^-8 |ref| + slack, NaN where ref is."""
+    got = got.double().cpu()
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    nan = torch.isnan(ref)
+    assert torch.equal(torch.isnan(got), nan), f"{what}: NaN in other places"
+    err = (got - ref).abs()[~nan]
+    tol = (BF * ref.abs() + slack)[~nan] + 1e-30
+    bad = int((err > tol).sum())
+    if bad:
+        i = int((err - tol).argmax())
+        raise AssertionError(f"{what}: {bad} of {err.numel()} out of tolerance; worst {float(err[i])} > {float(tol[i])}")
+
+
+def base_i8(x, Wq, Ws):
+    """(y, slack) of the int8 product in fp64 (integer sums exact below 2^53)."""
+    q, s = quantise_rows(x)
+    acc = torch.matmul(q.double(), Wq.double().t())
+    y = acc * s[:, None] * Ws.double()[None]
+    y[torch.isnan(s)] = float("nan")
+    return y, 4 * U * y.abs().nan_to_num()
+
+
+def delta(x, A, B, scale):
+    """(delta, slack) of one adapter on rows x; A [r, d_in], B [d_out, r] fp64 values."""
+    x, A, B = x.double(), A.double(), B.double()
+    v = x @ A.t()
+    va = x.abs() @ A.abs().t()
+    r, d_in = A.shape
+    d = scale * (v @ B.t())
+    mag = abs(scale) * (va @ B.abs().t())
+    return d, (2 * (d_in + r + 2) * U + 2.0 ** -16) * mag
+
+
+def grouped_bf16(x, W):
+    x, W = x.double(), W.double()
+    return x @ W.t(), 2 * (W.shape[1] + 2) * U * (x.abs() @ W.abs().t())
+
+
+def int8_weight(gen, d_out, d_in, pitch=None):
+    """(Wq padded to a multiple of 16 with junk in the padding, Ws)."""
+    pitch = -(-d_in // 16) * 16 if pitch is None else pitch
+    Wq = torch.randint(-127, 128, (d_out, pitch), generator=gen, dtype=torch.int32).to(torch.int8)
+    Wq[:, :2] = -128  # the type's lowest value too
+    Ws = (torch.rand(d_out, generator=gen) + 0.5) / 127 * d_in ** -0.5
+    return Wq, Ws
+
+
+def bf16(gen, *shape, std=1.0):
+    return (torch.randn(*shape, generator=gen) * std).to(torch.bfloat16)
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def ids_of(kind, n, slots, seed):
+    r = np.random.RandomState(seed)
+    if kind == "distinct":
+        ids = r.permutation(max(n, slots))[:n] % slots
+    elif kind == "runs":
+        cuts = np.sort(r.randint(0, n + 1, max(slots - 1, 0)))
+        ids = np.searchsorted(cuts, np.arange(n), side="right")
+        ids = r.permutation(slots)[np.minimum(ids, slots - 1)]
+    elif kind == "one":
+        ids = np.full(n, slots - 1)
+    elif kind == "none":
+        ids = np.full(n, -1)
+    else:  # mixed: uniform, some base only, some out of range
+        ids = r.randint(0, slots, n)
+        ids[r.rand(n) < 0.15] = -1
+        ids[r.rand(n) < 0.05] = slots + 3
+    return ids.astype(np.int32)
