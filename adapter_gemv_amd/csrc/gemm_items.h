@@ -38,8 +38,9 @@ namespace lora {
 
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 
-template <bool I8_, int RT_, int NC_, int WR_, int WC_, int WK_, int KB_, int S_, int EU_>
+template <bool I8_, int RT_, int NC_, int WR_, int WC_, int WK_, int KB_, int S_, int EU_, bool PIPE_ = false>
 struct GemmCfg {
+  static constexpr bool PIPE = PIPE_;                  // operands one step ahead in registers
   static constexpr bool I8 = I8_;
   static constexpr int RT = RT_, NC = NC_;             // rows and columns of a block
   static constexpr int WR = WR_, WC = WC_, WK = WK_;   // wave grid: rows, columns, k
@@ -180,6 +181,21 @@ __device__ __forceinline__ f32x4_t mma(u32x4 a, u32x4 b, f32x4_t c) {
 __device__ __forceinline__ i32x4_t mma(u32x4 a, u32x4 b, i32x4_t c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0,
                                                0);
+}
+
+// The same product with the sums pinned in place in accumulation registers
+// (the pipelined loop): a wave's 256 sums fill that file, and left to itself
+// the compiler moves them about.  The wait before the sums are read
+// (mma_drain) is the caller's.
+__device__ __forceinline__ void mma_acc(u32x4 a, u32x4 b, f32x4_t &c) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mma_acc(u32x4 a, u32x4 b, i32x4_t &c) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mma_drain() {
+  asm volatile("s_nop 15\n\ts_nop 15" : : : "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // The delta of one 16-row tile on top of its finished base sums acc[.] (4
@@ -399,14 +415,66 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = acc_t{0, 0, 0, 0};
 
+  constexpr int KS = C::KB / 64 / C::WK;  // matrix-core steps of a wave per stage
+  const int xrow = (wr * C::MT * 16 + r_in) * C::KB, wrow = C::XBYTES + (wc * C::NT * 16 + r_in) * C::KB;
+  if constexpr (C::PIPE) {
+    static_assert(!C::PIPE || (C::S == 2 && C::WK == 1 && KS == 2), "the pipelined loop");
+    u32x4 xa[C::MT], wa[C::NT], xb[C::MT], wb[C::NT];
+    const int s0 = ((0 + g) ^ (r_in & 7)) * 16, s1 = ((4 + g) ^ (r_in & 7)) * 16;
+    issue(0, 0);
+    issue(1, C::STAGE);
+    stage_barrier<C::XL + C::WL>();
+#pragma unroll
+    for (int mt = 0; mt < C::MT; ++mt) xa[mt] = *(const u32x4 *)(lds + xrow + mt * 16 * C::KB + s0);
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt) wa[nt] = *(const u32x4 *)(lds + wrow + nt * 16 * C::KB + s0);
+    auto round = [&](int r, uint32_t cur, bool fast) {
+      const uint8_t *buf = lds + cur, *nbuf = lds + (C::STAGE - cur);
+      constexpr int PER = C::MT * C::NT / (C::MT + C::NT);  // products per operand read
+      // step 0: its operands are in xa, wa; those of step 1 are read meanwhile
+#pragma unroll
+      for (int i = 0; i < C::MT + C::NT; ++i) {
+        if (i < C::MT) xb[i] = *(const u32x4 *)(buf + xrow + i * 16 * C::KB + s1);
+        else wb[i - C::MT] = *(const u32x4 *)(buf + wrow + (i - C::MT) * 16 * C::KB + s1);
+#pragma unroll
+        for (int k = i * PER; k < (i + 1) * PER; ++k) mma_acc(wa[k / C::MT], xa[k % C::MT], acc[k / C::MT][k % C::MT]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      stage_barrier<0>();  // stage r + 1 is there, and every wave holds the rest of stage r
+      const uint32_t soff = (uint32_t)((r + 2) * C::KB);
+      const uint32_t at = lds_base + cur + (uint32_t)w * 1024;
+      if (!fast) issue(r + 2, cur);
+#pragma unroll
+      for (int i = 0; i < C::MT + C::NT; ++i) {
+        if (i < C::MT) xa[i] = *(const u32x4 *)(nbuf + xrow + i * 16 * C::KB + s0);
+        else wa[i - C::MT] = *(const u32x4 *)(nbuf + wrow + (i - C::MT) * 16 * C::KB + s0);
+        if (fast) {
+          if (i < C::XL) dma16(rx, xoff[i], soff, at + i * C::NW * 1024);
+          else if (i < C::XL + C::WL) dma16(rw, woff[i - C::XL], soff, at + C::XBYTES + (i - C::XL) * C::NW * 1024);
+        }
+#pragma unroll
+        for (int k = i * PER; k < (i + 1) * PER; ++k) mma_acc(wb[k / C::MT], xb[k % C::MT], acc[k / C::MT][k % C::MT]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int r = 0;
+    uint32_t cur = 0;
+    for (; r + 2 < full; ++r) {
+      round(r, cur, true);
+      cur = C::STAGE - cur;
+    }
+    for (; r < rounds; ++r) {
+      round(r, cur, false);
+      cur = C::STAGE - cur;
+    }
+    mma_drain();
+  } else {
   uint32_t put = 0, get = 0;  // ring positions of the next stage to load and to use
 #pragma unroll
   for (int s = 0; s < C::S - 1; ++s) {
     issue(s, put);
     put += C::STAGE;
   }
-  constexpr int KS = C::KB / 64 / C::WK;  // matrix-core steps of a wave per stage
-  const int xrow = (wr * C::MT * 16 + r_in) * C::KB, wrow = C::XBYTES + (wc * C::NT * 16 + r_in) * C::KB;
   for (int r = 0; r < rounds; ++r) {
     stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
     issue(r + C::S - 1, put);
@@ -426,6 +494,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = mma(wo[nt], xo[mt], acc[nt][mt]);
     }
+  }
   }
   stage_barrier<0>();  // nothing in flight to LDS any more, and every wave is done with it
 
@@ -524,7 +593,16 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         }
         dr.v[ks] = split_v8(vv);
       }
-      add_delta<C::NTE>(m, dr, nw0, out);
+      constexpr int DT = C::NTE < 4 ? C::NTE : 4;  // column tiles whose B is held at a time
+#pragma unroll
+      for (int e = 0; e < C::NTE; e += DT) {
+        f32x4_t part[DT];
+#pragma unroll
+        for (int k = 0; k < DT; ++k) part[k] = out[e + k];
+        add_delta<DT>(m, dr, nw0 + e * 16, part);
+#pragma unroll
+        for (int k = 0; k < DT; ++k) out[e + k] = part[k];
+      }
     }
     if (on) {
       uint16_t *y = m.y + (int64_t)b * m.ldy;
