@@ -6,10 +6,10 @@
 namespace lora {
 namespace {
 
-template <class C, bool GROUPED, bool DELTA>
+template <class C, bool GROUPED, int KT>
 __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::EU))) void lora_gemm_kernel(GemmDesc d) {
   __shared__ __align__(16) uint8_t lds[C::LDS];
-  gemm_block<C, GROUPED, DELTA>(d, lds);
+  gemm_block<C, GROUPED, KT>(d, lds);
 }
 
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantDesc qd) {
@@ -63,18 +63,18 @@ template <bool I8> using Cfg64 = GemmCfg<I8, 64, 64, 2, 2, 1, 128, 4, 2>;
 template <bool I8> using Cfg128 = GemmCfg<I8, 128, 128, 2, 2, 1, 128, 4, 1>;
 template <bool I8> using Cfg256 = GemmCfg<I8, 256, 256, 2, 2, 1, 128, 2, 1, true>;
 
-template <class C, bool GROUPED, bool DELTA>
+template <class C, bool GROUPED, int KT>
 void launch(const GemmDesc &d, int blocks, hipStream_t s) {
-  lora_gemm_kernel<C, GROUPED, DELTA><<<blocks, C::THREADS, 0, s>>>(d);
+  lora_gemm_kernel<C, GROUPED, KT><<<blocks, C::THREADS, 0, s>>>(d);
 }
-template <bool I8, bool GROUPED, bool DELTA>
+template <bool I8, bool GROUPED, int KT>
 void pick(const GemmDesc &d, int cfg, int blocks, hipStream_t s) {
   switch (cfg) {
-    case 0: launch<Cfg16<I8>, GROUPED, DELTA>(d, blocks, s); break;
-    case 1: launch<Cfg32<I8>, GROUPED, DELTA>(d, blocks, s); break;
-    case 2: launch<Cfg64<I8>, GROUPED, DELTA>(d, blocks, s); break;
-    case 3: launch<Cfg128<I8>, GROUPED, DELTA>(d, blocks, s); break;
-    default: launch<Cfg256<I8>, GROUPED, DELTA>(d, blocks, s); break;
+    case 0: launch<Cfg16<I8>, GROUPED, KT>(d, blocks, s); break;
+    case 1: launch<Cfg32<I8>, GROUPED, KT>(d, blocks, s); break;
+    case 2: launch<Cfg64<I8>, GROUPED, KT>(d, blocks, s); break;
+    case 3: launch<Cfg128<I8>, GROUPED, KT>(d, blocks, s); break;
+    default: launch<Cfg256<I8>, GROUPED, KT>(d, blocks, s); break;
   }
 }
 
@@ -93,9 +93,12 @@ GemmTile gemm_tile(int cfg) {
 hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream) {
   if (blocks <= 0) return hipSuccess;
   switch (kind) {
-    case kLinearI8: pick<true, false, true>(d, cfg, blocks, stream); break;
-    case kGroupedBf16: pick<false, true, false>(d, cfg, blocks, stream); break;
-    default: pick<true, true, false>(d, cfg, blocks, stream); break;
+    case kLinearI8:
+      if (d.max_rank <= 32) pick<true, false, 1>(d, cfg, blocks, stream);
+      else pick<true, false, 2>(d, cfg, blocks, stream);
+      break;
+    case kGroupedBf16: pick<false, true, 0>(d, cfg, blocks, stream); break;
+    default: pick<true, true, 0>(d, cfg, blocks, stream); break;
   }
   return hipGetLastError();
 }

@@ -53,7 +53,13 @@ struct GemmCfg {
   static constexpr int XL = RT * KB / 1024 / NW, WL = NC * KB / 1024 / NW;  // loads per wave and stage
   static constexpr int XBYTES = RT * KB, STAGE = (RT + NC) * KB;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
-  static constexpr int LDS = S * STAGE > RED ? S * STAGE : RED;
+  static constexpr int TAIL = RED + 32 * RT;           // and the rows' descriptions, when the ring is done
+  static constexpr int LDS = S * STAGE > TAIL ? S * STAGE : TAIL;
+  static constexpr int DT = NTE < 4 ? NTE : 4;         // column tiles finished at a time
+  // Adapters whose B is in flight or in use (delta): rows of one decode tile
+  // all differ, and a wave waits for each adapter in turn; the rows of a
+  // prefill tile share one, which is kept from row tile to row tile instead.
+  static constexpr int AHEAD = RT >= 256 ? 1 : 4;
   static_assert(XL >= 1 && WL >= 1 && XL * NW * 1024 == RT * KB && WL * NW * 1024 == NC * KB, "loads per wave");
   static_assert(KB % (64 * WK) == 0 && KB >= 128, "k steps per wave");
   static_assert((S - 1) * (XL + WL) < 64, "the load counter holds the stages in flight");
@@ -204,94 +210,155 @@ __device__ __forceinline__ void mma_drain() {
 // operand and all 16 rows' v the B operand; the columns of that adapter's rows
 // are then added and the others dropped (selected, not multiplied by zero: a
 // non-finite factor of one row's adapter must not reach the others).  v, fp32,
-// enters as bf16 hi + lo (2^-16 relative).  The next adapter's B is requested
-// before the current one's products.
+// enters as bf16 hi + lo (2^-16 relative).  The B of the next adapters is
+// requested before the current one's products (AHEAD).
 // An int8 B (values exact in bf16) comes in the same 16-byte loads: the piece
-// that holds a lane's 8 values, of which it keeps its half; the outputs' scales
-// come with it (1 for bf16), so that no branch stands between a product and
-// the use of its result: there the compiler leaves out the wait states that
-// the matrix cores need (seen as wrong first elements; the assembly shows it).
-struct DeltaRows {
-  int a;                 // this lane's row: slot of its adapter, -1 for none
-  int rank, fmt;
-  const uint8_t *B;
-  V8Split v[2];          // scale * v, columns 32 ks + 8 g ..
+// that holds a lane's 8 values, of which it keeps its half; the output scales
+// come one per lane and are handed round.
+
+// Hold results of the matrix cores until they may be read: the compiler counts
+// the wait states on one of the paths that lead to the read only, so a branch
+// between them can leave too few (seen as wrong first elements of a tile).
+template <int N>
+__device__ __forceinline__ void mma_settle(f32x4_t (&t)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "tiles");
+  if constexpr (N == 1) asm volatile("s_nop 10" : "+v"(t[0]));
+  else if constexpr (N == 2) asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]));
+  else asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
+}
+
+// A row of the block's tile, in LDS for the epilogue.
+struct RowInfo {
+  const uint8_t *B;      // its adapter's B
+  int32_t a;             // and slot (-1: none)
+  int32_t rank, fmt;
+  float scale;
+  float xs;              // int8: the row's scale
+  int32_t b;             // its place in the batch
 };
-template <int NTE>
-__device__ __forceinline__ void add_delta(const GemmModule &m, const DeltaRows &dr, int n0, f32x4_t (&acc)[NTE]) {
+static_assert(sizeof(RowInfo) == 32, "RowInfo");
+
+// The B of one adapter for DT column tiles: values and output scales.
+template <int DT, int KT>
+struct BFrag {
+  u32x4 b[DT][KT];
+  float s[DT];
+  int a = -1;
+  bool q8;
+};
+
+template <int DT, int KT>
+__device__ __forceinline__ void load_b(const GemmModule &m, const RowInfo &ri, int l, bool on, int n0,
+                                       BFrag<DT, KT> &f) {
   const int lane = threadIdx.x & 63, r_in = lane & 15, g = lane >> 4;
-  struct Frag {
-    u32x4 b[NTE][2];
-    f32x4_t s[NTE];
-    int a;
-    bool q8;
-  };
-  uint64_t todo = __ballot(dr.a >= 0) & 0xffffull;
-  auto load = [&](Frag &f) {  // the next adapter among the rows (f.a = -1 at the end)
-    const bool on = todo != 0;
-    const int l = on ? __builtin_ctzll(todo) : 0;
-    f.a = on ? __builtin_amdgcn_readlane(dr.a, l) : -1;
-    todo &= ~__ballot(dr.a == f.a);
-    const int rank = on ? __builtin_amdgcn_readlane(dr.rank, l) : 0;
-    f.q8 = __builtin_amdgcn_readlane(dr.fmt, l) == LORA_FORMAT_INT8_ROWS;
-    const uint8_t *B = (const uint8_t *)(uintptr_t)(
-        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(uintptr_t)dr.B, l) |
-        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uintptr_t)dr.B >> 32), l) << 32));
-    const uint32_t row_bytes = f.q8 ? (uint32_t)ldb8_of(rank) : (uint32_t)((rank + 7) & ~7) * 2;
-    const uint8_t *vals = B + (f.q8 ? q8_values_offset(m.d_out) : 0);
-    const rsrc_t rb = make_rsrc(on ? vals : nullptr, on ? (uint32_t)m.d_out * row_bytes : 0u);
-    const rsrc_t rs = make_rsrc(on && f.q8 ? B : nullptr, on && f.q8 ? q8_values_offset(m.d_out) : 0u);
+  f.a = on ? __builtin_amdgcn_readlane(ri.a, l) : -1;
+  const int rank = on ? __builtin_amdgcn_readlane(ri.rank, l) : 0;
+  f.q8 = __builtin_amdgcn_readlane(ri.fmt, l) == LORA_FORMAT_INT8_ROWS;
+  const uint8_t *B = (const uint8_t *)(uintptr_t)(
+      (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(uintptr_t)ri.B, l) |
+      ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uintptr_t)ri.B >> 32), l) << 32));
+  const uint32_t row_bytes = f.q8 ? (uint32_t)ldb8_of(rank) : (uint32_t)((rank + 7) & ~7) * 2;
+  const uint8_t *vals = B + (f.q8 ? q8_values_offset(m.d_out) : 0);
+  const rsrc_t rb = make_rsrc(on ? vals : nullptr, on ? (uint32_t)m.d_out * row_bytes : 0u);
+  const rsrc_t rs = make_rsrc(on && f.q8 ? B : nullptr, on && f.q8 ? q8_values_offset(m.d_out) : 0u);
 #pragma unroll
-    for (int nt = 0; nt < NTE; ++nt) {
+  for (int nt = 0; nt < DT; ++nt) {
+    const int n = n0 + nt * 16 + r_in;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const int n = n0 + nt * 16 + r_in, j = ks * 32 + g * 8;
-        const uint32_t at = f.q8 ? (uint32_t)(j & ~15) : (uint32_t)j * 2;
-        f.b[nt][ks] = buf_ld16_stream(rb, n < m.d_out && j < rank ? (uint32_t)n * row_bytes + at : kOutOfRange, 0);
-      }
-      const int n = n0 + nt * 16 + g * 4;
-      f.s[nt] = __builtin_bit_cast(f32x4_t, buf_ld16(rs, n < m.d_out ? (uint32_t)n * 4 : kOutOfRange, 0));
+    for (int ks = 0; ks < KT; ++ks) {
+      const int j = ks * 32 + g * 8;
+      const uint32_t at = f.q8 ? (uint32_t)(j & ~15) : (uint32_t)j * 2;
+      f.b[nt][ks] = buf_ld16_stream(rb, n < m.d_out && j < rank ? (uint32_t)n * row_bytes + at : kOutOfRange, 0);
     }
-  };
-  auto use = [&](Frag &f) {
-    if (f.q8) {
-#pragma unroll
-      for (int nt = 0; nt < NTE; ++nt)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const u32x4 b = f.b[nt][ks];
-          f.b[nt][ks] = i8x8_to_bf16x8((g & 1) ? u32x2{b.z, b.w} : u32x2{b.x, b.y});
-        }
-    } else {
-#pragma unroll
-      for (int nt = 0; nt < NTE; ++nt) f.s[nt] = f32x4_t{1.f, 1.f, 1.f, 1.f};
-    }
-    const bool mine = dr.a == f.a;
-    f32x4_t t[NTE];
-#pragma unroll
-    for (int nt = 0; nt < NTE; ++nt) {
-      t[nt] = mma(f.b[nt][0], dr.v[0].lo, f32x4_t{0.f, 0.f, 0.f, 0.f});
-      t[nt] = mma(f.b[nt][0], dr.v[0].hi, t[nt]);
-      t[nt] = mma(f.b[nt][1], dr.v[1].lo, t[nt]);
-      t[nt] = mma(f.b[nt][1], dr.v[1].hi, t[nt]);
-    }
-#pragma unroll
-    for (int nt = 0; nt < NTE; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = mine ? fmaf(t[nt][i], f.s[nt][i], acc[nt][i]) : acc[nt][i];
-  };
-  Frag cur, nxt;
-  load(cur);
-  while (cur.a >= 0) {
-    load(nxt);
-    use(cur);
-    cur = nxt;
+    f.s[nt] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, n < m.d_out ? (uint32_t)n * 4 : kOutOfRange, 0, 0));
   }
 }
 
-template <class C, bool GROUPED, bool DELTA>
+template <int DT, int KT>
+__device__ __forceinline__ void use_b(const RowInfo &ri, const V8Split (&v)[KT], const BFrag<DT, KT> &f,
+                                      f32x4_t (&acc)[DT]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  u32x4 b[DT][KT];
+  f32x4_t sc[DT];
+#pragma unroll
+  for (int nt = 0; nt < DT; ++nt) {
+#pragma unroll
+    for (int ks = 0; ks < KT; ++ks) b[nt][ks] = f.b[nt][ks];
+    sc[nt] = f32x4_t{1.f, 1.f, 1.f, 1.f};
+  }
+  if (f.q8) {
+#pragma unroll
+    for (int nt = 0; nt < DT; ++nt) {
+#pragma unroll
+      for (int ks = 0; ks < KT; ++ks)
+        b[nt][ks] = i8x8_to_bf16x8((g & 1) ? u32x2{b[nt][ks].z, b[nt][ks].w} : u32x2{b[nt][ks].x, b[nt][ks].y});
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[nt][i] = __shfl(f.s[nt], 4 * g + i, 64);
+    }
+  }
+  const bool mine = ri.a == f.a;
+  f32x4_t t[DT];
+#pragma unroll
+  for (int nt = 0; nt < DT; ++nt) {
+    t[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < KT; ++ks) {
+      t[nt] = mma(b[nt][ks], v[ks].lo, t[nt]);
+      t[nt] = mma(b[nt][ks], v[ks].hi, t[nt]);
+    }
+  }
+  mma_settle(t);
+#pragma unroll
+  for (int nt = 0; nt < DT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[nt][i] = mine ? fmaf(t[nt][i], sc[nt][i], acc[nt][i]) : acc[nt][i];
+}
+
+// AHEAD == 1: f[0] may hold the last row tile's adapter, which is then not
+// loaded again.
+template <int DT, int KT, int AHEAD>
+__device__ __forceinline__ void add_delta(const GemmModule &m, const RowInfo &ri, const V8Split (&v)[KT], int n0,
+                                          BFrag<DT, KT> (&f)[AHEAD], f32x4_t (&acc)[DT]) {
+  uint64_t todo = __ballot(ri.a >= 0) & 0xffffull;
+  auto next = [&](bool *on) {  // a row of the next adapter
+    *on = todo != 0;
+    const int l = *on ? __builtin_ctzll(todo) : 0;
+    todo &= ~__ballot(ri.a == __builtin_amdgcn_readlane(ri.a, l));
+    return l;
+  };
+  bool on;
+  if constexpr (AHEAD == 1) {
+    while (todo) {
+      const int l = next(&on);
+      if (__builtin_amdgcn_readlane(ri.a, l) != f[0].a) load_b(m, ri, l, true, n0, f[0]);
+      use_b(ri, v, f[0], acc);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int l = next(&on);
+      load_b(m, ri, l, on, n0, f[k]);
+    }
+    for (bool more = true; more;) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (f[k].a < 0) {
+          more = false;
+          break;
+        }
+        use_b(ri, v, f[k], acc);
+        const int l = next(&on);
+        load_b(m, ri, l, on, n0, f[k]);
+      }
+    }
+  }
+}
+
+// KT: 32-wide steps of the ranks of a delta (1: ranks up to 32, 2: up to 64; 0: no delta).
+template <class C, bool GROUPED, int KT>
 __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   typedef typename AccOf<C::I8>::type acc_t;
+  constexpr bool DELTA = KT > 0;
   const int t = threadIdx.x, lane = t & 63, w = wave_id();
   const int r_in = lane & 15, g = lane >> 4;
   const int wk = w / (C::WR * C::WC), wr = (w / C::WC) % C::WR, wc = w % C::WC;
@@ -409,6 +476,32 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     }
   };
 
+  // this thread's row of the tile (loaded while the first stages are on their way)
+  RowInfo mine{};
+  auto load_info = [&]() {
+    if (t >= C::RT) return;
+    const int at = row0 + min(t, rows - 1);
+    mine.b = GROUPED ? (int)min((unsigned)d.perm[at], (unsigned)(d.num_rows - 1)) : at;
+    if constexpr (C::I8) mine.xs = m.xs[GROUPED ? mine.b / m.rows_per_x : mine.b];
+    mine.a = -1;
+    if constexpr (DELTA) {
+      // segments come in ascending slot order: later slots were dropped by the build
+      const int nseg = min(*d.num_segments, d.max_seg);
+      const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
+      const int a = t < rows ? d.ids[mine.b] : -1;
+      if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
+        const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + m.col];
+        if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
+          mine.a = a;
+          mine.rank = e.rank;
+          mine.fmt = e.format;
+          mine.scale = e.scale;
+          mine.B = static_cast<const uint8_t *>(e.B);
+        }
+      }
+    }
+  };
+
   acc_t acc[C::NT][C::MT];
 #pragma unroll
   for (int nt = 0; nt < C::NT; ++nt)
@@ -423,6 +516,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const int s0 = ((0 + g) ^ (r_in & 7)) * 16, s1 = ((4 + g) ^ (r_in & 7)) * 16;
     issue(0, 0);
     issue(1, C::STAGE);
+    load_info();
     stage_barrier<C::XL + C::WL>();
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt) xa[mt] = *(const u32x4 *)(lds + xrow + mt * 16 * C::KB + s0);
@@ -475,6 +569,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     issue(s, put);
     put += C::STAGE;
   }
+  load_info();
   for (int r = 0; r < rounds; ++r) {
     stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
     issue(r + C::S - 1, put);
@@ -498,9 +593,11 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   }
   stage_barrier<0>();  // nothing in flight to LDS any more, and every wave is done with it
 
-  // ---- sums of the k waves
+  // ---- sums of the k waves; the rows' descriptions
   int et0 = 0;  // first column tile this wave finishes
   acc_t fin[C::NTE][C::MT];
+  RowInfo *info = reinterpret_cast<RowInfo *>(lds + C::RED);
+  if (t < C::RT) info[t] = mine;
   if constexpr (C::WK > 1) {
     acc_t *red = reinterpret_cast<acc_t *>(lds);
     const int grp = w % (C::WR * C::WC);
@@ -523,94 +620,69 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         fin[e][mt] = s;
       }
   } else {
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < C::NTE; ++e)
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) fin[e][mt] = acc[e][mt];
   }
 
-  // ---- scales, delta, rounding, store
-  const int nw0 = n0 + (wc * C::NT + et0) * 16;  // first column of this wave's tiles
-  f32x4_t sw[C::NTE];
-  if constexpr (C::I8) {
+  // ---- scales, delta, rounding, store: DT column tiles at a time
 #pragma unroll
-    for (int e = 0; e < C::NTE; ++e) {
-      const int n = nw0 + e * 16 + g * 4;
-      sw[e] = n < m.d_out ? *(const f32x4_t *)(Ws + n) : f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-  }
-  int last_slot = -1;
-  if constexpr (DELTA) {  // segments come in ascending slot order: later slots were dropped by the build
-    const int nseg = min(uniform(*d.num_segments), d.max_seg);
-    last_slot = nseg > 0 ? uniform(d.seg_adapter[nseg - 1]) : -1;
-  }
-#pragma unroll
-  for (int mt = 0; mt < C::MT; ++mt) {
-    const int r = (wr * C::MT + mt) * 16 + r_in;
-    const bool on = r < rows;
-    int b = row0 + min(r, rows - 1);
-    if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1));
-    f32x4_t out[C::NTE];
+  for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
+    const int nw0 = n0 + (wc * C::NT + et0 + e0) * 16;  // first column
+    f32x4_t sw[C::DT];
     if constexpr (C::I8) {
-      const float sx = m.xs[GROUPED ? b / m.rows_per_x : b];
 #pragma unroll
-      for (int e = 0; e < C::NTE; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out[e][i] = (float)fin[e][mt][i] * sx * sw[e][i];
-    } else {
-#pragma unroll
-      for (int e = 0; e < C::NTE; ++e) out[e] = fin[e][mt];
-    }
-    if constexpr (DELTA) {
-      DeltaRows dr;
-      const int a = on ? d.ids[b] : -1;
-      dr.a = -1;
-      dr.rank = dr.fmt = 0;
-      dr.B = nullptr;
-      float scale = 0.f;
-      if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
-        const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + m.col];
-        if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
-          dr.a = a;
-          dr.rank = e.rank;
-          dr.fmt = e.format;
-          dr.B = static_cast<const uint8_t *>(e.B);
-          scale = e.scale;
-        }
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        float vv[8];
-        const int j0 = ks * 32 + g * 8;
-        const float *src = m.v + (int64_t)b * d.rs + j0;
-        const bool von = j0 < dr.rank;
-        const f32x4_t lo = von ? *(const f32x4_t *)src : f32x4_t{0.f, 0.f, 0.f, 0.f};
-        const f32x4_t hi = von ? *(const f32x4_t *)(src + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vv[i] = j0 + i < dr.rank ? lo[i] * scale : 0.f;
-          vv[4 + i] = j0 + 4 + i < dr.rank ? hi[i] * scale : 0.f;
-        }
-        dr.v[ks] = split_v8(vv);
-      }
-      constexpr int DT = C::NTE < 4 ? C::NTE : 4;  // column tiles whose B is held at a time
-#pragma unroll
-      for (int e = 0; e < C::NTE; e += DT) {
-        f32x4_t part[DT];
-#pragma unroll
-        for (int k = 0; k < DT; ++k) part[k] = out[e + k];
-        add_delta<DT>(m, dr, nw0 + e * 16, part);
-#pragma unroll
-        for (int k = 0; k < DT; ++k) out[e + k] = part[k];
-      }
-    }
-    if (on) {
-      uint16_t *y = m.y + (int64_t)b * m.ldy;
-#pragma unroll
-      for (int e = 0; e < C::NTE; ++e) {
+      for (int e = 0; e < C::DT; ++e) {
         const int n = nw0 + e * 16 + g * 4;
-        if (n < m.d_out)
-          *(u32x2 *)(y + n) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
+        sw[e] = n < m.d_out ? *(const f32x4_t *)(Ws + n) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+    BFrag<C::DT, DELTA ? KT : 1> bf[C::AHEAD];
+    (void)bf;
+#pragma unroll
+    for (int mt = 0; mt < C::MT; ++mt) {
+      const int r = (wr * C::MT + mt) * 16 + r_in;
+      const RowInfo ri = info[r];
+      f32x4_t out[C::DT];
+#pragma unroll
+      for (int e = 0; e < C::DT; ++e) {
+        if constexpr (C::I8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[e][i] = (float)fin[e0 + e][mt][i] * ri.xs * sw[e][i];
+        } else {
+          out[e] = fin[e0 + e][mt];
+        }
+      }
+      if constexpr (DELTA) {
+        V8Split v[KT];
+        const float *src = m.v + (int64_t)ri.b * d.rs + g * 8;
+        f32x4_t raw[KT][2];
+#pragma unroll
+        for (int ks = 0; ks < KT; ++ks) {
+          const bool von = ks * 32 + g * 8 < ri.rank;
+          raw[ks][0] = von ? *(const f32x4_t *)(src + ks * 32) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+          raw[ks][1] = von ? *(const f32x4_t *)(src + ks * 32 + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int ks = 0; ks < KT; ++ks) {
+          float vv[8];
+          const int j0 = ks * 32 + g * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) vv[i] = j0 + i < ri.rank ? raw[ks][i / 4][i % 4] * ri.scale : 0.f;
+          v[ks] = split_v8(vv);
+        }
+        add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
+      }
+      if (r < rows) {
+        uint16_t *y = m.y + (int64_t)ri.b * m.ldy;
+#pragma unroll
+        for (int e = 0; e < C::DT; ++e) {
+          const int n = nw0 + e * 16 + g * 4;
+          if (n < m.d_out)
+            *(u32x2 *)(y + n) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
+        }
       }
     }
   }
