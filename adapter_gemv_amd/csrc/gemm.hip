@@ -57,10 +57,10 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantDesc qd) {
 }
 
 //                         I8  RT   NC  WR WC WK  KB  S EU
-template <bool I8> using Cfg16 = GemmCfg<I8, 16, 32, 1, 1, 4, 512, 3, 2>;
+template <bool I8> using Cfg16 = GemmCfg<I8, 16, 64, 1, 1, 4, 512, 2, 2>;
 template <bool I8> using Cfg32 = GemmCfg<I8, 32, 64, 1, 1, 4, 256, 3, 2>;
-template <bool I8> using Cfg64 = GemmCfg<I8, 64, 64, 2, 2, 1, 128, 4, 2>;
-template <bool I8> using Cfg128 = GemmCfg<I8, 128, 128, 2, 2, 1, 128, 4, 1>;
+template <bool I8> using Cfg64 = GemmCfg<I8, 64, 64, 2, 2, 1, 256, 2, 2>;
+template <bool I8> using Cfg128 = GemmCfg<I8, 128, 128, 4, 2, 1, 128, 4, 2>;
 template <bool I8> using Cfg256 = GemmCfg<I8, 256, 256, 2, 2, 1, 128, 2, 1, true>;
 
 template <class C, bool GROUPED, int KT>

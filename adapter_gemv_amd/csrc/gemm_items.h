@@ -96,8 +96,8 @@ __device__ __forceinline__ void stage_barrier() {
 // Segments of at most max_seg, as tiles of RT rows: how many tiles there are,
 // and the segment of one.  Every wave does it for itself, 64 segments a step.
 struct TileOf {
-  int slot, pos0, rows;  // segment's slot, first sorted row of the tile, rows of the tile
-  bool first;            // the segment's first tile
+  int slot, pos0, rows;  // segment's slot, first sorted row and rows
+  int first, tiles;      // its first tile's number, and its tiles
 };
 template <int RT>
 __device__ __forceinline__ int seg_tiles(const GemmDesc &d, int s, int nseg, int *slot, int *o0, int *len) {
@@ -142,12 +142,11 @@ __device__ __forceinline__ bool find_tile(const GemmDesc &d, int nseg, int t, Ti
     if (hit) {
       const int l = __builtin_ctzll(hit);
       const int start = __builtin_amdgcn_readlane(upto - n, l);
-      const int k = t - start;
-      const int length = __builtin_amdgcn_readlane(len, l);
       out->slot = __builtin_amdgcn_readlane(slot, l);
-      out->pos0 = __builtin_amdgcn_readlane(o0, l) + k * RT;
-      out->rows = min(RT, length - k * RT);
-      out->first = k == 0;
+      out->pos0 = __builtin_amdgcn_readlane(o0, l);
+      out->rows = __builtin_amdgcn_readlane(len, l);
+      out->first = start;
+      out->tiles = __builtin_amdgcn_readlane(n, l);
       return true;
     }
     before = __builtin_amdgcn_readlane(upto, 63);
@@ -157,13 +156,14 @@ __device__ __forceinline__ bool find_tile(const GemmDesc &d, int nseg, int t, Ti
 
 // Order of a module's tiles over its blocks: blocks go to the 8 XCDs in turn,
 // so each XCD takes one contiguous eighth of an order that walks kPatchRows
-// row tiles before it moves to the next column tile; the tiles an XCD works on
-// at one time then share rows and columns in its L2.
+// row tiles (of one segment) before it moves to the next column tile; the
+// tiles an XCD works on at one time then share rows and columns in its L2.
 constexpr int kPatchRows = 4;
-__device__ __forceinline__ void tile_order(int local, int row_tiles, int col_tiles, int *rt, int *ct) {
-  const int n = row_tiles * col_tiles;
+__device__ __forceinline__ int xcd_order(int local, int n) {  // the local-th block's place in the order of n tiles
   const int xcd = local & 7, i = local >> 3;
-  const int lin = xcd * (n >> 3) + min(xcd, n & 7) + i;
+  return xcd * (n >> 3) + min(xcd, n & 7) + i;
+}
+__device__ __forceinline__ void patch_order(int lin, int row_tiles, int col_tiles, int *rt, int *ct) {
   const int group = lin / (kPatchRows * col_tiles);
   const int in = lin - group * kPatchRows * col_tiles;
   const int gr = min(kPatchRows, row_tiles - group * kPatchRows);
@@ -221,9 +221,10 @@ __device__ __forceinline__ void mma_drain() {
 // between them can leave too few (seen as wrong first elements of a tile).
 template <int N>
 __device__ __forceinline__ void mma_settle(f32x4_t (&t)[N]) {
-  static_assert(N == 1 || N == 2 || N == 4, "tiles");
+  static_assert(N >= 1 && N <= 4, "tiles");
   if constexpr (N == 1) asm volatile("s_nop 10" : "+v"(t[0]));
   else if constexpr (N == 2) asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]));
+  else if constexpr (N == 3) asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]));
   else asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
 }
 
@@ -383,18 +384,21 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         if ((unsigned)a >= (unsigned)d.num_slots || o0 < 0 || o1 <= o0 || o1 > d.num_rows) atomicAdd(d.status, 1);
       }
     int rt;
+    TileOf tile;
     if constexpr (C::RT >= 128) {
       const int total = total_tiles<C::RT>(d, nseg);
       if (local >= total * m.n_tiles) return;
-      tile_order(local, total, m.n_tiles, &rt, &ct);
+      const int lin = xcd_order(local, total * m.n_tiles);
+      if (!find_tile<C::RT>(d, nseg, lin / m.n_tiles, &tile)) return;
+      patch_order(lin - tile.first * m.n_tiles, tile.tiles, m.n_tiles, &rt, &ct);
     } else {
       rt = local / m.n_tiles;
       ct = local - rt * m.n_tiles;
+      if (!find_tile<C::RT>(d, nseg, rt, &tile)) return;
+      rt -= tile.first;
     }
-    TileOf tile;
-    if (!find_tile<C::RT>(d, nseg, rt, &tile)) return;
-    row0 = tile.pos0;
-    rows = tile.rows;
+    row0 = tile.pos0 + rt * C::RT;
+    rows = min(C::RT, tile.rows - rt * C::RT);
     slot = tile.slot;
     const lora_weight_entry_t raw = d.weights[(int64_t)slot * kMaxModules + m.col];
     W = uniform(static_cast<const uint8_t *>(raw.W));
@@ -408,14 +412,14 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
                     ldw <= (int64_t)0xFFFFFF00 / elt / m.d_out &&
                     (!C::I8 || (Ws != nullptr && ((uintptr_t)Ws & 15) == 0));
     if (!ok) {
-      if (tile.first && ct == 0 && t == 0) atomicAdd(d.status, 1);
+      if (rt == 0 && ct == 0 && t == 0) atomicAdd(d.status, 1);
       return;
     }
     ldw *= elt;
   } else {
     int rt;
     if constexpr (C::RT >= 128) {
-      tile_order(local, d.row_tiles, m.n_tiles, &rt, &ct);
+      patch_order(xcd_order(local, d.row_tiles * m.n_tiles), d.row_tiles, m.n_tiles, &rt, &ct);
     } else {
       rt = local / m.n_tiles;
       ct = local - rt * m.n_tiles;
@@ -563,16 +567,24 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     }
     mma_drain();
   } else {
+  // Blocks start at different places along k (a ring): rows of W are a power of
+  // two apart or near it, and blocks in step would all read the same few
+  // channels of HBM.  Few rows: 32 places within an XCD (x is small and stays
+  // in L2; 5.8 -> 6.3 TB/s of W at 16 rows).  128 rows: one place per XCD, so
+  // that its blocks share each stage of x (221 -> 207 us for the 0.86 GB of a
+  // whole layer).
+  const int r0 = C::RT >= 128 ? (int)(((local & 7) * rounds) >> 3) : (int)((((local >> 3) & 31) * rounds) >> 5);
+  auto stage_of = [&](int r) { return r >= rounds ? rounds : r + r0 >= rounds ? r + r0 - rounds : r + r0; };
   uint32_t put = 0, get = 0;  // ring positions of the next stage to load and to use
 #pragma unroll
   for (int s = 0; s < C::S - 1; ++s) {
-    issue(s, put);
+    issue(stage_of(s), put);
     put += C::STAGE;
   }
   load_info();
   for (int r = 0; r < rounds; ++r) {
     stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
-    issue(r + C::S - 1, put);
+    issue(stage_of(r + C::S - 1), put);
     put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
     const uint8_t *buf = lds + get;
     get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
