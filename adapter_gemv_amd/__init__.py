@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -180,10 +181,36 @@ def _check(code: int, what: str):
         raise LoraError(f"{what}: {status_string(code)}")
 
 
+_raw_stream = None  # torch's lookup of the current stream's handle, without a Stream object around it
+
+
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    global _raw_stream
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # initialises the device
+        get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _raw_stream = ((lambda: get(dev())) if get and dev else (lambda: torch.cuda.current_stream().cuda_stream))
+    return ctypes.c_void_p(_raw_stream())
+
+
+def _rows(t, dtype, rows, dev, name, field):
+    """(address, row stride) of a matrix on device `dev` with unit stride along
+    its rows and at least `rows` of them; the checks of _need, in few steps
+    for the ordinary case (a decode call marshals up to 28 tensors)."""
+    try:
+        n, st = t.size(0), t.stride()
+        if t.dtype is dtype and t.get_device() == dev and n >= rows and len(st) == 2 and (st[1] == 1 or t.size(1) <= 1):
+            # a single row's stride has no meaning: torch may give any
+            return t.data_ptr(), st[0] if n > 1 else -(-t.size(1) // 16) * 16
+    except (AttributeError, IndexError):
+        pass
+    _need(t, dtype, f"{name}.{field}", 2)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}.{field} is on another device than the rest of the call")
+    raise ValueError(f"{name}.{field}: fewer than {rows} rows")
 
 
 def _ptr(t):
@@ -312,6 +339,53 @@ def linear_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, sum_d_i
     return int(lib().lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules))
 
 
+_LIN_I8_PACK = struct.Struct("qqqqqqqii")
+_GROUPED_PACK = struct.Struct("qqqqiiii")
+assert _LIN_I8_PACK.size == ctypes.sizeof(_LinI8IO) and _GROUPED_PACK.size == ctypes.sizeof(_GroupedIO)
+
+
+def _one_device(dev, tensors, what):
+    """The call's device is the current one (its stream runs the kernels) and holds these tensors too."""
+    import torch
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what}: the tensors are on another device than the current one")
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: the tensors are on more than one device")
+
+
+def _linear_i8_array(ios, num_rows, row_adapter, rest):
+    import torch
+    bf16, i8, f32 = torch.bfloat16, torch.int8, torch.float32
+    if row_adapter.size(0) < num_rows:
+        raise ValueError("row_adapter: fewer ids than num_rows")
+    dev = row_adapter.get_device()
+    if dev < 0:
+        raise ValueError("row_adapter must be on the GPU")
+    arr = (_LinI8IO * 7)()
+    mask = 0
+    for i, name in enumerate(MODULES):
+        io = ios.get(name)
+        if io is None:
+            continue
+        if not isinstance(io, LinearI8IO):
+            raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every "
+                            "projection LinearI8IO")
+        Ws, d_out = io.Ws, io.d_out
+        xp, ldx = _rows(io.x, bf16, num_rows, dev, name, "x")
+        yp, ldy = _rows(io.y, bf16, num_rows, dev, name, "y")
+        wp, ldw = _rows(io.Wq, i8, d_out, dev, name, "Wq")
+        if Ws.dtype is not f32 or Ws.get_device() != dev or Ws.stride() != (1,):
+            _need(Ws, f32, f"{name}.Ws", 1)
+            _one_device(dev, (Ws,), name)
+        if Ws.size(0) < d_out:
+            raise ValueError(f"{name}.Ws: fewer scales than d_out")
+        _LIN_I8_PACK.pack_into(arr, i * _LIN_I8_PACK.size, xp, ldx, wp, ldw, Ws.data_ptr(), yp, ldy, io.d_in, d_out)
+        mask |= 1 << i
+    _one_device(dev, rest, "linear_layer")
+    return arr, mask
+
+
 _LINEAR_KINDS = {LinearIO: (_LinIO, ""), LinearQ4IO: (_LinQ4IO, "_q4"), LinearI8IO: (_LinI8IO, "_i8")}
 
 
@@ -323,9 +397,18 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
     lora_linear_layer_i8."""
     import torch
     _need(row_adapter, torch.int32, "row_adapter", 1)
-    kind = next((k for k in _LINEAR_KINDS if any(isinstance(io, k) for io in ios.values())), LinearIO)
-    struct, suffix = _LINEAR_KINDS[kind]
-    arr = (struct * 7)()
+    kind = type(next(iter(ios.values()))) if ios else LinearIO
+    if kind not in _LINEAR_KINDS:
+        kind = next((k for k in _LINEAR_KINDS if any(isinstance(io, k) for io in ios.values())), LinearIO)
+    cstruct, suffix = _LINEAR_KINDS[kind]
+    if kind is LinearI8IO:
+        arr, mask = _linear_i8_array(ios, num_rows, row_adapter, (table, ws, seg.perm))
+        _fn += suffix
+        _check(getattr(lib(), _fn)(arr, mask if module_mask is None else module_mask, num_rows, _ptr(row_adapter),
+                                   _ptr(table), num_slots, seg.c(), max_rank, _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream)), _fn)
+        return
+    arr = (cstruct * 7)()
     mask = 0
     for i, name in enumerate(MODULES):
         io = ios.get(name)
@@ -343,13 +426,6 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
             _need(io.Ws, torch.float32, f"{name}.Ws", 2)
             arr[i] = _LinQ4IO(io.x.data_ptr(), io.x.stride(0), io.Wq.data_ptr(), io.Wq.stride(0), io.Ws.data_ptr(),
                               io.Ws.stride(0), io.y.data_ptr(), io.y.stride(0), io.d_in, io.d_out)
-        elif kind is LinearI8IO:
-            _need(io.Wq, torch.int8, f"{name}.Wq", 2)
-            _need(io.Ws, torch.float32, f"{name}.Ws", 1)
-            if io.Wq.shape[0] < io.d_out or io.Ws.shape[0] < io.d_out:
-                raise ValueError(f"{name}: fewer weight rows or scales than d_out")
-            arr[i] = _LinI8IO(io.x.data_ptr(), io.x.stride(0), io.Wq.data_ptr(), io.Wq.stride(0), io.Ws.data_ptr(),
-                              io.y.data_ptr(), io.y.stride(0), io.d_in, io.d_out)
         else:
             arr[i] = _LinIO(io.x.data_ptr(), io.x.stride(0), io.W.data_ptr(), io.W.stride(0), io.y.data_ptr(),
                             io.y.stride(0), io.d_in, io.d_out)
@@ -420,23 +496,26 @@ def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, 
     weights are int8 with output scales, rows of x are quantised in the call
     and ``ws`` is needed.  See lora_grouped_layer and lora_grouped_layer_i8."""
     import torch
+    bf16 = torch.bfloat16
     arr = (_GroupedIO * 7)()
     mask = 0
+    dev = weights.get_device()
+    if dev < 0:
+        raise ValueError("weights must be on the GPU")
     for i, name in enumerate(MODULES):
         io = ios.get(name)
         if io is None:
             continue
-        _need(io.x, torch.bfloat16, f"{name}.x", 2)
-        _need(io.y, torch.bfloat16, f"{name}.y", 2)
-        if io.rows_per_x < 1:
+        fan = io.rows_per_x
+        if fan < 1:
             raise ValueError(f"{name}: rows_per_x must be >= 1")
-        if io.x.shape[0] < -(-num_rows // io.rows_per_x) or io.y.shape[0] < num_rows:
-            raise ValueError(f"{name}: fewer rows than num_rows")
-        arr[i] = _GroupedIO(io.x.data_ptr(), io.x.stride(0), io.y.data_ptr(), io.y.stride(0), io.d_in, io.d_out,
-                            io.rows_per_x, 0)
+        xp, ldx = _rows(io.x, bf16, -(-num_rows // fan), dev, name, "x")
+        yp, ldy = _rows(io.y, bf16, num_rows, dev, name, "y")
+        _GROUPED_PACK.pack_into(arr, i * _GROUPED_PACK.size, xp, ldx, yp, ldy, io.d_in, io.d_out, fan, 0)
         mask |= 1 << i
     if module_mask is not None:
         mask = module_mask
+    _one_device(dev, (seg.perm,) if ws is None else (seg.perm, ws), "grouped_layer")
     if int8:
         _check(lib().lora_grouped_layer_i8(arr, mask, num_rows, _ptr(weights), num_slots, seg.c(), _ptr(ws),
                                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),

@@ -642,12 +642,11 @@ lora_status_t check_linear(const lora_linear_i8_io_t &m, LinearArgs *a) {
 // projections that share it (same pointer, ldx and d_in) share its rows.
 struct QuantInputs {
   QuantDesc d{};
-  int n = 0;
   size_t used = 0;
   int add(const void *x, int64_t ldx, int d_in, int64_t rows, void *ws) {
-    for (int i = 0; i < n; ++i)
+    for (int i = 0; i < d.n; ++i)
       if (d.in[i].x == x && d.in[i].ldx == ldx && d.in[i].d_in == d_in && d.in[i].rows == rows) return i;
-    auto &in = d.in[n];
+    QuantInput &in = d.in[d.n];
     in.x = static_cast<const uint16_t *>(x);
     in.ldx = ldx;
     in.d_in = d_in;
@@ -660,21 +659,40 @@ struct QuantInputs {
     };
     in.q = static_cast<int8_t *>(take((size_t)rows * in.pitch));
     in.s = static_cast<float *>(take((size_t)rows * 4));
-    return n++;
+    in.block_base = d.blocks;
+    d.blocks += (int)rows;  // at most 7 times the rows of a matrix of 16-byte rows below 4 GiB
+    return d.n++;
   }
 };
 
-// The tile configuration of a product (index into gemm_tile): the smallest
-// row tile that holds the rows a block can expect, and the largest tile only
-// where it still gives every compute unit a block.
+// The tile configuration of a product (index into gemm_tile), by the rows
+// that a group (the whole batch, or a slot's segment on average) has:
+//  * up to 16, 32 and 64: the smallest row tile that holds them (the weights
+//    are read once, whatever the tile; columns and k are cut fine enough to
+//    fill the device);
+//  * more than 128 and at least 256 tiles of 256 x 256 (one per compute unit):
+//    the largest tile, which the matrix cores bound (8192 rows x 8192 x 8192
+//    bf16: 1.3 PFLOP/s against 0.9 with 128 x 128);
+//  * else 128 rows: by 128 columns, one block per compute unit, or by 96, two
+//    blocks per unit, whichever leaves less of the last round of blocks idle
+//    (256 rows on 18432 outputs: 288 blocks for 256 places against 384 for
+//    512, 127 and 103 us; 128 rows on 84000 outputs, 656 against 875: 452 and
+//    486 us).
+constexpr int kComputeUnits = 256;
 int pick_gemm(int64_t rows, int64_t groups, const int *d_out, int n) {
   const int64_t per = (rows + groups - 1) / groups;
-  for (int cfg = 0; cfg < kGemmTiles - 2; ++cfg)
+  for (int cfg = 0; cfg < 3; ++cfg)
     if (per <= gemm_tile(cfg).rows) return cfg;
-  const GemmTile t = gemm_tile(kGemmTiles - 1);
-  int64_t blocks = 0;
-  for (int i = 0; i < n; ++i) blocks += (rows / t.rows) * ((d_out[i] + t.cols - 1) / t.cols);
-  return blocks >= 256 ? kGemmTiles - 1 : kGemmTiles - 2;
+  auto blocks = [&](int cfg) {
+    const GemmTile t = gemm_tile(cfg);
+    int64_t b = 0;
+    for (int i = 0; i < n; ++i) b += groups * ((per + t.rows - 1) / t.rows) * ((d_out[i] + t.cols - 1) / t.cols);
+    return b;
+  };
+  if (per > 128 && blocks(5) >= kComputeUnits) return 5;
+  const int64_t wide = (blocks(4) + kComputeUnits - 1) / kComputeUnits * gemm_tile(4).cols;
+  const int64_t narrow = (blocks(3) + 2 * kComputeUnits - 1) / (2 * kComputeUnits) * 2 * gemm_tile(3).cols;
+  return narrow < wide ? 3 : 4;
 }
 
 // Number the blocks of n projections (g.mod[0..n), longest d_in first: a
@@ -752,10 +770,6 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
   if constexpr (kI8) {  // the int8 rows of x, behind the v planes
     void *qws = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
     for (int i = 0; i < n; ++i) quant_of[i] = quant.add(la[i].x, la[i].ldx, la[i].d_in, num_rows, qws);
-    if (do_shrink) {
-      st = launched(launch_quantize(quant.d, quant.n, s));
-      if (st != LORA_OK) return st;
-    }
   }
   if (do_shrink) {
     // 1. v partials of every projection (segment-grouped: each adapter's A once)
@@ -766,7 +780,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
     fill_desc(d, ms, n, true, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws);
     d.v_out = vplanes;
     d.ldv = rs;
-    st = launched(launch_shrink_reduce(d, s));
+    st = launched(kI8 ? launch_quantize_reduce(d, quant.d, s) : launch_shrink_reduce(d, s));
     if (st != LORA_OK) return st;
   }
   if (!do_fused) return LORA_OK;
@@ -955,7 +969,7 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
   if (num_rows == 0) return LORA_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (i8) {
-    st = launched(launch_quantize(quant.d, quant.n, s));
+    st = launched(launch_quantize(quant.d, s));
     if (st != LORA_OK) return st;
   }
   g.weights = weights;

@@ -2,6 +2,7 @@
 // (gemm_items.h): one kernel per kind and tile configuration, and the row
 // quantiser.
 #include "gemm_items.h"
+#include "shrink_reduce.h"
 
 namespace lora {
 namespace {
@@ -13,46 +14,20 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::E
 }
 
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantDesc qd) {
-  __shared__ float red[4];
-  __shared__ int badv[4];
-  const auto &in = (*(const QuantDesc *)(const void *)__builtin_amdgcn_kernarg_segment_ptr()).in[blockIdx.y];
-  const int row = blockIdx.x, t = threadIdx.x;
-  if (row >= in.rows) return;  // the grid covers the input with the most rows
-  const uint16_t *x = in.x + (int64_t)row * in.ldx;
-  const int n8 = in.d_in / 8;  // pieces of 8 values
-  u32x4 keep[kQuantRegs];
-  float mx = 0.f;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kQuantRegs; ++i) {
-    const int p = i * 256 + t;
-    keep[i] = p < n8 ? *(const u32x4 *)(x + (int64_t)p * 8) : zero4();
-  }
-#pragma unroll
-  for (int i = 0; i < kQuantRegs; ++i) mx = abs_max8(keep[i], mx, &bad);
-  for (int p = kQuantRegs * 256 + t; p < n8; p += 256) mx = abs_max8(*(const u32x4 *)(x + (int64_t)p * 8), mx, &bad);
-#pragma unroll
-  for (int k = 32; k >= 1; k /= 2) mx = fmaxf(mx, __shfl_xor(mx, k, 64));
-  const bool wbad = __ballot(bad) != 0;
-  if ((t & 63) == 0) {
-    red[t >> 6] = mx;
-    badv[t >> 6] = wbad;
-  }
-  __syncthreads();
-  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const bool nan = badv[0] | badv[1] | badv[2] | badv[3];
-  const bool live = mx > 0.f && !nan;
-  int8_t *q = in.q + (int64_t)row * in.pitch;
-#pragma unroll
-  for (int i = 0; i < kQuantRegs; ++i) {
-    const int p = i * 256 + t;
-    if (p < n8) *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(keep[i], mx) : u32x2{0u, 0u};
-  }
-  for (int p = kQuantRegs * 256 + t; p < n8; p += 256)
-    *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(*(const u32x4 *)(x + (int64_t)p * 8), mx) : u32x2{0u, 0u};
-  if (t == 0) {
-    if (in.d_in < in.pitch) *(u32x2 *)(q + in.d_in) = u32x2{0u, 0u};  // the row's last half piece
-    in.s[row] = nan ? __int_as_float(0x7fc00000) : mx / 127.f;
+  quantize_block(qd, *(const QuantDesc *)(const void *)__builtin_amdgcn_kernarg_segment_ptr(), blockIdx.x);
+}
+
+// Between the grouped shrink and the product of an int8 layer call: the rows'
+// quantiser, which needs nothing of the shrink, and the sum of the shrink's
+// partials, in one launch instead of two (4 us of a small call's 25).
+__global__ __launch_bounds__(256) void quantize_reduce_kernel(LayerDesc d, QuantDesc qd, int reduce_blocks) {
+  constexpr int kAt = (sizeof(LayerDesc) + 7) / 8 * 8;  // where the second argument lies
+  const int b = blockIdx.x;
+  if (b < qd.blocks) {
+    quantize_block(qd, *(const QuantDesc *)((const char *)(const void *)__builtin_amdgcn_kernarg_segment_ptr() + kAt), b);
+  } else {
+    const int module = (b - qd.blocks) / reduce_blocks;
+    shrink_reduce(d, b - qd.blocks - module * reduce_blocks, module);
   }
 }
 
@@ -60,6 +35,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantDesc qd) {
 template <bool I8> using Cfg16 = GemmCfg<I8, 16, 64, 1, 1, 4, 512, 2, 2>;
 template <bool I8> using Cfg32 = GemmCfg<I8, 32, 64, 1, 1, 4, 256, 3, 2>;
 template <bool I8> using Cfg64 = GemmCfg<I8, 64, 64, 2, 2, 1, 256, 2, 2>;
+template <bool I8> using Cfg128n = GemmCfg<I8, 128, 96, 2, 2, 1, 128, 2, 2>;
 template <bool I8> using Cfg128 = GemmCfg<I8, 128, 128, 4, 2, 1, 128, 4, 2>;
 template <bool I8> using Cfg256 = GemmCfg<I8, 256, 256, 2, 2, 1, 128, 2, 1, true>;
 
@@ -73,7 +49,8 @@ void pick(const GemmDesc &d, int cfg, int blocks, hipStream_t s) {
     case 0: launch<Cfg16<I8>, GROUPED, KT>(d, blocks, s); break;
     case 1: launch<Cfg32<I8>, GROUPED, KT>(d, blocks, s); break;
     case 2: launch<Cfg64<I8>, GROUPED, KT>(d, blocks, s); break;
-    case 3: launch<Cfg128<I8>, GROUPED, KT>(d, blocks, s); break;
+    case 3: launch<Cfg128n<I8>, GROUPED, KT>(d, blocks, s); break;
+    case 4: launch<Cfg128<I8>, GROUPED, KT>(d, blocks, s); break;
     default: launch<Cfg256<I8>, GROUPED, KT>(d, blocks, s); break;
   }
 }
@@ -85,7 +62,8 @@ GemmTile gemm_tile(int cfg) {
     case 0: return {Cfg16<true>::RT, Cfg16<true>::NC};
     case 1: return {Cfg32<true>::RT, Cfg32<true>::NC};
     case 2: return {Cfg64<true>::RT, Cfg64<true>::NC};
-    case 3: return {Cfg128<true>::RT, Cfg128<true>::NC};
+    case 3: return {Cfg128n<true>::RT, Cfg128n<true>::NC};
+    case 4: return {Cfg128<true>::RT, Cfg128<true>::NC};
     default: return {Cfg256<true>::RT, Cfg256<true>::NC};
   }
 }
@@ -103,11 +81,18 @@ hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hi
   return hipGetLastError();
 }
 
-hipError_t launch_quantize(const QuantDesc &d, int n_inputs, hipStream_t stream) {
-  int rows = 0;
-  for (int i = 0; i < n_inputs; ++i) rows = d.in[i].rows > rows ? d.in[i].rows : rows;
-  if (rows <= 0) return hipSuccess;
-  quantize_rows_kernel<<<dim3((unsigned)rows, (unsigned)n_inputs), 256, 0, stream>>>(d);
+hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream) {
+  if (d.blocks <= 0) return hipSuccess;
+  quantize_rows_kernel<<<d.blocks, 256, 0, stream>>>(d);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_reduce(const LayerDesc &d, const QuantDesc &q, hipStream_t stream) {
+  const int64_t reduce = ((int64_t)d.num_rows * d.max_rank + 255) / 256;
+  const int64_t blocks = q.blocks + reduce * d.n_active;
+  if (blocks <= 0) return hipSuccess;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  quantize_reduce_kernel<<<(unsigned)blocks, 256, 0, stream>>>(d, q, (int)reduce);
   return hipGetLastError();
 }
 

@@ -734,4 +734,52 @@ __device__ __forceinline__ u32x2 quant8(u32x4 p, float amax) {
   return u32x2{o[0], o[1]};
 }
 
+// One row of a call's inputs; q0 is qd where it lies in the kernel's arguments.
+__device__ __forceinline__ void quantize_block(const QuantDesc &qd, const QuantDesc &q0, int block) {
+  __shared__ float red[4];
+  __shared__ int badv[4];
+  int k = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxModules; ++i)
+    if (i < qd.n && block >= qd.in[i].block_base) k = i;
+  const QuantInput in = q0.in[k];
+  const int row = block - in.block_base, t = threadIdx.x;
+  const uint16_t *x = in.x + (int64_t)row * in.ldx;
+  const int n8 = in.d_in / 8;  // pieces of 8 values
+  u32x4 keep[kQuantRegs];
+  float mx = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kQuantRegs; ++i) {
+    const int p = i * 256 + t;
+    keep[i] = p < n8 ? *(const u32x4 *)(x + (int64_t)p * 8) : zero4();
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantRegs; ++i) mx = abs_max8(keep[i], mx, &bad);
+  for (int p = kQuantRegs * 256 + t; p < n8; p += 256) mx = abs_max8(*(const u32x4 *)(x + (int64_t)p * 8), mx, &bad);
+#pragma unroll
+  for (int i = 32; i >= 1; i /= 2) mx = fmaxf(mx, __shfl_xor(mx, i, 64));
+  const bool wbad = __ballot(bad) != 0;
+  if ((t & 63) == 0) {
+    red[t >> 6] = mx;
+    badv[t >> 6] = wbad;
+  }
+  __syncthreads();
+  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const bool nan = badv[0] | badv[1] | badv[2] | badv[3];
+  const bool live = mx > 0.f && !nan;
+  int8_t *q = in.q + (int64_t)row * in.pitch;
+#pragma unroll
+  for (int i = 0; i < kQuantRegs; ++i) {
+    const int p = i * 256 + t;
+    if (p < n8) *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(keep[i], mx) : u32x2{0u, 0u};
+  }
+  for (int p = kQuantRegs * 256 + t; p < n8; p += 256)
+    *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(*(const u32x4 *)(x + (int64_t)p * 8), mx) : u32x2{0u, 0u};
+  if (t == 0) {
+    if (in.d_in < in.pitch) *(u32x2 *)(q + in.d_in) = u32x2{0u, 0u};  // the row's last half piece
+    in.s[row] = nan ? __int_as_float(0x7fc00000) : mx / 127.f;
+  }
+}
+
 }  // namespace lora

@@ -8,6 +8,7 @@
 #include "fused_items.h"
 #include "onepass_items.h"
 #include "sgmv_items.h"
+#include "shrink_reduce.h"
 
 namespace lora {
 namespace {
@@ -71,36 +72,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(CLS <= 1 ? 
   else if (b < sg + decode_blocks) decode_expand_block<LPR>(d, b - sg, nseg, lds);
 }
 
-// Sum the k-chunk partials of each row in a segment into v[b][0..max_rank)
-// (zero past the entry's rank), for module blockIdx.y into the plane
-// v_out + blockIdx.y * num_rows * ldv (lora_shrink: one module, the caller's
-// v; the fused layer: every module, planes in the workspace).
-__global__ __launch_bounds__(256) void shrink_reduce_kernel(LayerDesc d) {
-  const int nseg = min(*d.num_segments, d.max_seg);
-  if (nseg <= 0) return;
-  const int nvalid = min(d.seg_offsets[nseg], d.num_rows);
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int p = (int)(idx / d.max_rank);
-  const int j = (int)(idx - (int64_t)p * d.max_rank);
-  if (p >= nvalid) return;
-  int lo = 0, hi = nseg - 1;  // segment s with seg_offsets[s] <= p < seg_offsets[s+1]
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (d.seg_offsets[mid] <= p) lo = mid;
-    else hi = mid - 1;
-  }
-  const ModuleDesc m = kernel_desc().mod[blockIdx.y];
-  float *v_out = d.v_out + (int64_t)blockIdx.y * d.num_rows * d.ldv;
-  const int a = d.seg_adapter[lo];
-  if ((unsigned)a >= (unsigned)d.num_slots) return;
-  const lora_adapter_entry_t e = d.table[(int64_t)a * d.table_cols + m.col];  // varies per lane
-  const bool ok = entry_ok(e, d.max_rank);
-  float sum = 0.f;
-  if (ok && j < e.rank)
-    for (int c = 0; c < m.n_chunks; ++c) sum += d.part[((int64_t)(m.part_base + c) * d.num_rows + p) * d.rs + j];
-  const int b = d.perm[p];
-  if ((unsigned)b < (unsigned)d.num_rows) v_out[(int64_t)b * d.ldv + j] = sum;
-}
+// lora_shrink: one module, the caller's v; the fused layer: every module,
+// planes in the workspace.
+__global__ __launch_bounds__(256) void shrink_reduce_kernel(LayerDesc d) { shrink_reduce(d, blockIdx.x, blockIdx.y); }
 
 // Sum the k-chunk partials of every row in a segment into its first chunk,
 // for module blockIdx.y.  A prefill call runs this between its shrink and

@@ -216,16 +216,20 @@ struct GemmDesc {
 };
 
 // Rows of up to kMaxModules distinct inputs to quantise.
+struct QuantInput {
+  const uint16_t *x;
+  int64_t ldx;       // elements
+  int8_t *q;
+  float *s;
+  int32_t d_in;
+  int32_t pitch;     // bytes of a row of q, a multiple of 16
+  int32_t rows;
+  int32_t block_base;  // first block of this input (one per row)
+};
 struct QuantDesc {
-  struct {
-    const uint16_t *x;
-    int64_t ldx;       // elements
-    int8_t *q;
-    float *s;
-    int32_t d_in;
-    int32_t pitch;     // bytes of a row of q, a multiple of 16
-    int32_t rows;
-  } in[kMaxModules];
+  QuantInput in[kMaxModules];
+  int32_t n;
+  int32_t blocks;
 };
 
 enum GemmKind { kLinearI8 = 0, kGroupedBf16 = 1, kGroupedI8 = 2 };
@@ -233,10 +237,12 @@ enum GemmKind { kLinearI8 = 0, kGroupedBf16 = 1, kGroupedI8 = 2 };
 struct GemmTile {
   int rows, cols;
 };
-constexpr int kGemmTiles = 5;
+constexpr int kGemmTiles = 6;
 GemmTile gemm_tile(int cfg);
 hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
-hipError_t launch_quantize(const QuantDesc &d, int n_inputs, hipStream_t stream);
+hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream);
+// The same, and launch_shrink_reduce of d, in one launch.
+hipError_t launch_quantize_reduce(const LayerDesc &d, const QuantDesc &q, hipStream_t stream);
 
 inline int round_up(int a, int b) { return (a + b - 1) / b * b; }
 inline int partial_row_stride(int max_rank) { return round_up(max_rank, 8); }
