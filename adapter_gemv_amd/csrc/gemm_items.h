@@ -54,7 +54,8 @@ struct GemmCfg {
   static constexpr int XBYTES = RT * KB, STAGE = (RT + NC) * KB;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
   static constexpr int TAIL = RED + 32 * RT;           // and the rows' descriptions, when the ring is done
-  static constexpr int LDS = S * STAGE > TAIL ? S * STAGE : TAIL;
+  static constexpr int RING = PIPE ? 5 * XBYTES : S * STAGE;  // pipelined: five places of one operand's stage
+  static constexpr int LDS = RING > TAIL ? RING : TAIL;
   static constexpr int DT = NTE < 4 ? NTE : 4;         // column tiles finished at a time
   // Adapters whose B is in flight or in use (delta): rows of one decode tile
   // all differ, and a wave waits for each adapter in turn; the rows of a
@@ -158,17 +159,21 @@ __device__ __forceinline__ bool find_tile(const GemmDesc &d, int nseg, int t, Ti
 // so each XCD takes one contiguous eighth of an order that walks kPatchRows
 // row tiles (of one segment) before it moves to the next column tile; the
 // tiles an XCD works on at one time then share rows and columns in its L2.
-constexpr int kPatchRows = 4;
+// A segment of up to 8 row tiles is one patch (32 segments of 128 to 2048 rows
+// on 8192 x 8192: bf16 4.26 -> 4.15 ms, int8 4.81 -> 4.65; in longer segments
+// 8 rows measured up to 10% slower than 4).
+constexpr int kPatchRows = 4, kPatchMost = 8;
 __device__ __forceinline__ int xcd_order(int local, int n) {  // the local-th block's place in the order of n tiles
   const int xcd = local & 7, i = local >> 3;
   return xcd * (n >> 3) + min(xcd, n & 7) + i;
 }
 __device__ __forceinline__ void patch_order(int lin, int row_tiles, int col_tiles, int *rt, int *ct) {
-  const int group = lin / (kPatchRows * col_tiles);
-  const int in = lin - group * kPatchRows * col_tiles;
-  const int gr = min(kPatchRows, row_tiles - group * kPatchRows);
+  const int patch = row_tiles <= kPatchMost ? row_tiles : kPatchRows;
+  const int group = lin / (patch * col_tiles);
+  const int in = lin - group * patch * col_tiles;
+  const int gr = min(patch, row_tiles - group * patch);
   *ct = in / gr;
-  *rt = group * kPatchRows + in - *ct * gr;
+  *rt = group * patch + in - *ct * gr;
 }
 
 template <bool I8>
@@ -457,27 +462,41 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
   const int rounds = (m.kbytes + C::KB - 1) / C::KB;
   const int full = m.kbytes / C::KB;
-  auto issue = [&](int r, uint32_t buf) {
+  // the loads of one operand of stage r to LDS at `at`; a last, partial stage
+  // and those past the end get zeros beyond the row
+  auto issue_x = [&](int r, uint32_t at) {
     const uint32_t soff = (uint32_t)(r * C::KB);
-    const uint32_t at = lds_base + buf + (uint32_t)w * 1024;
+    const int left = m.kbytes - r * C::KB;
+    at += lds_base + (uint32_t)w * 1024;
     if (r < full) {
 #pragma unroll
       for (int i = 0; i < C::XL; ++i) dma16(rx, xoff[i], soff, at + i * C::NW * 1024);
-#pragma unroll
-      for (int i = 0; i < C::WL; ++i) dma16(rw, woff[i], soff, at + C::XBYTES + i * C::NW * 1024);
-    } else {  // the last, partial stage and those past the end: zeros beyond the row
-      const int left = m.kbytes - r * C::KB;
+    } else {
 #pragma unroll
       for (int i = 0; i < C::XL; ++i) {
         const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & 7);
         dma16(rx, piece * 16 < left ? xoff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
       }
+    }
+  };
+  auto issue_w = [&](int r, uint32_t at) {
+    const uint32_t soff = (uint32_t)(r * C::KB);
+    const int left = m.kbytes - r * C::KB;
+    at += lds_base + (uint32_t)w * 1024;
+    if (r < full) {
+#pragma unroll
+      for (int i = 0; i < C::WL; ++i) dma16(rw, woff[i], soff, at + i * C::NW * 1024);
+    } else {
 #pragma unroll
       for (int i = 0; i < C::WL; ++i) {
         const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & 7);
-        dma16(rw, piece * 16 < left ? woff[i] + soff : kOutOfRange, 0, at + C::XBYTES + i * C::NW * 1024);
+        dma16(rw, piece * 16 < left ? woff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
       }
     }
+  };
+  auto issue = [&](int r, uint32_t buf) {
+    issue_x(r, buf);
+    issue_w(r, buf + C::XBYTES);
   };
 
   // this thread's row of the tile (loaded while the first stages are on their way)
@@ -515,56 +534,64 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   constexpr int KS = C::KB / 64 / C::WK;  // matrix-core steps of a wave per stage
   const int xrow = (wr * C::MT * 16 + r_in) * C::KB, wrow = C::XBYTES + (wc * C::NT * 16 + r_in) * C::KB;
   if constexpr (C::PIPE) {
-    static_assert(!C::PIPE || (C::S == 2 && C::WK == 1 && KS == 2), "the pipelined loop");
+    // The ring has five places of one operand's stage.  In round r: w(r) and
+    // x(r) in A and B (the first step's operands already in registers), w(r+1)
+    // and x(r+1) in C and D; w(r+2) is sent to E during the first step.  Past
+    // the barrier between the steps every wave holds the rest of stage r in
+    // registers, so x(r+2) goes to A during the second.  W, which comes from
+    // HBM, has a round and a half to arrive, x, mostly in L2, one.  Reads, loads
+    // and products are laid out by hand, one of each in turn, and kept so.
+    static_assert(!C::PIPE || (C::WK == 1 && KS == 2 && C::RT == C::NC && C::MT == C::NT), "the pipelined loop");
+    constexpr int PL = C::XBYTES;                      // bytes of a place
+    constexpr int SLOTS = C::MT + C::NT, PER = C::MT * C::NT / SLOTS;  // operand reads of a step, products per read
+    static_assert(!C::PIPE || (C::XL * 2 == SLOTS && C::WL * 2 == SLOTS), "a load every second operand read");
     u32x4 xa[C::MT], wa[C::NT], xb[C::MT], wb[C::NT];
     const int s0 = ((0 + g) ^ (r_in & 7)) * 16, s1 = ((4 + g) ^ (r_in & 7)) * 16;
-    issue(0, 0);
-    issue(1, C::STAGE);
+    const int wrow0 = wrow - C::XBYTES;
+    uint32_t A = 0, B = PL, Cc = 2 * PL, D = 3 * PL, E = 4 * PL;
+    issue_w(0, A);
+    issue_x(0, B);
+    issue_w(1, Cc);
+    issue_x(1, D);
     load_info();
     stage_barrier<C::XL + C::WL>();
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt) xa[mt] = *(const u32x4 *)(lds + xrow + mt * 16 * C::KB + s0);
+    for (int mt = 0; mt < C::MT; ++mt) xa[mt] = *(const u32x4 *)(lds + B + xrow + mt * 16 * C::KB + s0);
 #pragma unroll
-    for (int nt = 0; nt < C::NT; ++nt) wa[nt] = *(const u32x4 *)(lds + wrow + nt * 16 * C::KB + s0);
-    auto round = [&](int r, uint32_t cur, bool fast) {
-      const uint8_t *buf = lds + cur, *nbuf = lds + (C::STAGE - cur);
-      constexpr int PER = C::MT * C::NT / (C::MT + C::NT);  // products per operand read
-      // step 0: its operands are in xa, wa; those of step 1 are read meanwhile
+    for (int nt = 0; nt < C::NT; ++nt) wa[nt] = *(const u32x4 *)(lds + A + wrow0 + nt * 16 * C::KB + s0);
+    auto round = [&](int r, bool fast) {
+      const uint32_t soff = (uint32_t)((r + 2) * C::KB);
+      if (!fast) issue_w(r + 2, E);
 #pragma unroll
-      for (int i = 0; i < C::MT + C::NT; ++i) {
-        if (i < C::MT) xb[i] = *(const u32x4 *)(buf + xrow + i * 16 * C::KB + s1);
-        else wb[i - C::MT] = *(const u32x4 *)(buf + wrow + (i - C::MT) * 16 * C::KB + s1);
+      for (int i = 0; i < SLOTS; ++i) {
+        if (i < C::MT) xb[i] = *(const u32x4 *)(lds + B + xrow + i * 16 * C::KB + s1);
+        else wb[i - C::MT] = *(const u32x4 *)(lds + A + wrow0 + (i - C::MT) * 16 * C::KB + s1);
+        if (fast && (i & 1) == 0) dma16(rw, woff[i / 2], soff, lds_base + E + (uint32_t)w * 1024 + i / 2 * C::NW * 1024);
 #pragma unroll
         for (int k = i * PER; k < (i + 1) * PER; ++k) mma_acc(wa[k / C::MT], xa[k % C::MT], acc[k / C::MT][k % C::MT]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      stage_barrier<0>();  // stage r + 1 is there, and every wave holds the rest of stage r
-      const uint32_t soff = (uint32_t)((r + 2) * C::KB);
-      const uint32_t at = lds_base + cur + (uint32_t)w * 1024;
-      if (!fast) issue(r + 2, cur);
+      stage_barrier<C::WL>();  // stage r + 1 is there, w(r + 2) may still be on its way
+      if (!fast) issue_x(r + 2, A);
 #pragma unroll
-      for (int i = 0; i < C::MT + C::NT; ++i) {
-        if (i < C::MT) xa[i] = *(const u32x4 *)(nbuf + xrow + i * 16 * C::KB + s0);
-        else wa[i - C::MT] = *(const u32x4 *)(nbuf + wrow + (i - C::MT) * 16 * C::KB + s0);
-        if (fast) {
-          if (i < C::XL) dma16(rx, xoff[i], soff, at + i * C::NW * 1024);
-          else if (i < C::XL + C::WL) dma16(rw, woff[i - C::XL], soff, at + C::XBYTES + (i - C::XL) * C::NW * 1024);
-        }
+      for (int i = 0; i < SLOTS; ++i) {
+        if (i < C::MT) xa[i] = *(const u32x4 *)(lds + D + xrow + i * 16 * C::KB + s0);
+        else wa[i - C::MT] = *(const u32x4 *)(lds + Cc + wrow0 + (i - C::MT) * 16 * C::KB + s0);
+        if (fast && (i & 1) == 0) dma16(rx, xoff[i / 2], soff, lds_base + A + (uint32_t)w * 1024 + i / 2 * C::NW * 1024);
 #pragma unroll
         for (int k = i * PER; k < (i + 1) * PER; ++k) mma_acc(wb[k / C::MT], xb[k % C::MT], acc[k / C::MT][k % C::MT]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      const uint32_t a = A, b = B;
+      A = Cc;
+      B = D;
+      Cc = E;
+      D = a;
+      E = b;
     };
     int r = 0;
-    uint32_t cur = 0;
-    for (; r + 2 < full; ++r) {
-      round(r, cur, true);
-      cur = C::STAGE - cur;
-    }
-    for (; r < rounds; ++r) {
-      round(r, cur, false);
-      cur = C::STAGE - cur;
-    }
+    for (; r + 2 < full; ++r) round(r, true);
+    for (; r < rounds; ++r) round(r, false);
     mma_drain();
   } else {
   // Blocks start at different places along k (a ring): rows of W are a power of
