@@ -53,7 +53,13 @@ struct GemmCfg {
   static constexpr int XL = RT * KB / 1024 / NW, WL = NC * KB / 1024 / NW;  // loads per wave and stage
   static constexpr int XBYTES = RT * KB, STAGE = (RT + NC) * KB;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
-  static constexpr int TAIL = RED + 32 * RT;           // and the rows' descriptions, when the ring is done
+  // A wave of at least 64 finished columns turns its outputs round in LDS and
+  // stores whole lines; 8-byte pieces of 16 rows at a time cost a 256 x 256
+  // tile 9 us (8% of an int8 tile of 8192 inputs).
+  static constexpr bool TURN = NTE >= 4;
+  static constexpr int YROW = NTE * 32 + 16;           // bytes of an output row in LDS
+  static constexpr int YWAVE = TURN ? MT * 16 * YROW : 0;
+  static constexpr int TAIL = RED + 32 * RT + NW * YWAVE;  // and the rows' descriptions, when the ring is done
   static constexpr int RING = PIPE ? 5 * XBYTES : S * STAGE;  // pipelined: five places of one operand's stage
   static constexpr int LDS = RING > TAIL ? RING : TAIL;
   static constexpr int DT = NTE < 4 ? NTE : 4;         // column tiles finished at a time
@@ -667,6 +673,8 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   }
 
   // ---- scales, delta, rounding, store: DT column tiles at a time
+  uint8_t *yw = lds + C::RED + 32 * C::RT + w * C::YWAVE;
+  (void)yw;
 #pragma unroll
   for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
     const int nw0 = n0 + (wc * C::NT + et0 + e0) * 16;  // first column
@@ -714,7 +722,12 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         }
         add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
       }
-      if (r < rows) {
+      if constexpr (C::TURN) {
+        uint8_t *at = yw + (mt * 16 + r_in) * C::YROW + e0 * 32 + g * 8;
+#pragma unroll
+        for (int e = 0; e < C::DT; ++e)
+          *(u32x2 *)(at + e * 32) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
+      } else if (r < rows) {
         uint16_t *y = m.y + (int64_t)ri.b * m.ldy;
 #pragma unroll
         for (int e = 0; e < C::DT; ++e) {
@@ -723,6 +736,17 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
             *(u32x2 *)(y + n) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
         }
       }
+    }
+  }
+  if constexpr (C::TURN) {  // the wave's own rows of LDS: no barrier
+    constexpr int PPR = C::NTE * 2, STEPS = C::MT * 16 * PPR / 64;  // 16-byte pieces of a row; stores
+    const int nw0 = n0 + (wc * C::NT + et0) * 16;
+#pragma unroll 4
+    for (int i = 0; i < STEPS; ++i) {
+      const int at = i * 64 + lane, lr = at / PPR, piece = at % PPR;
+      const int r = wr * C::MT * 16 + lr, n = nw0 + piece * 8;
+      const u32x4 v = *(const u32x4 *)(yw + lr * C::YROW + piece * 16);
+      if (r < rows && n < m.d_out) *(u32x4 *)(m.y + (int64_t)info[r].b * m.ldy + n) = v;
     }
   }
 }
