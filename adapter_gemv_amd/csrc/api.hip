@@ -2,6 +2,7 @@
 // launches.  Every check runs before the first HIP call, so a rejected call
 // touches neither the device nor the stream.
 #include <algorithm>
+#include <cmath>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -665,34 +666,59 @@ struct QuantInputs {
   }
 };
 
-// The tile configuration of a product (index into gemm_tile), by the rows
-// that a group (the whole batch, or a slot's segment on average) has:
-//  * up to 16, 32 and 64: the smallest row tile that holds them (the weights
-//    are read once, whatever the tile; columns and k are cut fine enough to
-//    fill the device);
-//  * more than 128 and at least 256 tiles of 256 x 256 (one per compute unit):
-//    the largest tile, which the matrix cores bound (8192 rows x 8192 x 8192
-//    bf16: 1.3 PFLOP/s against 0.9 with 128 x 128);
-//  * else 128 rows: by 128 columns, one block per compute unit, or by 96, two
-//    blocks per unit, whichever leaves less of the last round of blocks idle
-//    (256 rows on 18432 outputs: 288 blocks for 256 places against 384 for
-//    512, 127 and 103 us; 128 rows on 84000 outputs, 656 against 875: 452 and
-//    486 us).
+// The tile configuration of a product (index into gemm_tile): the one that a
+// simple account of its blocks gives the least time.  A block costs a start and
+// an end (gemm_tile's `fixed`) and, for every byte of k, the bytes of its x and
+// W rows at the rate one compute unit fetches and uses them, shared by the
+// blocks that run on the unit together; blocks run in rounds.  Row tiles above
+// twice the smallest that holds an average group are left out, and the largest
+// is for groups of more than 128 rows (16 slots x 128 rows on 8192 x 8192, W
+// from HBM once: 254 us with 128 rows a tile, 287 with 256, int8; the account
+// knows no HBM).  Measured against it (us): 128 rows on a whole layer's 84000
+// outputs, 195 expected and 207 measured by 128 columns, 293 and 250 by 96;
+// 256 rows on 18432 outputs, 89 and 68 by 96 columns (384 blocks on 512
+// places), 109 and 87 by 128 (288 on 256); 8 experts x 16 rows on average on 2
+// x 28672 outputs, 590 and 630 by 32 rows, 752 and 780 by 16.
 constexpr int kComputeUnits = 256;
-int pick_gemm(int64_t rows, int64_t groups, const int *d_out, int n) {
+constexpr double kUnitBytesPerUs = 45000;
+
+// Row tiles of t rows: every group ends inside one, in its middle on average;
+// a group expected to fit in one may be larger than the average.
+double row_tiles_expected(int64_t rows, int64_t groups, int t) {
+  if (groups == 1) return (double)((rows + t - 1) / t);
+  const double per = (double)rows / (double)groups;
+  if (per >= t) return (double)groups * (per / t + 0.5);
+  const double spread = std::sqrt(per) + 0.15 * per;
+  return (double)groups * (1 + std::max(0.0, 0.5 - (t - per) / (3.4 * spread)));
+}
+
+int pick_gemm(int64_t rows, int64_t groups, const GemmModule *m, int n) {
   const int64_t per = (rows + groups - 1) / groups;
-  for (int cfg = 0; cfg < 3; ++cfg)
-    if (per <= gemm_tile(cfg).rows) return cfg;
-  auto blocks = [&](int cfg) {
+  int fit = 0;
+  while (fit + 1 < kGemmTiles && gemm_tile(fit).rows < per) ++fit;
+  int best = 0;
+  double least = 0;
+  for (int cfg = 0; cfg < kGemmTiles; ++cfg) {
     const GemmTile t = gemm_tile(cfg);
-    int64_t b = 0;
-    for (int i = 0; i < n; ++i) b += groups * ((per + t.rows - 1) / t.rows) * ((d_out[i] + t.cols - 1) / t.cols);
-    return b;
-  };
-  if (per > 128 && blocks(5) >= kComputeUnits) return 5;
-  const int64_t wide = (blocks(4) + kComputeUnits - 1) / kComputeUnits * gemm_tile(4).cols;
-  const int64_t narrow = (blocks(3) + 2 * kComputeUnits - 1) / (2 * kComputeUnits) * 2 * gemm_tile(3).cols;
-  return narrow < wide ? 3 : 4;
+    if (cfg > 0 && (t.rows > 2 * gemm_tile(fit).rows || (t.rows > 128 && per <= 128))) continue;
+    const double rt = row_tiles_expected(rows, groups, t.rows);
+    double blocks = 0;
+    for (int i = 0; i < n; ++i) blocks += rt * ((m[i].d_out + t.cols - 1) / t.cols);
+    const double share = std::min((double)t.per_unit, std::ceil(blocks / kComputeUnits));
+    double sum = 0, longest = 0;
+    for (int i = 0; i < n; ++i) {
+      const double one = t.fixed + share * (t.rows + t.cols) * (double)m[i].kbytes / kUnitBytesPerUs;
+      sum += rt * ((m[i].d_out + t.cols - 1) / t.cols) * one;
+      longest = std::max(longest, one);
+    }
+    const double fill = blocks / (kComputeUnits * t.per_unit);  // rounds; the last of many overlaps the one before
+    const double us = std::max(longest, sum / blocks * (fill <= 2 ? std::ceil(fill) : fill + 0.4));
+    if (cfg == 0 || us < least) {
+      best = cfg;
+      least = us;
+    }
+  }
+  return best;
 }
 
 // Number the blocks of n projections (g.mod[0..n), longest d_in first: a
@@ -786,11 +812,6 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
   if (!do_fused) return LORA_OK;
   if constexpr (kI8) {
     GemmDesc g{};
-    int outs[LORA_NUM_MODULES];
-    for (int i = 0; i < n; ++i) outs[i] = la[i].d_out;
-    const int cfg = pick_gemm(num_rows, 1, outs, n);
-    const GemmTile tile = gemm_tile(cfg);
-    g.row_tiles = (num_rows + tile.rows - 1) / tile.rows;
     for (int i = 0; i < n; ++i) {
       const auto &in = quant.d.in[quant_of[i]];
       GemmModule &gm = g.mod[i];
@@ -810,6 +831,8 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       gm.col = ms[i].col;
       gm.rows_per_x = 1;
     }
+    const int cfg = pick_gemm(num_rows, 1, g.mod, n);
+    g.row_tiles = (num_rows + gemm_tile(cfg).rows - 1) / gemm_tile(cfg).rows;
     g.rs = rs;
     g.max_rank = max_rank;
     g.ids = row_adapter;
@@ -927,7 +950,6 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
   if (num_rows < 0 || num_slots < 1) return LORA_ERR_SHAPE;
   GemmDesc g{};
   QuantInputs quant;
-  int outs[LORA_NUM_MODULES];
   int n = 0;
   int64_t sum_d_in = 0;
   for (int c = 0; c < LORA_NUM_MODULES; ++c) {
@@ -955,7 +977,7 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
     gm.y = static_cast<uint16_t *>(m.y);
     gm.ldy = m.ldy;
     gm.d_in = m.d_in;
-    gm.d_out = outs[n] = m.d_out;
+    gm.d_out = m.d_out;
     gm.col = c;
     gm.rows_per_x = m.rows_per_x;
     sum_d_in += m.d_in;
@@ -974,7 +996,7 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
   }
   g.weights = weights;
   const int groups = segment_bound(num_rows, num_slots, seg);
-  const int cfg = pick_gemm(num_rows, groups, outs, n);
+  const int cfg = pick_gemm(num_rows, groups, g.mod, n);
   const int rt = gemm_tile(cfg).rows;
   // every segment's last tile may be partial
   const int64_t row_tiles = std::min<int64_t>(num_rows, (int64_t)num_rows / rt + groups);

@@ -57,14 +57,21 @@ void pick(const GemmDesc &d, int cfg, int blocks, hipStream_t s) {
 
 }  // namespace
 
+namespace {
+template <class C>
+constexpr GemmTile tile_of(double fixed) {
+  return {C::RT, C::NC, 160 * 1024 / C::LDS, fixed};
+}
+}  // namespace
+
 GemmTile gemm_tile(int cfg) {
   switch (cfg) {
-    case 0: return {Cfg16<true>::RT, Cfg16<true>::NC};
-    case 1: return {Cfg32<true>::RT, Cfg32<true>::NC};
-    case 2: return {Cfg64<true>::RT, Cfg64<true>::NC};
-    case 3: return {Cfg128n<true>::RT, Cfg128n<true>::NC};
-    case 4: return {Cfg128<true>::RT, Cfg128<true>::NC};
-    default: return {Cfg256<true>::RT, Cfg256<true>::NC};
+    case 0: return tile_of<Cfg16<true>>(6);
+    case 1: return tile_of<Cfg32<true>>(6);
+    case 2: return tile_of<Cfg64<true>>(6);
+    case 3: return tile_of<Cfg128n<true>>(8);
+    case 4: return tile_of<Cfg128<true>>(8);
+    default: return tile_of<Cfg256<true>>(16);
   }
 }
 

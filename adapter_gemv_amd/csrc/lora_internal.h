@@ -236,6 +236,8 @@ enum GemmKind { kLinearI8 = 0, kGroupedBf16 = 1, kGroupedI8 = 2 };
 // Tile configurations by rows per block; index into gemm_tile().
 struct GemmTile {
   int rows, cols;
+  int per_unit;   // blocks that a compute unit holds (their LDS)
+  double fixed;   // us from a block's start to its first product, and of its end
 };
 constexpr int kGemmTiles = 6;
 GemmTile gemm_tile(int cfg);
