@@ -660,15 +660,17 @@ struct QuantInputs {
     };
     in.q = static_cast<int8_t *>(take((size_t)rows * in.pitch));
     in.s = static_cast<float *>(take((size_t)rows * 4));
+    in.rows_per_block = d_in <= kQuantWaveMax ? 4 : 1;
     in.block_base = d.blocks;
-    d.blocks += (int)rows;  // at most 7 times the rows of a matrix of 16-byte rows below 4 GiB
+    d.blocks += (int)((rows + in.rows_per_block - 1) / in.rows_per_block);  // at most 7 times the rows of a matrix of 16-byte rows below 4 GiB
     return d.n++;
   }
 };
 
 // The tile configuration of a product (index into gemm_tile): the one that a
 // simple account of its blocks gives the least time.  A block costs a start and
-// an end (gemm_tile's `fixed`) and, for every byte of k, the bytes of its x and
+// an end (gemm_tile's `fixed`, and `per_adapter` for each adapter that 16 of
+// its rows may have) and, for every byte of k, the bytes of its x and
 // W rows at the rate one compute unit fetches and uses them, shared by the
 // blocks that run on the unit together; blocks run in rounds.  Row tiles above
 // twice the smallest that holds an average group are left out, and the largest
@@ -692,7 +694,7 @@ double row_tiles_expected(int64_t rows, int64_t groups, int t) {
   return (double)groups * (1 + std::max(0.0, 0.5 - (t - per) / (3.4 * spread)));
 }
 
-int pick_gemm(int64_t rows, int64_t groups, const GemmModule *m, int n) {
+int pick_gemm(int64_t rows, int64_t groups, int adapters, const GemmModule *m, int n) {
   const int64_t per = (rows + groups - 1) / groups;
   int fit = 0;
   while (fit + 1 < kGemmTiles && gemm_tile(fit).rows < per) ++fit;
@@ -707,7 +709,7 @@ int pick_gemm(int64_t rows, int64_t groups, const GemmModule *m, int n) {
     const double share = std::min((double)t.per_unit, std::ceil(blocks / kComputeUnits));
     double sum = 0, longest = 0;
     for (int i = 0; i < n; ++i) {
-      const double one = t.fixed + share * (t.rows + t.cols) * (double)m[i].kbytes / kUnitBytesPerUs;
+      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + share * (t.rows + t.cols) * (double)m[i].kbytes / kUnitBytesPerUs;
       sum += rt * ((m[i].d_out + t.cols - 1) / t.cols) * one;
       longest = std::max(longest, one);
     }
@@ -831,7 +833,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       gm.col = ms[i].col;
       gm.rows_per_x = 1;
     }
-    const int cfg = pick_gemm(num_rows, 1, g.mod, n);
+    const int cfg = pick_gemm(num_rows, 1, segment_bound(num_rows, num_slots, seg), g.mod, n);
     g.row_tiles = (num_rows + gemm_tile(cfg).rows - 1) / gemm_tile(cfg).rows;
     g.rs = rs;
     g.max_rank = max_rank;
@@ -996,7 +998,7 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
   }
   g.weights = weights;
   const int groups = segment_bound(num_rows, num_slots, seg);
-  const int cfg = pick_gemm(num_rows, groups, g.mod, n);
+  const int cfg = pick_gemm(num_rows, groups, 0, g.mod, n);
   const int rt = gemm_tile(cfg).rows;
   // every segment's last tile may be partial
   const int64_t row_tiles = std::min<int64_t>(num_rows, (int64_t)num_rows / rt + groups);

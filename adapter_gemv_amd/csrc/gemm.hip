@@ -60,7 +60,7 @@ void pick(const GemmDesc &d, int cfg, int blocks, hipStream_t s) {
 namespace {
 template <class C>
 constexpr GemmTile tile_of(double fixed) {
-  return {C::RT, C::NC, 160 * 1024 / C::LDS, fixed};
+  return {C::RT, C::NC, 160 * 1024 / C::LDS, fixed, 0.3 * C::MT * C::NTE / C::DT};
 }
 }  // namespace
 

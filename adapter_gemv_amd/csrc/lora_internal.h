@@ -224,8 +224,10 @@ struct QuantInput {
   int32_t d_in;
   int32_t pitch;     // bytes of a row of q, a multiple of 16
   int32_t rows;
-  int32_t block_base;  // first block of this input (one per row)
+  int32_t block_base;  // first block of this input
+  int32_t rows_per_block;  // 1, or 4 (a wave each) for rows up to kQuantWaveMax
 };
+constexpr int kQuantWaveMax = 4096;
 struct QuantDesc {
   QuantInput in[kMaxModules];
   int32_t n;
@@ -238,6 +240,7 @@ struct GemmTile {
   int rows, cols;
   int per_unit;   // blocks that a compute unit holds (their LDS)
   double fixed;   // us from a block's start to its first product, and of its end
+  double per_adapter;  // us of its end for each adapter among 16 rows (its waves' row tiles in turn)
 };
 constexpr int kGemmTiles = 6;
 GemmTile gemm_tile(int cfg);
