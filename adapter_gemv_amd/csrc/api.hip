@@ -625,9 +625,14 @@ lora_status_t check_linear(const lora_linear_q4_io_t &m, LinearArgs *a) {
   return LORA_OK;
 }
 
+// Widths and leading dimensions beyond this are refused before any product of
+// them is formed (a matrix of one such row is 1 GiB of bf16).
+constexpr int64_t kMaxDim = 1 << 29;
+
 lora_status_t check_linear(const lora_linear_i8_io_t &m, LinearArgs *a) {
   if (!m.x || !m.y || !m.Wq || !m.Ws) return LORA_ERR_NULL;
-  if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.ldwq < m.d_in || m.d_in > LORA_I8_MAX_IN)
+  if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.ldwq < m.d_in || m.d_in > LORA_I8_MAX_IN ||
+      m.ldx > kMaxDim || m.ldy > kMaxDim || m.d_out > kMaxDim)
     return LORA_ERR_SHAPE;
   if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || (m.ldwq & 15) || !aligned16(m.x) ||
       !aligned16(m.y) || !aligned16(m.Wq) || !aligned16(m.Ws))
@@ -958,7 +963,9 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
     if (!(module_mask & (1u << c))) continue;
     const lora_grouped_io_t &m = io[c];
     if (!m.x || !m.y) return LORA_ERR_NULL;
-    if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.rows_per_x < 1) return LORA_ERR_SHAPE;
+    if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.rows_per_x < 1 || m.ldx > kMaxDim ||
+        m.ldy > kMaxDim)
+      return LORA_ERR_SHAPE;
     if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || !aligned16(m.x) || !aligned16(m.y))
       return LORA_ERR_ALIGN;
     if (i8 && m.d_in > LORA_I8_MAX_IN) return LORA_ERR_SHAPE;

@@ -557,8 +557,9 @@ size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots,
  * the delta alone; a row that holds an infinity or a NaN gives NaN in all its
  * outputs, and only there.  Any batch, from one decode row to a prefill: the
  * tile follows the number of rows.  Projections of a call that share x (same
- * pointer, ldx and d_in) share its quantised rows.  Launches on `stream`: the
- * row quantiser, the grouped shrink, the sum of its partials, one product.
+ * pointer, ldx and d_in) share its quantised rows.  Three launches on `stream`:
+ * the grouped shrink, the row quantiser with the sum of the shrink's partials,
+ * one product.  Results are bit-reproducible.
  *
  *   io           array of LORA_NUM_MODULES entries, read where module_mask
  *                has a bit: x, Wq, Ws, y 16-byte aligned; d_in, d_out, ldx,
@@ -568,7 +569,7 @@ size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots,
  *
  * Errors: those of lora_linear_layer; LORA_ERR_NULL for a null Wq or Ws,
  * LORA_ERR_ALIGN for an ldwq that is not a multiple of 16, LORA_ERR_SHAPE for
- * ldwq < d_in or d_in > LORA_I8_MAX_IN.
+ * ldwq < d_in, d_in > LORA_I8_MAX_IN, or a d_out, ldx or ldy above 2^29.
  */
 lora_status_t lora_linear_layer_i8(const lora_linear_i8_io_t *io, uint32_t module_mask,
                                    int32_t num_rows, const int32_t *row_adapter,
@@ -645,7 +646,9 @@ size_t lora_grouped_workspace_bytes(int32_t num_rows, int32_t num_slots,
  * and Evolution" (promotion: W' = W + BA for a hot adapter, served as a full
  * weight); "LoRA, quotas and noisy neighbours", "One weight read, many
  * adapters" (rows tagged and grouped, each weight read once for its group).
- * bf16 matrix cores, fp32 sums, one rounding; one launch.
+ * bf16 matrix cores, fp32 sums, one rounding; one launch.  The order of a sum
+ * depends on the tile, which follows the batch, so a row's bits may differ
+ * between batches; the same call gives the same bits.
  *
  *   io       array of LORA_NUM_MODULES entries, read where module_mask has a
  *            bit: x, y 16-byte aligned; d_in, d_out, ldx, ldy multiples of 8
@@ -655,8 +658,8 @@ size_t lora_grouped_workspace_bytes(int32_t num_rows, int32_t num_slots,
  *            fit the batch and one per (segment, projection) whose entry
  *            cannot be used
  * No workspace.
- * Errors: LORA_ERR_NULL, LORA_ERR_SHAPE (sizes, rows_per_x < 1, a matrix of 4
- * GiB or more), LORA_ERR_ALIGN, LORA_ERR_MODULE (mask 0 or above 0x7f),
+ * Errors: LORA_ERR_NULL, LORA_ERR_SHAPE (sizes, rows_per_x < 1, a leading
+ * dimension above 2^29, a matrix of 4 GiB or more), LORA_ERR_ALIGN, LORA_ERR_MODULE (mask 0 or above 0x7f),
  * LORA_ERR_LAUNCH.
  */
 lora_status_t lora_grouped_layer(const lora_grouped_io_t *io, uint32_t module_mask,

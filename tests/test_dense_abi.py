@@ -32,6 +32,7 @@ CALL = dict(mask=1, n=40, ids=P, table=P, slots=4, seg=seg(), rank=16, ws=P, ws_
     (dict(d_in=0), {}, SHAPE), (dict(d_out=-8), {}, SHAPE), (dict(ldx=248), {}, SHAPE), (dict(ldy=120), {}, SHAPE),
     (dict(ldwq=240), {}, SHAPE), (dict(d_in=131080, ldx=131080, ldwq=131088), {}, SHAPE),
     (dict(d_out=1 << 25, ldy=1 << 25), {}, SHAPE), (dict(ldwq=1 << 60), {}, SHAPE), (dict(ldx=1 << 40), {}, SHAPE),
+    (dict(ldx=1 << 61), {}, SHAPE), (dict(ldy=1 << 61), {}, SHAPE), (dict(d_out=(1 << 29) + 8, ldy=(1 << 29) + 8), {}, SHAPE),
     ({}, dict(n=-1), SHAPE), ({}, dict(slots=0), SHAPE), ({}, dict(seg=seg(max_segments=-1)), SHAPE),
     (dict(d_in=252), {}, ALIGN), (dict(d_out=124), {}, ALIGN), (dict(ldx=260), {}, ALIGN), (dict(ldy=132), {}, ALIGN),
     (dict(ldwq=264), {}, ALIGN), (dict(x=P + 8), {}, ALIGN), (dict(y=P + 2), {}, ALIGN), (dict(Wq=P + 8), {}, ALIGN),
@@ -55,7 +56,9 @@ def test_linear_i8_rejects(fn, io, call, code):
     ({}, dict(seg=seg(seg_offsets=None)), NULL),
     (dict(d_in=0), {}, SHAPE), (dict(d_out=0), {}, SHAPE), (dict(ldx=248), {}, SHAPE), (dict(ldy=120), {}, SHAPE),
     (dict(rows_per_x=0), {}, SHAPE), (dict(rows_per_x=-2), {}, SHAPE), (dict(ldx=1 << 40), {}, SHAPE),
-    (dict(ldy=1 << 40), {}, SHAPE), ({}, dict(n=-1), SHAPE), ({}, dict(slots=0), SHAPE),
+    (dict(ldy=1 << 40), {}, SHAPE), (dict(ldx=1 << 61), {}, SHAPE), (dict(ldy=1 << 61), {}, SHAPE),
+    (dict(d_in=1 << 30, ldx=1 << 30), dict(n=1), SHAPE), (dict(d_out=1 << 30, ldy=1 << 30), dict(n=1), SHAPE),
+    ({}, dict(n=-1), SHAPE), ({}, dict(slots=0), SHAPE),
     ({}, dict(seg=seg(max_segments=-1)), SHAPE),
     (dict(d_in=252), {}, ALIGN), (dict(d_out=124), {}, ALIGN), (dict(ldx=260), {}, ALIGN), (dict(ldy=132), {}, ALIGN),
     (dict(x=P + 8), {}, ALIGN), (dict(y=P + 8), {}, ALIGN),

@@ -297,3 +297,40 @@ def test_experts_of_an_mlp(int8):
     down.dev["down"].x = h
     down.cpu["down"]["x"] = h.cpu()
     down.check()
+
+
+@pytest.mark.parametrize("int8", FORMS)
+def test_offsets_near_4_gib(int8):
+    """x rows and weight rows so far apart that the last ones start just below 4 GiB."""
+    rows, d = 262000, 72
+    ldx = 8192 - 8                                   # 262000 rows * 16368 bytes
+    r = Run(int8, ids_of("mixed", 300, 2, 3), 2, {"q": (d, 40, "a")}, seed=91)
+    keep = [0, 1, rows // 2, rows - 2, rows - 1]
+    ids = np.full(rows, -1, np.int32)
+    ids[keep] = [0, 1, 1, 0, 1]
+    x = torch.zeros(rows * ldx, dtype=torch.bfloat16, device="cuda").view(rows, ldx)
+    xs = bf16(gen(5), len(keep), d)
+    x[keep, :d] = xs.cuda()
+    y = torch.full((rows, 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    elt = 1 if int8 else 2
+    ldw = (4294967040 // elt // 40) // 16 * 16
+    host = r.host.copy()
+    big = torch.zeros(40 * ldw, dtype=torch.int8 if int8 else torch.bfloat16, device="cuda").view(40, ldw)
+    W = r.cpu["q"]["W"][1]
+    big[:, :d] = W.cuda()
+    host["W"][1, 0], host["ldw"][1, 0] = big.data_ptr(), ldw
+    table = torch.from_numpy(host.view(np.uint8).reshape(-1).copy()).cuda()
+    seg = lg.Segments(rows, max_segments=2)
+    ws = torch.empty(max(lg.grouped_workspace_bytes(rows, 2, d, 1), 16), dtype=torch.uint8, device="cuda")
+    dids = torch.from_numpy(ids).cuda()
+    lg.build_segments(dids, 2, seg, ws)
+    lg.grouped_layer({"q": lg.GroupedIO(x, y, d_in=d)}, rows, table, 2, seg, ws, int8=int8)
+    torch.cuda.synchronize()
+    assert int(seg.status.item()) == 0
+    for i, b in enumerate(keep):
+        a = int(ids[b])
+        Ws = r.cpu["q"]["Ws"][a]
+        ref, slack = (base_i8(xs[i:i + 1], r.cpu["q"]["W"][a], Ws) if int8 else grouped_bf16(xs[i:i + 1], r.cpu["q"]["W"][a]))
+        close(y[b:b + 1], ref, slack, f"row {b}")
+    y[keep] = 7.0
+    assert bool((y == 7).all())
