@@ -187,13 +187,13 @@ _raw_stream = None  # torch's lookup of the current stream's handle, without a S
 def _stream(stream):
     global _raw_stream
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     if _raw_stream is None:
         import torch
         torch.cuda.current_stream()  # initialises the device
         get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
         _raw_stream = ((lambda: get(dev())) if get and dev else (lambda: torch.cuda.current_stream().cuda_stream))
-    return ctypes.c_void_p(_raw_stream())
+    return _raw_stream()
 
 
 def _rows(t, dtype, rows, dev, name, field):
@@ -214,7 +214,7 @@ def _rows(t, dtype, rows, dev, name, field):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, dtype, what, ndim=None):
@@ -396,7 +396,9 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
     base weights); see lora_linear_layer, lora_linear_layer_q4 and
     lora_linear_layer_i8."""
     import torch
-    _need(row_adapter, torch.int32, "row_adapter", 1)
+    if type(row_adapter) is not torch.Tensor or row_adapter.dtype is not torch.int32 or not row_adapter.is_cuda or \
+            row_adapter.stride() != (1,):
+        _need(row_adapter, torch.int32, "row_adapter", 1)
     kind = type(next(iter(ios.values()))) if ios else LinearIO
     if kind not in _LINEAR_KINDS:
         kind = next((k for k in _LINEAR_KINDS if any(isinstance(io, k) for io in ios.values())), LinearIO)
@@ -528,8 +530,10 @@ def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, 
 def build_segments(row_adapter, num_slots: int, seg: Segments, ws, stream=None):
     """Group rows by adapter slot (stable); see lora_build_segments."""
     import torch
-    _need(row_adapter, torch.int32, "row_adapter", 1)
-    n = row_adapter.shape[0]
+    if type(row_adapter) is not torch.Tensor or row_adapter.dtype is not torch.int32 or not row_adapter.is_cuda or \
+            row_adapter.stride() != (1,):
+        _need(row_adapter, torch.int32, "row_adapter", 1)
+    n = row_adapter.size(0)
     if n > seg.num_rows:
         raise ValueError("Segments buffers too small for this batch")
     _check(lib().lora_build_segments(_ptr(row_adapter), n, num_slots, seg.c(), _ptr(ws), ws.numel() * ws.element_size(),
