@@ -637,7 +637,8 @@ lora_status_t check_linear(const lora_linear_i8_io_t &m, LinearArgs *a) {
   if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || (m.ldwq & 15) || !aligned16(m.x) ||
       !aligned16(m.y) || !aligned16(m.Wq) || !aligned16(m.Ws))
     return LORA_ERR_ALIGN;
-  if (m.ldwq > (int64_t)0xFFFFFF00 / m.d_out) return LORA_ERR_SHAPE;
+  // the weight, and a B of the largest rank, below 4 GiB
+  if (m.ldwq > (int64_t)0xFFFFFF00 / m.d_out || m.d_out > (int64_t)0xFFFFFF00 / (2 * LORA_MAX_RANK)) return LORA_ERR_SHAPE;
   *a = LinearArgs{m.x, m.ldx, m.Wq, m.ldwq, static_cast<const float *>(m.Ws), 0, m.y, m.ldy, m.d_in, m.d_out};
   return LORA_OK;
 }

@@ -90,7 +90,7 @@ __device__ __forceinline__ void dma16(u32x4 r, uint32_t voff, uint32_t soff, uin
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-               : "memory");
+               : "memory", "m0");
 }
 
 // Wait until at most N of this wave's loads are outstanding and its LDS reads
@@ -446,6 +446,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   // ---- this lane's pieces of a stage: offsets of the rows it loads
   const u32x4 rx = rsrc_words(m.x, m.x_bytes);
   const u32x4 rw = rsrc_words(W, (uint32_t)(ldw * m.d_out));
+  // the resources are written by vector instructions; the assembly that reads
+  // them needs 5 wait states after those, which the compiler does not count
+  asm volatile("s_nop 4" : : "s"(rx), "s"(rw));
   constexpr int RPI = 1024 / C::KB > 0 ? 1024 / C::KB : 1;  // rows per load instruction
   static_assert(C::KB <= 1024, "a load instruction covers whole rows");
   const int lrow = lane / C::PIECES, lslot = lane % C::PIECES;

@@ -569,7 +569,8 @@ size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots,
  *
  * Errors: those of lora_linear_layer; LORA_ERR_NULL for a null Wq or Ws,
  * LORA_ERR_ALIGN for an ldwq that is not a multiple of 16, LORA_ERR_SHAPE for
- * ldwq < d_in, d_in > LORA_I8_MAX_IN, or a d_out, ldx or ldy above 2^29.
+ * ldwq < d_in, d_in > LORA_I8_MAX_IN, an ldx or ldy above 2^29, or a
+ * d_out of 2^25 and more (a factor B of 4 GiB).
  */
 lora_status_t lora_linear_layer_i8(const lora_linear_i8_io_t *io, uint32_t module_mask,
                                    int32_t num_rows, const int32_t *row_adapter,

@@ -33,6 +33,7 @@ CALL = dict(mask=1, n=40, ids=P, table=P, slots=4, seg=seg(), rank=16, ws=P, ws_
     (dict(ldwq=240), {}, SHAPE), (dict(d_in=131080, ldx=131080, ldwq=131088), {}, SHAPE),
     (dict(d_out=1 << 25, ldy=1 << 25), {}, SHAPE), (dict(ldwq=1 << 60), {}, SHAPE), (dict(ldx=1 << 40), {}, SHAPE),
     (dict(ldx=1 << 61), {}, SHAPE), (dict(ldy=1 << 61), {}, SHAPE), (dict(d_out=(1 << 29) + 8, ldy=(1 << 29) + 8), {}, SHAPE),
+    (dict(d_in=8, ldx=8, ldwq=16, d_out=1 << 25, ldy=1 << 25), dict(n=1), SHAPE),
     ({}, dict(n=-1), SHAPE), ({}, dict(slots=0), SHAPE), ({}, dict(seg=seg(max_segments=-1)), SHAPE),
     (dict(d_in=252), {}, ALIGN), (dict(d_out=124), {}, ALIGN), (dict(ldx=260), {}, ALIGN), (dict(ldy=132), {}, ALIGN),
     (dict(ldwq=264), {}, ALIGN), (dict(x=P + 8), {}, ALIGN), (dict(y=P + 2), {}, ALIGN), (dict(Wq=P + 8), {}, ALIGN),
