@@ -755,9 +755,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 }
 
 // Rows of x as int8 with one scale each: s = max|x| / 127, q = rint(127 x /
-// max|x|).  127 x is exact in fp32 for bf16 x, and the quotient of two 8-bit
-// significands times 127 is a tie or at least 2^-9 away from one, so the
-// correctly rounded quotient rounds to the same integer as the real one.  A
+// max|x|), halves to even.  A
 // zero row: q = 0, s = 0.  A row with an infinity or a NaN: s = NaN (its
 // outputs are NaN), q = 0.  [d_in, pitch) gets 0.  36534 rows of 8192, two
 // inputs: 1.8 GB in 300 us, 6 TB/s.
@@ -771,7 +769,22 @@ __device__ __forceinline__ float abs_max8(u32x4 p, float m, bool *bad) {
   }
   return m;
 }
-__device__ __forceinline__ u32x2 quant8(u32x4 p, float amax) {
+// rint(127 x / amax) for 8 values without a division each: x scaled by amax's
+// power of two, times 127 over the rest of amax (one division a row), is within
+// 2 units of the last place of the real quotient.  With 8-bit significands that
+// quotient is a tie or at least 1 / (127 * 255) of itself, 2^8 units, away from
+// one, so rounded to a multiple of 64 units it is exact on a tie and stays on
+// its side otherwise.
+struct QuantScale {
+  int exp;
+  float r;
+};
+__device__ __forceinline__ QuantScale quant_scale(float amax) {
+  int e;
+  const float f = frexpf(amax, &e);
+  return QuantScale{-e, 127.f / f};
+}
+__device__ __forceinline__ u32x2 quant8(u32x4 p, QuantScale qs) {
   uint32_t o[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -780,7 +793,8 @@ __device__ __forceinline__ u32x2 quant8(u32x4 p, float amax) {
     for (int i = 0; i < 4; ++i) {
       const uint32_t u = p[h * 2 + i / 2];
       const float f = (i & 1) ? bf16_hi(u) : bf16_lo(u);
-      v |= ((uint32_t)(int)rintf(f * 127.f / amax) & 0xffu) << (8 * i);
+      const uint32_t near = (__float_as_uint(ldexpf(f, qs.exp) * qs.r) + 32u) & ~63u;
+      v |= ((uint32_t)(int)rintf(__uint_as_float(near)) & 0xffu) << (8 * i);
     }
     o[h] = v;
   }
@@ -806,14 +820,15 @@ __device__ __forceinline__ void quantize_row(const QuantInput &in, int row, int 
   for (int p = REGS * LANES + t; p < n8; p += LANES) mx = abs_max8(*(const u32x4 *)(x + (int64_t)p * 8), mx, &bad);
   row_max(&mx, &bad);
   const bool live = mx > 0.f && !bad;
+  const QuantScale qs = quant_scale(live ? mx : 1.f);
   int8_t *q = in.q + (int64_t)row * in.pitch;
 #pragma unroll
   for (int i = 0; i < REGS; ++i) {
     const int p = i * LANES + t;
-    if (p < n8) *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(keep[i], mx) : u32x2{0u, 0u};
+    if (p < n8) *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(keep[i], qs) : u32x2{0u, 0u};
   }
   for (int p = REGS * LANES + t; p < n8; p += LANES)
-    *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(*(const u32x4 *)(x + (int64_t)p * 8), mx) : u32x2{0u, 0u};
+    *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(*(const u32x4 *)(x + (int64_t)p * 8), qs) : u32x2{0u, 0u};
   if (t == 0) {
     if (in.d_in < in.pitch) *(u32x2 *)(q + in.d_in) = u32x2{0u, 0u};  // the row's last half piece
     in.s[row] = bad ? __int_as_float(0x7fc00000) : mx / 127.f;
@@ -839,7 +854,7 @@ __device__ __forceinline__ void quantize_block(const QuantDesc &qd, const QuantD
   };
   if (in.rows_per_block == 4) {
     const int row = (block - in.block_base) * 4 + w;
-    if (row < in.rows) quantize_row<64, kQuantWaveMax / 512>(in, row, lane, wave_max);
+    if (row < in.rows) quantize_row<64, kQuantRegs>(in, row, lane, wave_max);
     return;
   }
   quantize_row<256, kQuantRegs>(in, block - in.block_base, t, [&](float *mx, bool *bad) {

@@ -220,6 +220,30 @@ def test_ties_and_extremes_of_the_quantiser():
     r.check()
 
 
+@pytest.mark.parametrize("copies", [1, 5])
+def test_quantiser_over_every_pair_of_significands(copies):
+    # row a: amax with significand 128 + a, every significand at 8 magnitudes below it; W is the identity, so the
+    # outputs are the quantised values times the scale (5 copies: rows past the quantiser's registers)
+    sig = torch.arange(128, 256).double()
+    cols = torch.cat([sig * 2.0 ** -k for k in range(1, 9)])                    # all below 128
+    x = torch.stack([torch.cat([cols * (1 if a % 2 else -1), torch.tensor([float(a)]).double()]) for a in range(128, 256)])
+    x = torch.nn.functional.pad(x, (0, 7))                                      # 1032 inputs
+    d = x.shape[1]
+    r = Run(128, 1, {"q": (d * copies, d, "a")}, 8, "none", seed=7)
+    xb = x.repeat(1, copies).to(torch.bfloat16)
+    assert torch.equal(xb[:, :d].double(), x)                                    # every value is a bf16
+    r.cpu["q"]["x"] = xb
+    r.dev["q"].x = xb.cuda()
+    W = torch.zeros(d, -(-d * copies // 16) * 16, dtype=torch.int8)
+    W[torch.arange(d), torch.arange(d) + d * (copies - 1)] = 1                  # the last copy
+    r.dev["q"].Wq.copy_(W)
+    r.dev["q"].Ws.fill_(1.0)
+    got = r.run()["q"].cpu()
+    amax = x.abs().amax(1, keepdim=True)
+    want = (torch.round(127.0 * x / amax).float() * (amax.float() / 127.0)).to(torch.bfloat16)
+    assert torch.equal(got, want)
+
+
 def test_non_finite_rows_stay_alone():
     r = Run(40, 3, {"q": (264, 136, "a")}, 0, "none", seed=8)
     x = r.cpu["q"]["x"].clone()
