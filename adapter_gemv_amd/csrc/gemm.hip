@@ -31,7 +31,28 @@ __global__ __launch_bounds__(256) void quantize_reduce_kernel(LayerDesc d, Quant
   }
 }
 
-//                         I8  RT   NC  WR WC WK  KB  S EU
+// The tiles.  Measured on one MI355X (us; in brackets what was taken):
+//  * 16 rows: 32 slots, 128 rows, 8192 x 8192 bf16 (4.3 GB of weights), by
+//    columns x stages x blocks per unit at 512 bytes of k a stage:
+//    [64 x 2 x 2: 749], 32 x 2 x 3: 800, 32 x 3 x 2: 868, 32 x 6 x 1: 1040,
+//    128 x 2 x 1: 779; 1024 bytes of k: 859.  Two blocks on a unit overlap one
+//    another's start and end, which a deeper ring of one block does not.
+//  * 32 rows: 16 slots x 24 rows, 8192 x 8192, int8 and bf16: [64 columns, 256
+//    bytes, 3 stages: 191, 385], 8 waves on 512 bytes: 198, 361 to 388, 32
+//    columns on 512 bytes: 203, 345.
+//  * 64 rows: 16 slots x 64 rows, bf16: [256 bytes, 2 stages: 425], 128 bytes, 4
+//    stages: 453; 128 columns: 459; int8 216 to 219 either way.
+//  * 128 rows: 128 columns on 8 waves, 4 stages, one block a unit; 96 columns on
+//    4 waves, 2 stages, two blocks (see pick_gemm).  A whole layer's int8 base and delta: [676
+//    and 712], 128 columns with 5 stages 683, 256 bytes x 2 stages 692, 2
+//    stages and two blocks 746, 64 columns 732, 256 columns 780.
+//  * 256 x 256 on 4 waves of 128 x 128 (gemm_block): 8192 x 8192 x 8192 bf16 860
+//    to 900 us (1.22 to 1.28 PFLOP/s; torch.mm 800), 16384 of
+//    each 1.41 to 1.46 PFLOP/s (1.58), int8 with the quantiser 2.6 POP/s
+//    (2.38).  The counters show the matrix cores busy for 71% of the cycles of
+//    a prefill at the 1.8 GHz its power leaves.  8 waves of 128 x 64 with no
+//    operands ahead: 1.05 PFLOP/s on the grouped prefill against 1.2.
+//                                           I8  RT   NC  WR WC WK  KB  S EU
 template <bool I8> using Cfg16 = GemmCfg<I8, 16, 64, 1, 1, 4, 512, 2, 2>;
 template <bool I8> using Cfg32 = GemmCfg<I8, 32, 64, 1, 1, 4, 256, 3, 2>;
 template <bool I8> using Cfg64 = GemmCfg<I8, 64, 64, 2, 2, 1, 256, 2, 2>;
