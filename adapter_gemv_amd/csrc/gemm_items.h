@@ -12,9 +12,10 @@
 // body serves both and only the matrix-core instruction differs.
 //   * x and W go to LDS by direct loads (no registers in between), S stages of
 //     KB bytes per row in a ring, S - 1 of them in flight.  The 16-byte pieces
-//     of a row are stored at piece ^ (row mod 8), so that the 8 rows an
-//     operand read touches per cycle fall into different banks; the loads
-//     write LDS in lane order, so the lanes fetch the pieces in that order.
+//     of a row are stored at piece ^ (row mod 16) (rows of 128 bytes: mod 8, a
+//     row fills half the 64 banks), so that the 16 rows an operand read
+//     touches per cycle fall into different banks; the loads write LDS in
+//     lane order, so the lanes fetch the pieces in that order.
 //   * The loads are issued by inline assembly: they return nothing to
 //     registers, and the compiler, which does not know which stage a load
 //     fills, would wait for all of them before every LDS read.  A wave waits
@@ -52,6 +53,7 @@ struct GemmCfg {
   static constexpr int MT = RT / WR / 16, NT = NC / WC / 16;  // 16 x 16 tiles of a wave
   static constexpr int NTE = NT >= WK ? NT / WK : 1;   // column tiles a wave finishes (epilogue)
   static constexpr int PIECES = KB / 16;
+  static constexpr int SWZ = PIECES >= 16 ? 15 : 7;    // rows whose pieces are moved against one another
   static constexpr int XL = RT * KB / 1024 / NW, WL = NC * KB / 1024 / NW;  // loads per wave and stage
   static constexpr int XBYTES = RT * KB, STAGE = (RT + NC) * KB;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
@@ -461,13 +463,13 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const int rr = min(r, rows - 1);  // past the tile: its last row again (never stored)
     int b = row0 + rr;
     if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
-    xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & 7)) * 16);
+    xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
   }
 #pragma unroll
   for (int i = 0; i < C::WL; ++i) {
     const int r = (i * C::NW + w) * RPI + lrow;
     const int n = min(n0 + r, m.d_out - 1);
-    woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((lslot ^ (r & 7)) * 16);
+    woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
   }
 
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
@@ -485,7 +487,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     } else {
 #pragma unroll
       for (int i = 0; i < C::XL; ++i) {
-        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & 7);
+        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & C::SWZ);
         dma16(rx, piece * 16 < left ? xoff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
       }
     }
@@ -500,7 +502,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     } else {
 #pragma unroll
       for (int i = 0; i < C::WL; ++i) {
-        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & 7);
+        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & C::SWZ);
         dma16(rw, piece * 16 < left ? woff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
       }
     }
@@ -557,7 +559,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     constexpr int SLOTS = C::MT + C::NT, PER = C::MT * C::NT / SLOTS;  // operand reads of a step, products per read
     static_assert(!C::PIPE || (C::XL * 2 == SLOTS && C::WL * 2 == SLOTS), "a load every second operand read");
     u32x4 xa[C::MT], wa[C::NT], xb[C::MT], wb[C::NT];
-    const int s0 = ((0 + g) ^ (r_in & 7)) * 16, s1 = ((4 + g) ^ (r_in & 7)) * 16;
+    const int s0 = ((0 + g) ^ (r_in & C::SWZ)) * 16, s1 = ((4 + g) ^ (r_in & C::SWZ)) * 16;
     const int wrow0 = wrow - C::XBYTES;
     uint32_t A = 0, B = PL, Cc = 2 * PL, D = 3 * PL, E = 4 * PL;
     issue_w(0, A);
@@ -628,7 +630,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & 7)) * 16;
+      const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & C::SWZ)) * 16;
       u32x4 xo[C::MT], wo[C::NT];
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) xo[mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + slot16);

@@ -219,6 +219,17 @@ def test_non_finite_rows_and_weights_stay_alone(int8):
         assert bool(torch.isnan(got[7]).all())
 
 
+@pytest.mark.parametrize("rows,fan", [(1, 1), (37, 2), (300, 1)])
+def test_workspace_is_not_overrun(rows, fan):
+    shapes = {"q": (1032, 72, "a"), "o": (8, 264, "o"), "down": (4104, 16, "d")}
+    r = Run(True, ids_of("mixed", rows, 5, 2), 5, shapes, fan=fan, seed=17)
+    n = lg.grouped_workspace_bytes(rows, 5, sum(s[0] for s in shapes.values()), len(shapes))
+    big = torch.full((n + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    r.ws = big[:n]
+    r.check()
+    assert bool((big[n:] == 0x5a).all())
+
+
 @pytest.mark.parametrize("int8", FORMS)
 def test_no_rows(int8):
     r = Run(int8, [-1] * 20, 3, {"q": (136, 72, "a")}, seed=15)

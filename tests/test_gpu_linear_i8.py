@@ -401,3 +401,14 @@ def test_most_inputs_and_largest_sums():
     r.cpu["down"]["Wq"][:] = -128
     r.dev["down"].Wq.fill_(-128)
     r.check()
+
+
+@pytest.mark.parametrize("rows", [1, 37, 300])
+def test_workspace_is_not_overrun(rows):
+    shapes = {"q": (1032, 72, "a"), "k": (1032, 40, "a"), "o": (8, 264, "o"), "down": (4104, 16, "d")}
+    r = Run(rows, 5, shapes, (5, 64), "mixed", seed=63)
+    n = r.ws.numel()
+    big = torch.full((n + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    r.ws = big[:n]
+    r.check()
+    assert bool((big[n:] == 0x5a).all())
