@@ -272,6 +272,9 @@ size_t quant_ws_bytes(int64_t num_rows, int64_t sum_d_in, int n) {
   return per + (size_t)n * ((size_t)num_rows * 4 + 512);
 }
 
+// The rows by slot.
+size_t order_ws_bytes(int num_rows) { return ((size_t)num_rows * 4 + 255) & ~(size_t)255; }
+
 // The end of the v planes of a fused layer call's workspace (a multiple of
 // 256): the int8 form's quantised rows follow.
 size_t linear_v_end(int num_rows, int max_rank, int64_t sum_d_in, int n_modules) {
@@ -295,7 +298,8 @@ size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots, int32
                                       int32_t n_modules) {
   const size_t base = lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules);
   if (base == 0) return 0;
-  const size_t need = linear_v_end(num_rows, max_rank, sum_d_in, n_modules) + quant_ws_bytes(num_rows, sum_d_in, n_modules);
+  const size_t need = linear_v_end(num_rows, max_rank, sum_d_in, n_modules) + order_ws_bytes(num_rows) +
+                      quant_ws_bytes(num_rows, sum_d_in, n_modules);
   return need > base ? need : base;
 }
 
@@ -801,8 +805,13 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
                                              ((partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255));
   QuantInputs quant;
   int quant_of[LORA_NUM_MODULES] = {};
-  if constexpr (kI8) {  // the int8 rows of x, behind the v planes
-    void *qws = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
+  int32_t *order = nullptr;
+  if constexpr (kI8) {  // the rows by slot and the int8 rows of x, behind the v planes
+    char *behind = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
+    // (a stated bound of nearly a segment per row: nothing to gather)
+    const bool shared = seg.max_segments == 0 || 2 * (int64_t)num_rows >= 3 * (int64_t)seg.max_segments;
+    if (num_rows >= kOrderRows && shared) order = reinterpret_cast<int32_t *>(behind);
+    void *qws = behind + order_ws_bytes(num_rows);
     for (int i = 0; i < n; ++i) quant_of[i] = quant.add(la[i].x, la[i].ldx, la[i].d_in, num_rows, qws);
   }
   if (do_shrink) {
@@ -814,7 +823,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
     fill_desc(d, ms, n, true, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws);
     d.v_out = vplanes;
     d.ldv = rs;
-    st = launched(kI8 ? launch_quantize_reduce(d, quant.d, s) : launch_shrink_reduce(d, s));
+    st = launched(kI8 ? launch_quantize_reduce(d, quant.d, row_adapter, order, s) : launch_shrink_reduce(d, s));
     if (st != LORA_OK) return st;
   }
   if (!do_fused) return LORA_OK;
@@ -839,11 +848,14 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       gm.col = ms[i].col;
       gm.rows_per_x = 1;
     }
-    const int cfg = pick_gemm(num_rows, 1, segment_bound(num_rows, num_slots, seg), g.mod, n);
+    const int segs = segment_bound(num_rows, num_slots, seg);  // adapters among 16 rows: in order, those that meet there
+    const int cfg = pick_gemm(num_rows, 1, order ? (int)std::min<int64_t>(segs, 1 + 16 * (int64_t)segs / num_rows) : segs,
+                              g.mod, n);
     g.row_tiles = (num_rows + gemm_tile(cfg).rows - 1) / gemm_tile(cfg).rows;
     g.rs = rs;
     g.max_rank = max_rank;
     g.ids = row_adapter;
+    g.order = order;
     g.table = table;
     return gemm_launch(g, n, g.row_tiles, num_rows, num_slots, seg, kLinearI8, cfg, s);
   } else {

@@ -18,11 +18,20 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantDesc qd) {
 }
 
 // Between the grouped shrink and the product of an int8 layer call: the rows'
-// quantiser, which needs nothing of the shrink, and the sum of the shrink's
-// partials, in one launch instead of two (4 us of a small call's 25).
-__global__ __launch_bounds__(256) void quantize_reduce_kernel(LayerDesc d, QuantDesc qd, int reduce_blocks) {
+// quantiser and the rows by slot, which need nothing of the shrink, and the sum
+// of the shrink's partials, in one launch (each apart is 4 us of a small
+// call's 25).
+__global__ __launch_bounds__(256) void quantize_reduce_kernel(LayerDesc d, QuantDesc qd, int reduce_blocks,
+                                                              const int32_t *ids, int32_t *order) {
   constexpr int kAt = (sizeof(LayerDesc) + 7) / 8 * 8;  // where the second argument lies
-  const int b = blockIdx.x;
+  // the rows' order first: its last block counts over all the ids before it
+  const int order_blocks = order ? (d.num_rows + 255) / 256 : 0;
+  int b = blockIdx.x;
+  if (b < order_blocks) {
+    order_block(d, ids, order, b);
+    return;
+  }
+  b -= order_blocks;
   if (b < qd.blocks) {
     quantize_block(qd, *(const QuantDesc *)((const char *)(const void *)__builtin_amdgcn_kernarg_segment_ptr() + kAt), b);
   } else {
@@ -115,12 +124,13 @@ hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_quantize_reduce(const LayerDesc &d, const QuantDesc &q, hipStream_t stream) {
+hipError_t launch_quantize_reduce(const LayerDesc &d, const QuantDesc &q, const int32_t *ids, int32_t *order,
+                                  hipStream_t stream) {
   const int64_t reduce = ((int64_t)d.num_rows * d.max_rank + 255) / 256;
-  const int64_t blocks = q.blocks + reduce * d.n_active;
+  const int64_t blocks = q.blocks + reduce * d.n_active + (order ? (d.num_rows + 255) / 256 : 0);
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  quantize_reduce_kernel<<<(unsigned)blocks, 256, 0, stream>>>(d, q, (int)reduce);
+  quantize_reduce_kernel<<<(unsigned)blocks, 256, 0, stream>>>(d, q, (int)reduce, ids, order);
   return hipGetLastError();
 }
 

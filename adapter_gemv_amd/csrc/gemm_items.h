@@ -463,6 +463,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const int rr = min(r, rows - 1);  // past the tile: its last row again (never stored)
     int b = row0 + rr;
     if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
+    else if (d.order) b = (int)min((unsigned)d.order[b], (unsigned)(d.num_rows - 1));
     xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
   }
 #pragma unroll
@@ -517,7 +518,8 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   auto load_info = [&]() {
     if (t >= C::RT) return;
     const int at = row0 + min(t, rows - 1);
-    mine.b = GROUPED ? (int)min((unsigned)d.perm[at], (unsigned)(d.num_rows - 1)) : at;
+    const int32_t *order = GROUPED ? d.perm : d.order;
+    mine.b = order ? (int)min((unsigned)order[at], (unsigned)(d.num_rows - 1)) : at;
     if constexpr (C::I8) mine.xs = m.xs[GROUPED ? mine.b / m.rows_per_x : mine.b];
     mine.a = -1;
     if constexpr (DELTA) {
@@ -803,6 +805,39 @@ __device__ __forceinline__ u32x2 quant8(u32x4 p, QuantScale qs) {
     o[h] = v;
   }
   return u32x2{o[0], o[1]};
+}
+
+// The batch's rows by slot: first those of the segments, as the build sorted
+// them, then the rows whose id has no segment (base only, bad, dropped past the
+// caller's bound) in their own order.  A block places 256 of each; it counts
+// the rows without a segment before its own from the ids.
+__device__ __forceinline__ void order_block(const LayerDesc &d, const int32_t *ids, int32_t *order, int block) {
+  __shared__ int wsum[4];
+  const int t = threadIdx.x, lane = t & 63, w = wave_id();
+  const int nseg = min(*d.num_segments, d.max_seg);
+  const int nvalid = nseg > 0 ? min(max(d.seg_offsets[nseg], 0), d.num_rows) : 0;
+  const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
+  auto without = [&](int b) {
+    const int a = ids[b];
+    return !((unsigned)a < (unsigned)d.num_slots && a <= last_slot);
+  };
+  const int b = block * 256 + t;
+  if (b < nvalid) order[b] = d.perm[b];
+  int before = 0;
+#pragma unroll 8
+  for (int i = t; i < block * 256; i += 256) before += without(i);
+  const uint64_t mine = __ballot(b < d.num_rows && without(min(b, d.num_rows - 1)));
+#pragma unroll
+  for (int k = 32; k >= 1; k /= 2) before += __shfl_xor(before, k, 64);
+  if (lane == 0) wsum[w] = before;
+  __syncthreads();
+  int base = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+  __syncthreads();
+  if (lane == 0) wsum[w] = __popcll(mine);
+  __syncthreads();
+  for (int k = 0; k < w; ++k) base += wsum[k];
+  const int at = nvalid + base + __popcll(mine & ((1ull << lane) - 1));
+  if ((mine >> lane & 1) && at < d.num_rows) order[at] = b;
 }
 
 // `lanes` threads (a wave, or a block of 256) quantise one row, keeping REGS
