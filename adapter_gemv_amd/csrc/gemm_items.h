@@ -243,6 +243,14 @@ __device__ __forceinline__ void mma_settle(f32x4_t (&t)[N]) {
   else asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
 }
 
+// The segments, of a build for more rows than the batch only those that end in it.
+__device__ __forceinline__ int fitting_segments(const int32_t *num_segments, int max_seg, const int32_t *offsets,
+                                                int num_rows) {
+  int n = min(*num_segments, max_seg);
+  while (n > 0 && offsets[n] > num_rows) --n;
+  return n;
+}
+
 // A row of the block's tile, in LDS for the epilogue.
 struct RowInfo {
   const uint8_t *B;      // its adapter's B
@@ -523,8 +531,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     if constexpr (C::I8) mine.xs = m.xs[GROUPED ? mine.b / m.rows_per_x : mine.b];
     mine.a = -1;
     if constexpr (DELTA) {
-      // segments come in ascending slot order: later slots were dropped by the build
-      const int nseg = min(*d.num_segments, d.max_seg);
+      // segments come in ascending slot order: later slots were dropped by the
+      // build, or their segments do not fit the batch and have no v
+      const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
       const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
       const int a = t < rows ? d.ids[mine.b] : -1;
       if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
@@ -814,7 +823,7 @@ __device__ __forceinline__ u32x2 quant8(u32x4 p, QuantScale qs) {
 __device__ __forceinline__ void order_block(const LayerDesc &d, const int32_t *ids, int32_t *order, int block) {
   __shared__ int wsum[4];
   const int t = threadIdx.x, lane = t & 63, w = wave_id();
-  const int nseg = min(*d.num_segments, d.max_seg);
+  const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
   const int nvalid = nseg > 0 ? min(max(d.seg_offsets[nseg], 0), d.num_rows) : 0;
   const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
   auto without = [&](int b) {

@@ -28,7 +28,8 @@ __device__ __forceinline__ void shrink_reduce(const LayerDesc &d, int block, int
   const int a = d.seg_adapter[lo];
   if ((unsigned)a >= (unsigned)d.num_slots) return;
   const lora_adapter_entry_t e = d.table[(int64_t)a * d.table_cols + m.col];  // varies per lane
-  const bool ok = entry_ok(e, d.max_rank);
+  // a segment that does not fit the batch was skipped by the shrink: no delta
+  const bool ok = entry_ok(e, d.max_rank) && d.seg_offsets[lo + 1] <= d.num_rows;
   float sum = 0.f;
   if (ok && j < e.rank)
     for (int c = 0; c < m.n_chunks; ++c) sum += d.part[((int64_t)(m.part_base + c) * d.num_rows + p) * d.rs + j];

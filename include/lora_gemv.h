@@ -559,9 +559,10 @@ size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots,
  * tile follows the number of rows.  Projections of a call that share x (same
  * pointer, ldx and d_in) share its quantised rows.  Three launches on `stream`:
  * the grouped shrink, the row quantiser with the sum of the shrink's partials,
- * one product.  Results are bit-reproducible.  row_adapter and
- * seg belong together: with segments built from other ids or for another
- * number of rows, rows of y may be left unwritten.
+ * one product.  Results are bit-reproducible.  row_adapter and seg belong
+ * together: with segments built from other ids or for another number of rows,
+ * rows of y may be left unwritten (and rows of a segment that does not fit the
+ * batch get no delta).
  *
  *   io           array of LORA_NUM_MODULES entries, read where module_mask
  *                has a bit: x, Wq, Ws, y 16-byte aligned; d_in, d_out, ldx,

@@ -317,6 +317,18 @@ def test_rows_past_the_batch_and_columns_past_d_out_stay():
     close(y[:21, :72], ref, slack, "q")
 
 
+def test_segments_of_a_longer_batch_stay_inside_this_one():
+    # a breach of the precondition (segments and rows belong together): what is written stays inside the batch
+    r = Run(100, 5, {"q": (136, 72, "a")}, 8, "mixed", seed=35)
+    lg.build_segments(r.dids, r.slots, r.seg, r.ws)
+    y = torch.full((100, 72), 7.0, dtype=torch.bfloat16, device="cuda")
+    r.dev["q"].y = y
+    r.rows = 70
+    lg.linear_layer(*r.args())
+    torch.cuda.synchronize()
+    assert bool((y[70:] == 7).all()) and bool(torch.isfinite(y).all())
+
+
 def test_zero_rows():
     r = Run(4, 2, {"q": (136, 72, "a")}, 8, "mixed", seed=34)
     r.rows = 0
