@@ -805,12 +805,12 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
                                              ((partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255));
   QuantInputs quant;
   int quant_of[LORA_NUM_MODULES] = {};
-  int32_t *order = nullptr;
+  int32_t *by_slot = nullptr;
   if constexpr (kI8) {  // the rows by slot and the int8 rows of x, behind the v planes
     char *behind = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
     // (a stated bound of nearly a segment per row: nothing to gather)
     const bool shared = seg.max_segments == 0 || 2 * (int64_t)num_rows >= 3 * (int64_t)seg.max_segments;
-    if (num_rows >= kOrderRows && shared) order = reinterpret_cast<int32_t *>(behind);
+    if (num_rows >= kOrderRows && shared) by_slot = reinterpret_cast<int32_t *>(behind);
     void *qws = behind + order_ws_bytes(num_rows);
     for (int i = 0; i < n; ++i) quant_of[i] = quant.add(la[i].x, la[i].ldx, la[i].d_in, num_rows, qws);
   }
@@ -823,7 +823,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
     fill_desc(d, ms, n, true, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws);
     d.v_out = vplanes;
     d.ldv = rs;
-    st = launched(kI8 ? launch_quantize_reduce(d, quant.d, row_adapter, order, s) : launch_shrink_reduce(d, s));
+    st = launched(kI8 ? launch_quantize_reduce(d, quant.d, row_adapter, by_slot, s) : launch_shrink_reduce(d, s));
     if (st != LORA_OK) return st;
   }
   if (!do_fused) return LORA_OK;
@@ -849,16 +849,16 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       gm.rows_per_x = 1;
     }
     const int segs = segment_bound(num_rows, num_slots, seg);  // adapters among 16 rows: in order, those that meet there
-    const int cfg = pick_gemm(num_rows, 1, order ? (int)std::min<int64_t>(segs, 1 + 16 * (int64_t)segs / num_rows) : segs,
+    const int cfg = pick_gemm(num_rows, 1, by_slot ? (int)std::min<int64_t>(segs, 1 + 16 * (int64_t)segs / num_rows) : segs,
                               g.mod, n);
     g.row_tiles = (num_rows + gemm_tile(cfg).rows - 1) / gemm_tile(cfg).rows;
     g.rs = rs;
     g.max_rank = max_rank;
     g.ids = row_adapter;
-    g.order = order;
+    g.order = by_slot;
     g.table = table;
     return gemm_launch(g, n, g.row_tiles, num_rows, num_slots, seg, kLinearI8, cfg, s);
-  } else {
+  }
   // 3. base projection + delta.  A block's work grows with its module's
   // d_in, and the blocks are dispatched in order, so the modules are numbered
   // longest first: a module of a long d_in (a down projection, 3.5x the
@@ -904,7 +904,6 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
   f.seg_adapter = seg.seg_adapter;
   f.max_seg = segment_bound(num_rows, num_slots, seg);
   return launched(launch_fused(f, kQ4, (int)blocks, s));
-  }
 }
 
 }  // namespace

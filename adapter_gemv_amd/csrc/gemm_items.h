@@ -618,41 +618,41 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     for (; r < rounds; ++r) round(r, false);
     mma_drain();
   } else {
-  // Blocks start at different places along k (a ring): rows of W are a power of
-  // two apart or near it, and blocks in step would all read the same few
-  // channels of HBM.  Few rows: 32 places within an XCD (x is small and stays
-  // in L2; 5.8 -> 6.3 TB/s of W at 16 rows).  128 rows: one place per XCD, so
-  // that its blocks share each stage of x (221 -> 207 us for the 0.86 GB of a
-  // whole layer).
-  const int r0 = C::RT >= 128 ? (int)(((local & 7) * rounds) >> 3) : (int)((((local >> 3) & 31) * rounds) >> 5);
-  auto stage_of = [&](int r) { return r >= rounds ? rounds : r + r0 >= rounds ? r + r0 - rounds : r + r0; };
-  uint32_t put = 0, get = 0;  // ring positions of the next stage to load and to use
+    // Blocks start at different places along k (a ring): rows of W are a power of
+    // two apart or near it, and blocks in step would all read the same few
+    // channels of HBM.  Few rows: 32 places within an XCD (x is small and stays
+    // in L2; 5.8 -> 6.3 TB/s of W at 16 rows).  128 rows: one place per XCD, so
+    // that its blocks share each stage of x (221 -> 207 us for the 0.86 GB of a
+    // whole layer).
+    const int r0 = C::RT >= 128 ? (int)(((local & 7) * rounds) >> 3) : (int)((((local >> 3) & 31) * rounds) >> 5);
+    auto stage_of = [&](int r) { return r >= rounds ? rounds : r + r0 >= rounds ? r + r0 - rounds : r + r0; };
+    uint32_t put = 0, get = 0;  // ring positions of the next stage to load and to use
 #pragma unroll
-  for (int s = 0; s < C::S - 1; ++s) {
-    issue(stage_of(s), put);
-    put += C::STAGE;
-  }
-  load_info();
-  for (int r = 0; r < rounds; ++r) {
-    stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
-    issue(stage_of(r + C::S - 1), put);
-    put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
-    const uint8_t *buf = lds + get;
-    get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & C::SWZ)) * 16;
-      u32x4 xo[C::MT], wo[C::NT];
-#pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt) xo[mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + slot16);
-#pragma unroll
-      for (int nt = 0; nt < C::NT; ++nt) wo[nt] = *(const u32x4 *)(buf + wrow + nt * 16 * C::KB + slot16);
-#pragma unroll
-      for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = mma(wo[nt], xo[mt], acc[nt][mt]);
+    for (int s = 0; s < C::S - 1; ++s) {
+      issue(stage_of(s), put);
+      put += C::STAGE;
     }
-  }
+    load_info();
+    for (int r = 0; r < rounds; ++r) {
+      stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
+      issue(stage_of(r + C::S - 1), put);
+      put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
+      const uint8_t *buf = lds + get;
+      get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & C::SWZ)) * 16;
+        u32x4 xo[C::MT], wo[C::NT];
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) xo[mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + slot16);
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt) wo[nt] = *(const u32x4 *)(buf + wrow + nt * 16 * C::KB + slot16);
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = mma(wo[nt], xo[mt], acc[nt][mt]);
+      }
+    }
   }
   stage_barrier<0>();  // nothing in flight to LDS any more, and every wave is done with it
 
