@@ -258,7 +258,7 @@ struct RowInfo {
   int32_t rank, fmt;
   float scale;
   float xs;              // int8: the row's scale
-  int32_t b;             // its place in the batch
+  int32_t b;             // its place in the batch (-1: none, not stored)
 };
 static_assert(sizeof(RowInfo) == 32, "RowInfo");
 
@@ -456,6 +456,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   const int n0 = ct * C::NC;
 
   // ---- this lane's pieces of a stage: offsets of the rows it loads
+  // (an index past the batch is moved into it for the load; load_info drops its row)
   const u32x4 rx = rsrc_words(m.x, m.x_bytes);
   const u32x4 rw = rsrc_words(W, (uint32_t)(ldw * m.d_out));
   // the resources are written by vector instructions; the assembly that reads
@@ -527,15 +528,17 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     if (t >= C::RT) return;
     const int at = row0 + min(t, rows - 1);
     const int32_t *order = GROUPED ? d.perm : d.order;
-    mine.b = order ? (int)min((unsigned)order[at], (unsigned)(d.num_rows - 1)) : at;
-    if constexpr (C::I8) mine.xs = m.xs[GROUPED ? mine.b / m.rows_per_x : mine.b];
+    const int b = order ? order[at] : at;
+    const bool in = (unsigned)b < (unsigned)d.num_rows;  // a stray index (segments of another batch) touches nothing
+    mine.b = in && t < rows ? b : -1;
+    if constexpr (C::I8) mine.xs = m.xs[in ? (GROUPED ? b / m.rows_per_x : b) : 0];
     mine.a = -1;
     if constexpr (DELTA) {
       // segments come in ascending slot order: later slots were dropped by the
       // build, or their segments do not fit the batch and have no v
       const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
       const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
-      const int a = t < rows ? d.ids[mine.b] : -1;
+      const int a = mine.b >= 0 ? d.ids[mine.b] : -1;
       if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
         const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + m.col];
         if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
@@ -745,7 +748,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
         for (int e = 0; e < C::DT; ++e)
           *(u32x2 *)(at + e * 32) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
-      } else if (r < rows) {
+      } else if (ri.b >= 0) {
         uint16_t *y = m.y + (int64_t)ri.b * m.ldy;
 #pragma unroll
         for (int e = 0; e < C::DT; ++e) {
@@ -762,9 +765,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll 4
     for (int i = 0; i < STEPS; ++i) {
       const int at = i * 64 + lane, lr = at / PPR, piece = at % PPR;
-      const int r = wr * C::MT * 16 + lr, n = nw0 + piece * 8;
+      const int b = info[wr * C::MT * 16 + lr].b, n = nw0 + piece * 8;
       const u32x4 v = *(const u32x4 *)(yw + lr * C::YROW + piece * 16);
-      if (r < rows && n < m.d_out) *(u32x4 *)(m.y + (int64_t)info[r].b * m.ldy + n) = v;
+      if (b >= 0 && n < m.d_out) *(u32x4 *)(m.y + (int64_t)b * m.ldy + n) = v;
     }
   }
 }

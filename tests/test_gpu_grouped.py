@@ -345,3 +345,25 @@ def test_offsets_near_4_gib(int8):
         close(y[b:b + 1], ref, slack, f"row {b}")
     y[keep] = 7.0
     assert bool((y == 7).all())
+
+
+@pytest.mark.parametrize("int8", FORMS)
+@pytest.mark.parametrize("lengths,rows", [((10, 10, 10), 25), ((10, 10, 10), 21), ((5, 1, 40, 9, 30), 60), ((70, 60, 90), 150),
+                                          ((300, 280, 520), 700)])
+def test_rows_past_the_batch_in_segments_that_fit_touch_nothing(int8, lengths, rows):
+    # segments of a longer, shuffled batch: those that end inside this one hold rows past it, which are skipped; no row of
+    # this batch gets another row's result, the last one (and rows past it) included
+    r = Run(int8, ragged(lengths, 4), len(lengths), {"q": (136, 200, "a"), "o": (72, 40, "o")}, seed=19)
+    fit = [s for s in range(len(lengths)) if sum(lengths[:s + 1]) <= rows]
+    assert any((r.ids[rows:] == s).any() for s in fit)  # stray rows are there
+    for io in r.dev.values():
+        io.y.fill_(7.0)
+    lg.build_segments(r.dids, r.slots, r.seg, r.ws)
+    lg.grouped_layer(r.dev, rows, r.table, r.slots, r.seg, r.ws, int8=int8)
+    torch.cuda.synchronize()
+    assert int(r.seg.status.item()) == len(lengths) - len(fit)
+    got = r.out()
+    for m in got:
+        assert bool((got[m][rows:] == 7).all()), m
+    r.ids = np.where(np.arange(r.rows) < rows, r.ids, -1)
+    r.check(got, skip=[s for s in range(len(lengths)) if s not in fit])

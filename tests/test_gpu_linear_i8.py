@@ -424,3 +424,26 @@ def test_workspace_is_not_overrun(rows):
     r.ws = big[:n]
     r.check()
     assert bool((big[n:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("rows,upto", [(100, 70), (40, 30), (300, 200), (700, 400)])
+@pytest.mark.parametrize("bound", [False, True])
+def test_rows_past_the_batch_in_segments_that_fit_touch_nothing(rows, upto, bound):
+    # segments of a longer batch: every row of this one gets its own result or none, the delta only from a segment that
+    # ends inside the batch, and rows past it are left alone
+    r = Run(rows, 5, {"q": (136, 200, "a"), "o": (72, 40, "o")}, 8, "mixed", seed=36, bound=bound)
+    lg.build_segments(r.dids, r.slots, r.seg, r.ws)
+    _, offs, slots, _ = r.seg.host()
+    fit = [int(s) for s, end in zip(slots, offs[1:]) if end <= upto]
+    assert any((r.ids[upto:] == s).any() for s in fit)  # stray rows are there
+    for io in r.dev.values():
+        io.y.fill_(7.0)
+    r.rows = upto
+    lg.linear_layer(*r.args())
+    torch.cuda.synchronize()
+    for m, y in r.out().items():
+        assert bool((y[upto:] == 7).all()), m
+        written = torch.nonzero(~(y[:upto] == 7).all(1))[:, 0].cpu()
+        assert len(written) >= upto // 2
+        ref, slack = r.reference(m, skip=[s for s in range(r.slots) if s not in fit])
+        close(y[written], ref[written], slack[written], m)
