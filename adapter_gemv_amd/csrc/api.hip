@@ -669,7 +669,7 @@ struct QuantInputs {
       return p;
     };
     in.q = static_cast<int8_t *>(take((size_t)rows * in.pitch));
-    in.s = static_cast<float *>(take((size_t)rows * 4));
+    in.amax = static_cast<float *>(take((size_t)rows * 4));
     in.rows_per_block = d_in <= kQuantWaveMax ? 4 : 1;
     in.block_base = d.blocks;
     d.blocks += (int)((rows + in.rows_per_block - 1) / in.rows_per_block);  // at most 7 times the rows of a matrix of 16-byte rows below 4 GiB
@@ -834,7 +834,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       GemmModule &gm = g.mod[i];
       gm.x = in.q;
       gm.ldx = in.pitch;
-      gm.xs = in.s;
+      gm.xs = in.amax;
       gm.x_bytes = (uint32_t)((int64_t)num_rows * in.pitch);
       gm.W = static_cast<const uint8_t *>(la[i].W);
       gm.ldw = la[i].ldw;
@@ -992,7 +992,7 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
       const auto &in = quant.d.in[quant.add(m.x, m.ldx, m.d_in, x_rows, ws)];
       gm.x = in.q;
       gm.ldx = gm.kbytes = in.pitch;
-      gm.xs = in.s;
+      gm.xs = in.amax;
       gm.x_bytes = (uint32_t)(x_rows * in.pitch);
     }
     gm.y = static_cast<uint16_t *>(m.y);

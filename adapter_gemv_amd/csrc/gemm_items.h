@@ -255,9 +255,10 @@ __device__ __forceinline__ int fitting_segments(const int32_t *num_segments, int
 struct RowInfo {
   const uint8_t *B;      // its adapter's B
   int32_t a;             // and slot (-1: none)
-  int32_t rank, fmt;
+  int32_t rank;
+  int16_t fmt, xe;
   float scale;
-  float xs;              // int8: the row's scale
+  float xs;              // int8: the row's scale is xs * 2^xe
   int32_t b;             // its place in the batch (-1: none, not stored)
 };
 static_assert(sizeof(RowInfo) == 32, "RowInfo");
@@ -376,6 +377,17 @@ __device__ __forceinline__ void add_delta(const GemmModule &m, const RowInfo &ri
       }
     }
   }
+}
+
+// Four outputs rounded to bf16: on the largest tile two by one instruction; on
+// the others as pack_bf16x2 does it, in four (there the short form is scheduled
+// so that the rank 64 delta of the 128-row tile spills 26 registers, 646 -> 700
+// us for a whole layer).
+template <class C>
+__device__ __forceinline__ u32x2 pack_out(f32x4_t o) {
+  typedef __bf16 b16x4_t __attribute__((ext_vector_type(4)));
+  if constexpr (C::RT >= 256) return __builtin_bit_cast(u32x2, __builtin_convertvector(o, b16x4_t));
+  else return u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
 }
 
 // KT: 32-wide steps of the ranks of a delta (1: ranks up to 32, 2: up to 64; 0: no delta).
@@ -663,7 +675,13 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   int et0 = 0;  // first column tile this wave finishes
   acc_t fin[C::NTE][C::MT];
   RowInfo *info = reinterpret_cast<RowInfo *>(lds + C::RED);
-  if (t < C::RT) info[t] = mine;
+  if (t < C::RT) {
+    if constexpr (C::I8) {
+      mine.xe = (int16_t)__builtin_amdgcn_frexp_expf(mine.xs);
+      mine.xs = __builtin_amdgcn_frexp_mantf(mine.xs) / 127.f;
+    }
+    info[t] = mine;
+  }
   if constexpr (C::WK > 1) {
     acc_t *red = reinterpret_cast<acc_t *>(lds);
     const int grp = w % (C::WR * C::WC);
@@ -694,6 +712,11 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   }
 
   // ---- scales, delta, rounding, store: DT column tiles at a time
+  // int8: (sum * s) * Ws with the power of two of s apart and last.  With it a
+  // finite result may pass the ends of fp32 on the way (a sum of 2^31 times a row
+  // scale of 2^121, a scale of 2^-140); without it sum * s lies between 2^-8 and
+  // 2^24, and the three roundings are the same.  The output's power of two apart
+  // as well cost the prefills 2.5% (4465 -> 4575 us).
   uint8_t *yw = lds + C::RED + 32 * C::RT + w * C::YWAVE;
   (void)yw;
 #pragma unroll
@@ -718,7 +741,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       for (int e = 0; e < C::DT; ++e) {
         if constexpr (C::I8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) out[e][i] = (float)fin[e0 + e][mt][i] * ri.xs * sw[e][i];
+          for (int i = 0; i < 4; ++i) out[e][i] = ldexpf((float)fin[e0 + e][mt][i] * ri.xs * sw[e][i], ri.xe);
         } else {
           out[e] = fin[e0 + e][mt];
         }
@@ -747,14 +770,14 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         uint8_t *at = yw + (mt * 16 + r_in) * C::YROW + e0 * 32 + g * 8;
 #pragma unroll
         for (int e = 0; e < C::DT; ++e)
-          *(u32x2 *)(at + e * 32) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
+          *(u32x2 *)(at + e * 32) = pack_out<C>(out[e]);
       } else if (ri.b >= 0) {
         uint16_t *y = m.y + (int64_t)ri.b * m.ldy;
 #pragma unroll
         for (int e = 0; e < C::DT; ++e) {
           const int n = nw0 + e * 16 + g * 4;
           if (n < m.d_out)
-            *(u32x2 *)(y + n) = u32x2{pack_bf16x2(out[e][0], out[e][1]), pack_bf16x2(out[e][2], out[e][3])};
+            *(u32x2 *)(y + n) = pack_out<C>(out[e]);
         }
       }
     }
@@ -773,8 +796,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 }
 
 // Rows of x as int8 with one scale each: s = max|x| / 127, q = rint(127 x /
-// max|x|), halves to even.  A
-// zero row: q = 0, s = 0.  A row with an infinity or a NaN: s = NaN (its
+// max|x|), halves to even; what is kept of s is max|x| (the division, by the
+// product, is of its significand: s itself may be below the normal numbers).  A
+// zero row: q = 0, s = 0.  A row with an infinity or a NaN: NaN for max|x| (its
 // outputs are NaN), q = 0.  [d_in, pitch) gets 0.  36534 rows of 8192, two
 // inputs: 1.8 GB in 300 us, 6 TB/s.
 constexpr int kQuantRegs = 4;
@@ -882,7 +906,7 @@ __device__ __forceinline__ void quantize_row(const QuantInput &in, int row, int 
     *(u32x2 *)(q + (int64_t)p * 8) = live ? quant8(*(const u32x4 *)(x + (int64_t)p * 8), qs) : u32x2{0u, 0u};
   if (t == 0) {
     if (in.d_in < in.pitch) *(u32x2 *)(q + in.d_in) = u32x2{0u, 0u};  // the row's last half piece
-    in.s[row] = bad ? __int_as_float(0x7fc00000) : mx / 127.f;
+    in.amax[row] = bad ? __int_as_float(0x7fc00000) : mx;
   }
 }
 

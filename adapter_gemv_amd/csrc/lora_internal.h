@@ -179,7 +179,7 @@ hipError_t launch_onepass(const OnePassDesc &d, int grid, hipStream_t stream);
 struct GemmModule {
   const void *x;        // bf16 or int8 rows
   int64_t ldx;          // bytes
-  const float *xs;      // int8: scale of each row of x
+  const float *xs;      // int8: largest magnitude of each row of x (127 times its scale)
   const uint8_t *W;     // base weight [d_out] rows (not grouped)
   int64_t ldw;          // bytes
   const float *Ws;      // int8: scale of each output
@@ -221,7 +221,7 @@ struct QuantInput {
   const uint16_t *x;
   int64_t ldx;       // elements
   int8_t *q;
-  float *s;
+  float *amax;       // of each row; NaN: the row holds a NaN or an infinity
   int32_t d_in;
   int32_t pitch;     // bytes of a row of q, a multiple of 16
   int32_t rows;

@@ -520,7 +520,9 @@ typedef struct lora_linear_i8_io {
   const void *Wq; /* device, int8 [d_out][ldwq]                              */
   int64_t ldwq;   /* bytes per row: >= d_in rounded up to a multiple of 16,
                      a multiple of 16; bytes [d_in, ldwq) contribute nothing */
-  const void *Ws; /* device, fp32 [d_out]: the scale of each output          */
+  const void *Ws; /* device, fp32 [d_out]: the scale of each output; 0, or a
+                     magnitude from 2^-118 to 2^102 (beyond: y may lose
+                     precision or become infinite before it must)            */
   void *y;        /* device, bf16 [num_rows][ldy]: written, W.x + delta      */
   int64_t ldy;
   int32_t d_in;   /* up to LORA_I8_MAX_IN                                    */
@@ -604,8 +606,8 @@ lora_status_t lora_linear_expand_i8(const lora_linear_i8_io_t *io, uint32_t modu
  *        int8 [d_out][ldw] (lora_grouped_layer_i8; bytes [d_in, ldw) of a row
  *        contribute nothing).  NULL: the slot has no weight for the
  *        projection, and its rows of y are left as they are.
- *   Ws   int8: device fp32 [d_out], 16-byte aligned, the scale of each output;
- *        bf16: not read.
+ *   Ws   int8: device fp32 [d_out], 16-byte aligned, the scale of each output
+ *        (range as in lora_linear_i8_io_t); bf16: not read.
  *   ldw  elements per row: bf16 >= d_in and a multiple of 8, int8 >= d_in
  *        rounded up to a multiple of 16 and a multiple of 16.  A weight stays
  *        below 4 GiB.

@@ -109,3 +109,44 @@ def ids_of(kind, n, slots, seed):
         ids[r.rand(n) < 0.15] = -1
         ids[r.rand(n) < 0.05] = slots + 3
     return ids.astype(np.int32)
+
+
+def close_range(got, ref, rel, what):
+    """got (bf16 values) against ref (fp64) over the whole range of the type: |got - ref| <= (2^-8 + rel) |ref| plus half
+    a step of the smallest values (2^-134, and 2^-150 where fp32 rounds one to its own); infinite where ref rounds past
+    the largest value, NaN where ref is."""
+    got = got.double().cpu()
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    nan = torch.isnan(ref)
+    assert torch.equal(torch.isnan(got), nan), f"{what}: NaN in other places"
+    got, ref = got[~nan], ref[~nan]
+    edge = 2.0 ** 128 - 2.0 ** 119  # half a step above the largest value
+    over = ref.abs() > edge * (1 + rel)
+    assert torch.equal(got[over], ref[over].sign() * float("inf")), f"{what}: not infinite past the type"
+    sure = ref.abs() < edge * (1 - rel)
+    err, tol = (got - ref)[sure].abs(), (BF + rel) * ref[sure].abs() + 2.0 ** -134 + 2.0 ** -150
+    bad = int((~(err <= tol)).sum())
+    assert bad == 0, f"{what}: {bad} of {err.numel()} out of tolerance; largest error {float(err.max())}"
+
+
+def extreme_rows(d):
+    """[12, d] bf16 rows at both ends of the type, every value finite."""
+    ramp = torch.linspace(-1, 1, d).double()
+    top, low = 3e38, 2.0 ** -133  # near the largest value; the smallest of all
+    one = torch.zeros(d).double()
+    one[d // 3] = 1.0
+    rows = [ramp * top, ramp * 1e36, ramp * 1e30, one * top, ramp, torch.zeros(d).double(), ramp * 1e-30, ramp * 1e-38,
+            ramp * 2.0 ** -126, ramp * 2.0 ** -129, one * low, -one * low * 3]
+    x = torch.stack(rows).to(torch.bfloat16)
+    assert bool(torch.isfinite(x).all()) and float(x[0].abs().max()) > 2.9e38 and float(x[10].abs().max()) == low
+    return x
+
+
+def extreme_scales(Ws):
+    """The scales of the outputs by powers of two, exactly, so that products of either end meet scales of the other:
+    a quarter of the outputs each at 1, 2^60, 2^-60 and (half of them) 2^110 or 2^-110."""
+    n = Ws.numel()
+    e = torch.tensor([0, 60, -60, 110, 0, 60, -60, -110])[torch.arange(n) % 8]
+    out = torch.ldexp(Ws, e)
+    assert bool(torch.isfinite(out).all()) and bool((out.abs() > 2.0 ** -126).all())
+    return out

@@ -3,7 +3,8 @@ lora_grouped_layer_i8) against the 64-bit definition."""
 import numpy as np
 import pytest
 
-from tests.dense_cases import MODS, base_i8, bf16, close, gen, grouped_bf16, ids_of, int8_weight
+from tests.dense_cases import (MODS, U, base_i8, bf16, close, close_range, extreme_rows, extreme_scales, gen, grouped_bf16,
+                               ids_of, int8_weight)
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -367,3 +368,20 @@ def test_rows_past_the_batch_in_segments_that_fit_touch_nothing(int8, lengths, r
         assert bool((got[m][rows:] == 7).all()), m
     r.ids = np.where(np.arange(r.rows) < rows, r.ids, -1)
     r.check(got, skip=[s for s in range(len(lengths)) if s not in fit])
+
+
+def test_rows_and_scales_at_the_ends_of_the_type():
+    # int8: the row scale and the output scale multiply a sum of 2^23 without leaving the type on the way (four
+    # roundings); every row once under each of two slots
+    d = 264
+    ids = np.arange(24) % 2
+    r = Run(True, ids, 2, {"q": (d, 64, "a")}, fan=2, seed=18)
+    x = extreme_rows(d)
+    r.dev["q"].x.copy_(x)
+    for s in (0, 1):
+        r.cpu["q"]["Ws"][s] = extreme_scales(r.cpu["q"]["Ws"][s])
+        r.keep["q", s][1].copy_(r.cpu["q"]["Ws"][s])
+    got = r.run()["q"]
+    for s in (0, 1):
+        ref, _ = base_i8(x, r.cpu["q"]["W"][s], r.cpu["q"]["Ws"][s])
+        close_range(got[s::2], ref, 4 * U, f"slot {s}")

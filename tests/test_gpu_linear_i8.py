@@ -3,7 +3,8 @@
 import numpy as np
 import pytest
 
-from tests.dense_cases import MODS, base_i8, bf16, close, delta, gen, ids_of, int8_weight, quantise_rows
+from tests.dense_cases import (MODS, U, base_i8, bf16, close, close_range, delta, extreme_rows, extreme_scales, gen, ids_of,
+                               int8_weight, quantise_rows)
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -447,3 +448,32 @@ def test_rows_past_the_batch_in_segments_that_fit_touch_nothing(rows, upto, boun
         assert len(written) >= upto // 2
         ref, slack = r.reference(m, skip=[s for s in range(r.slots) if s not in fit])
         close(y[written], ref[written], slack[written], m)
+
+
+def test_rows_and_scales_at_the_ends_of_the_type():
+    # sums of 2^23 under row scales from 2^-140 to 2^121 and output scales from 2^-121 to 2^98: finite wherever the
+    # definition is (the smallest scales lie below the documented range, where sums as large as these are still safe).
+    # The base rounds four times: 4 u (extreme_rows and _scales hold no value that is not exact)
+    d = 264
+    r = Run(12, 1, {"q": (d, 64, "a")}, 8, "none", seed=1)
+    c = r.cpu["q"]
+    c["x"], c["Ws"] = extreme_rows(d), extreme_scales(c["Ws"])
+    r.dev["q"].x, r.dev["q"].Ws = c["x"].cuda(), c["Ws"].cuda()
+    ref, _ = r.reference("q")
+    assert int((ref.abs() < 2.0 ** 127).sum()) > ref.numel() // 2 and int((ref.abs() > 2.0 ** 100).sum()) > 100
+    close_range(r.run()["q"], ref, 4 * U, "q")
+
+
+@pytest.mark.parametrize("rows", [40, 200])
+def test_non_finite_rows_among_rows_with_adapters(rows):
+    r = Run(rows, 3, {"q": (264, 136, "a")}, (16, 64, 5), "mixed", seed=9)
+    x = r.cpu["q"]["x"].clone()
+    sick = [3, 9, 20, rows - 1]
+    for b, v in zip(sick, ("inf", "nan", "-inf", "nan")):
+        x[b, 17 + b] = float(v)
+    assert sum(r.ids[b] in (0, 1, 2) for b in sick) >= 2
+    r.cpu["q"]["x"] = x
+    r.dev["q"].x = x.cuda()
+    got = r.run()
+    r.check(got)
+    assert set(torch.nonzero(torch.isnan(got["q"]).any(1))[:, 0].tolist()) == set(sick)
