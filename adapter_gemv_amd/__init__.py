@@ -196,21 +196,29 @@ def _stream(stream):
     return _raw_stream()
 
 
-def _rows(t, dtype, rows, dev, name, field):
+def _rows(t, dtype, rows, cols, dev, name, field):
     """(address, row stride) of a matrix on device `dev` with unit stride along
-    its rows and at least `rows` of them; the checks of _need, in few steps
-    for the ordinary case (a decode call marshals up to 28 tensors)."""
+    its rows, at least `rows` of them and `cols` wide; the checks of _need, in
+    few steps for the ordinary case (a decode call marshals up to 28 tensors)."""
     try:
-        n, st = t.size(0), t.stride()
-        if t.dtype is dtype and t.get_device() == dev and n >= rows and len(st) == 2 and (st[1] == 1 or t.size(1) <= 1):
+        (n, c), (ld, unit) = t.size(), t.stride()
+        if t.dtype is dtype and t.get_device() == dev and n >= rows and c >= cols and (unit == 1 or c <= 1):
             # a single row's stride has no meaning: torch may give any
-            return t.data_ptr(), st[0] if n > 1 else -(-t.size(1) // 16) * 16
-    except (AttributeError, IndexError):
+            return t.data_ptr(), ld if n > 1 else -(-c // 16) * 16
+    except (AttributeError, TypeError, ValueError):
         pass
     _need(t, dtype, f"{name}.{field}", 2)
     if t.get_device() != dev:
         raise ValueError(f"{name}.{field} is on another device than the rest of the call")
-    raise ValueError(f"{name}.{field}: fewer than {rows} rows")
+    if t.shape[0] < rows:
+        raise ValueError(f"{name}.{field}: fewer than {rows} rows")
+    raise ValueError(f"{name}.{field}: fewer than {cols} columns")
+
+
+def _slot_table(t, num_slots, what):
+    """The device table of num_slots * 7 entries of 32 bytes, whole and in one piece."""
+    if t.numel() * t.element_size() < num_slots * (len(MODULES) * 32) or not t.is_contiguous():
+        raise ValueError(f"{what}: not the {num_slots} x {len(MODULES)} contiguous entries of 32 bytes that the call reads")
 
 
 def _ptr(t):
@@ -372,9 +380,9 @@ def _linear_i8_array(ios, num_rows, row_adapter, rest):
             raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every "
                             "projection LinearI8IO")
         Ws, d_out = io.Ws, io.d_out
-        xp, ldx = _rows(io.x, bf16, num_rows, dev, name, "x")
-        yp, ldy = _rows(io.y, bf16, num_rows, dev, name, "y")
-        wp, ldw = _rows(io.Wq, i8, d_out, dev, name, "Wq")
+        xp, ldx = _rows(io.x, bf16, num_rows, io.d_in, dev, name, "x")
+        yp, ldy = _rows(io.y, bf16, num_rows, d_out, dev, name, "y")
+        wp, ldw = _rows(io.Wq, i8, d_out, io.d_in, dev, name, "Wq")
         if Ws.dtype is not f32 or Ws.get_device() != dev or Ws.stride() != (1,):
             _need(Ws, f32, f"{name}.Ws", 1)
             _one_device(dev, (Ws,), name)
@@ -404,6 +412,7 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
         kind = next((k for k in _LINEAR_KINDS if any(isinstance(io, k) for io in ios.values())), LinearIO)
     cstruct, suffix = _LINEAR_KINDS[kind]
     if kind is LinearI8IO:
+        _slot_table(table, num_slots, "table")
         arr, mask = _linear_i8_array(ios, num_rows, row_adapter, (table, ws, seg.perm))
         _fn += suffix
         _check(getattr(lib(), _fn)(arr, mask if module_mask is None else module_mask, num_rows, _ptr(row_adapter),
@@ -504,6 +513,7 @@ def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, 
     dev = weights.get_device()
     if dev < 0:
         raise ValueError("weights must be on the GPU")
+    _slot_table(weights, num_slots, "weights")
     for i, name in enumerate(MODULES):
         io = ios.get(name)
         if io is None:
@@ -511,8 +521,8 @@ def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, 
         fan = io.rows_per_x
         if fan < 1:
             raise ValueError(f"{name}: rows_per_x must be >= 1")
-        xp, ldx = _rows(io.x, bf16, -(-num_rows // fan), dev, name, "x")
-        yp, ldy = _rows(io.y, bf16, num_rows, dev, name, "y")
+        xp, ldx = _rows(io.x, bf16, -(-num_rows // fan), io.d_in, dev, name, "x")
+        yp, ldy = _rows(io.y, bf16, num_rows, io.d_out, dev, name, "y")
         _GROUPED_PACK.pack_into(arr, i * _GROUPED_PACK.size, xp, ldx, yp, ldy, io.d_in, io.d_out, fan, 0)
         mask |= 1 << i
     if module_mask is not None:

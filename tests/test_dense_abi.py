@@ -128,3 +128,58 @@ def test_binding_checks_its_arguments():
         lg.grouped_layer({"q": io}, 4, x, 1, None)
     with pytest.raises(TypeError):
         lg.linear_layer({"q": lg.LinearI8IO(x, x, x, x), "k": lg.LinearIO(x, x, x)}, 4, x, x, 1, None, 8, x)
+
+
+def _on_gpu(*shape, dtype="bfloat16"):
+    """A CPU tensor that says it is on GPU 0: for checks that end before the device is touched."""
+    torch = pytest.importorskip("torch")
+
+    class OnGpu(torch.Tensor):
+        is_cuda = property(lambda self: True)
+
+        def get_device(self):
+            return 0
+
+    return torch.zeros(*shape, dtype=getattr(torch, dtype)).as_subclass(OnGpu)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("x,y,table,d_in,d_out,fan,what", [
+    ((4, 16), (4, 16), 2 * 7 * 32, 16, 16, 1, "weights: not the 3 x 7"),    # one slot short
+    ((4, 16), (4, 16), 3 * 7 * 32 - 1, 16, 16, 1, "weights: not the 3 x 7"),
+    ((4, 16), (4, 16), 0, 16, 16, 1, "weights: not the 3 x 7"),
+    ((4, 16), (4, 16), 3 * 7 * 32, 24, 16, 1, "q.x: fewer than 24 columns"),
+    ((1, 8), (4, 16), 3 * 7 * 32, 16, 16, 4, "q.x: fewer than 16 columns"),  # a single row: its stride says nothing
+    ((4, 16), (4, 16), 3 * 7 * 32, 16, 24, 1, "q.y: fewer than 24 columns"),
+    ((3, 16), (4, 16), 3 * 7 * 32, 16, 16, 1, "q.x: fewer than 4 rows"),
+    ((1, 16), (4, 16), 3 * 7 * 32, 16, 16, 2, "q.x: fewer than 2 rows"),
+    ((4, 16), (3, 16), 3 * 7 * 32, 16, 16, 1, "q.y: fewer than 4 rows"),
+])
+def test_grouped_layer_refuses_short_tables_and_matrices(int8, x, y, table, d_in, d_out, fan, what):
+    io = lg.GroupedIO(_on_gpu(*x), _on_gpu(*y), d_in=d_in, d_out=d_out, rows_per_x=fan)
+    with pytest.raises(ValueError, match=what):
+        lg.grouped_layer({"q": io}, 4, _on_gpu(table, dtype="uint8"), 3, None, int8=int8)
+
+
+@pytest.mark.parametrize("x,w,y,table,d_in,d_out,what", [
+    ((4, 16), (16, 16), (4, 16), 2 * 7 * 32, 16, 16, "table: not the 3 x 7"),
+    ((4, 16), (16, 16), (4, 16), 3 * 7 * 32, 24, 16, "q.x: fewer than 24 columns"),
+    ((4, 32), (16, 16), (4, 16), 3 * 7 * 32, 24, 16, "q.Wq: fewer than 24 columns"),
+    ((4, 16), (16, 16), (4, 16), 3 * 7 * 32, 16, 24, "q.y: fewer than 24 columns"),
+    ((4, 16), (16, 16), (4, 24), 3 * 7 * 32, 16, 24, "q.Wq: fewer than 24 rows"),
+    ((3, 16), (16, 16), (4, 16), 3 * 7 * 32, 16, 16, "q.x: fewer than 4 rows"),
+])
+def test_linear_layer_i8_refuses_short_tables_and_matrices(x, w, y, table, d_in, d_out, what):
+    io = lg.LinearI8IO(_on_gpu(*x), _on_gpu(*w, dtype="int8"), _on_gpu(w[0], dtype="float32"), _on_gpu(*y), d_in=d_in,
+                       d_out=d_out)
+    seg = type("Seg", (), {"perm": None})()
+    with pytest.raises(ValueError, match=what):
+        lg.linear_layer({"q": io}, 4, _on_gpu(4, dtype="int32"), _on_gpu(table, dtype="uint8"), 3, seg, 8,
+                        _on_gpu(64, dtype="uint8"))
+
+
+def test_tables_in_pieces_are_refused():
+    wide = _on_gpu(3 * 7, 64, dtype="uint8")[:, :32]
+    x = _on_gpu(4, 16)
+    with pytest.raises(ValueError, match="weights: not the 3 x 7"):
+        lg.grouped_layer({"q": lg.GroupedIO(x, x)}, 4, wide, 3, None)
