@@ -407,9 +407,8 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
     if type(row_adapter) is not torch.Tensor or row_adapter.dtype is not torch.int32 or not row_adapter.is_cuda or \
             row_adapter.stride() != (1,):
         _need(row_adapter, torch.int32, "row_adapter", 1)
-    kind = type(next(iter(ios.values()))) if ios else LinearIO
-    if kind not in _LINEAR_KINDS:
-        kind = next((k for k in _LINEAR_KINDS if any(isinstance(io, k) for io in ios.values())), LinearIO)
+    # any object with its attributes is a bf16 projection, as for the other layer calls
+    kind = next((k for k in (LinearQ4IO, LinearI8IO) if any(isinstance(io, k) for io in ios.values())), LinearIO)
     cstruct, suffix = _LINEAR_KINDS[kind]
     if kind is LinearI8IO:
         _slot_table(table, num_slots, "table")
@@ -425,7 +424,7 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
         io = ios.get(name)
         if io is None:
             continue
-        if not isinstance(io, kind):
+        if kind is not LinearIO and not isinstance(io, kind):
             raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every "
                             "projection LinearI8IO")
         for t, what in ((io.x, "x"), (io.y, "y")) + (((io.W, "W"),) if kind is LinearIO else ()):

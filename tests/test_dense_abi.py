@@ -183,3 +183,37 @@ def test_tables_in_pieces_are_refused():
     x = _on_gpu(4, 16)
     with pytest.raises(ValueError, match="weights: not the 3 x 7"):
         lg.grouped_layer({"q": lg.GroupedIO(x, x)}, 4, wide, 3, None)
+
+
+class _LikeLinear:
+    def __init__(self, **kw):
+        self.__dict__.update(kw)
+
+
+def _linear_call(ios):
+    held = type("Seg", (), {"perm": _on_gpu(4, dtype="int32"), "c": lambda self: seg()})()
+    lg.linear_layer(ios, 4, _on_gpu(4, dtype="int32"), _on_gpu(7 * 32, dtype="uint8"), 1, held, 8, _on_gpu(16, dtype="uint8"),
+                    stream=_LikeLinear(cuda_stream=0))
+
+
+def test_any_object_with_the_attributes_is_a_bf16_projection():
+    # it gets as far as the library's own check of the workspace (host only)
+    x, W = _on_gpu(4, 16), _on_gpu(16, 16)
+    like = _LikeLinear(x=x, W=W, y=x, d_in=16, d_out=16)
+    sub = type("Sub", (lg.LinearIO,), {})(x, W, x)
+    for ios in ({"q": like}, {"q": sub}, {"q": lg.LinearIO(x, W, x), "k": like}, {"q": like, "k": lg.LinearIO(x, W, x)},
+                {"q": None, "k": like}):
+        with pytest.raises(lg.LoraError, match="WORKSPACE"):
+            _linear_call(ios)
+
+
+def test_projections_of_two_kinds_are_refused():
+    x, W, q = _on_gpu(4, 128), _on_gpu(128, 128), _on_gpu(128, 64, dtype="uint8")
+    s = _on_gpu(128, 1, dtype="float32")
+    kinds = [_LikeLinear(x=x, W=W, y=x, d_in=128, d_out=128), lg.LinearIO(x, W, x), lg.LinearQ4IO(x, q, s, x),
+             lg.LinearI8IO(x, _on_gpu(128, 128, dtype="int8"), _on_gpu(128, dtype="float32"), x)]
+    for i, a in enumerate(kinds):
+        for j, b in enumerate(kinds):
+            if i != j and max(i, j) >= 2:
+                with pytest.raises(TypeError, match="every projection"):
+                    _linear_call({"q": a, "k": b})
