@@ -813,10 +813,12 @@ __device__ __forceinline__ float abs_max8(u32x4 p, float m, bool *bad) {
 }
 // rint(127 x / amax) for 8 values without a division each: x scaled by amax's
 // power of two, times 127 over the rest of amax (one division a row), is within
-// 2 units of the last place of the real quotient.  With 8-bit significands that
-// quotient is a tie or at least 1 / (127 * 255) of itself, 2^8 units, away from
-// one, so rounded to a multiple of 64 units it is exact on a tie and stays on
-// its side otherwise.
+// 2 units of the last place of the real quotient.  With significands of 8 bits,
+// X 2^-k of x beside a of amax, the quotient is
+// |254 X - (2j + 1) a 2^k| / (2 a 2^k) from the tie j + 1/2: on it, or at least
+// 1 / (510 * 2^k) away, 2^8 units of a quotient below 128 / 2^k (the nearest is
+// X = 254 beside a = 255).  Rounded to a multiple of 64 units it is exact on a
+// tie and stays on its side otherwise.
 struct QuantScale {
   int exp;
   float r;

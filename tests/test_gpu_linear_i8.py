@@ -477,3 +477,27 @@ def test_non_finite_rows_among_rows_with_adapters(rows):
     got = r.run()
     r.check(got)
     assert set(torch.nonzero(torch.isnan(got["q"]).any(1))[:, 0].tolist()) == set(sick)
+
+
+@pytest.mark.parametrize("copies", [8, 24, 64])
+def test_quantiser_over_the_significands_of_amaxs_own_power_of_two(copies):
+    # row a: amax with significand 128 + a and every significand up to it at its own power of two (q from 64 to 127, where
+    # a quotient comes nearest to a tie: 254 beside 255); W is the identity.  8 copies: a wave a row; 24: past its
+    # registers; 64: a block a row and past its registers
+    sig = torch.arange(128, 256).double()
+    x = torch.stack([torch.where(sig <= a, sig, torch.zeros(128).double()) * (1 if a % 2 else -1) for a in range(128, 256)])
+    x = torch.cat([x, sig[:, None], torch.zeros(128, 7).double()], 1)            # 136 inputs, the largest is a
+    d = x.shape[1]
+    r = Run(128, 1, {"q": (d * copies, d, "a")}, 8, "none", seed=7)
+    xb = x.repeat(1, copies).to(torch.bfloat16)
+    assert torch.equal(xb[:, :d].double(), x)                                    # every value is a bf16
+    r.cpu["q"]["x"] = xb
+    r.dev["q"].x = xb.cuda()
+    W = torch.zeros(d, -(-d * copies // 16) * 16, dtype=torch.int8)
+    W[torch.arange(d), torch.arange(d) + d * (copies - 1)] = 1                   # the last copy
+    r.dev["q"].Wq.copy_(W)
+    r.dev["q"].Ws.fill_(1.0)
+    got = r.run()["q"].cpu()
+    amax = x.abs().amax(1, keepdim=True)
+    want = (torch.round(127.0 * x / amax).float() * (amax.float() / 127.0)).to(torch.bfloat16)
+    assert torch.equal(got, want)
