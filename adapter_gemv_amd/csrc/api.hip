@@ -704,7 +704,7 @@ double row_tiles_expected(int64_t rows, int64_t groups, int t) {
   return (double)groups * (1 + std::max(0.0, 0.5 - (t - per) / (3.4 * spread)));
 }
 
-int pick_gemm(int64_t rows, int64_t groups, int adapters, const GemmModule *m, int n) {
+int pick_gemm(int64_t rows, int64_t groups, int adapters, const GemmModule *m, int n, double *expected_us) {
   const int64_t per = (rows + groups - 1) / groups;
   int fit = 0;
   while (fit + 1 < kGemmTiles && gemm_tile(fit).rows < per) ++fit;
@@ -730,7 +730,23 @@ int pick_gemm(int64_t rows, int64_t groups, int adapters, const GemmModule *m, i
       least = us;
     }
   }
+  if (expected_us) *expected_us = least;
   return best;
+}
+
+// The rows of an int8 layer call are multiplied in the order of their slots
+// (kOrderRows; a stated bound of nearly a segment per row: nothing to gather).
+bool rows_by_slot(int num_rows, const lora_segments_t &seg) {
+  return num_rows >= kOrderRows && (seg.max_segments == 0 || 2 * (int64_t)num_rows >= 3 * (int64_t)seg.max_segments);
+}
+
+// The tile of a call; adapters among 16 rows: by slot, those that meet there.
+int tile_of_call(GemmKind kind, int num_rows, int num_slots, const lora_segments_t &seg, const GemmModule *m, int n,
+                 double *expected_us = nullptr) {
+  const int segs = segment_bound(num_rows, num_slots, seg);
+  if (kind != kLinearI8) return pick_gemm(num_rows, segs, 0, m, n, expected_us);
+  const int adapters = rows_by_slot(num_rows, seg) ? (int)std::min<int64_t>(segs, 1 + 16 * (int64_t)segs / num_rows) : segs;
+  return pick_gemm(num_rows, 1, adapters, m, n, expected_us);
 }
 
 // Number the blocks of n projections (g.mod[0..n), longest d_in first: a
@@ -808,9 +824,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
   int32_t *by_slot = nullptr;
   if constexpr (kI8) {  // the rows by slot and the int8 rows of x, behind the v planes
     char *behind = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
-    // (a stated bound of nearly a segment per row: nothing to gather)
-    const bool shared = seg.max_segments == 0 || 2 * (int64_t)num_rows >= 3 * (int64_t)seg.max_segments;
-    if (num_rows >= kOrderRows && shared) by_slot = reinterpret_cast<int32_t *>(behind);
+    if (rows_by_slot(num_rows, seg)) by_slot = reinterpret_cast<int32_t *>(behind);
     void *qws = behind + order_ws_bytes(num_rows);
     for (int i = 0; i < n; ++i) quant_of[i] = quant.add(la[i].x, la[i].ldx, la[i].d_in, num_rows, qws);
   }
@@ -848,9 +862,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       gm.col = ms[i].col;
       gm.rows_per_x = 1;
     }
-    const int segs = segment_bound(num_rows, num_slots, seg);  // adapters among 16 rows: in order, those that meet there
-    const int cfg = pick_gemm(num_rows, 1, by_slot ? (int)std::min<int64_t>(segs, 1 + 16 * (int64_t)segs / num_rows) : segs,
-                              g.mod, n);
+    const int cfg = tile_of_call(kLinearI8, num_rows, num_slots, seg, g.mod, n);
     g.row_tiles = (num_rows + gemm_tile(cfg).rows - 1) / gemm_tile(cfg).rows;
     g.rs = rs;
     g.max_rank = max_rank;
@@ -1016,15 +1028,30 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
     if (st != LORA_OK) return st;
   }
   g.weights = weights;
-  const int groups = segment_bound(num_rows, num_slots, seg);
-  const int cfg = pick_gemm(num_rows, groups, 0, g.mod, n);
+  const GemmKind kind = i8 ? kGroupedI8 : kGroupedBf16;
+  const int cfg = tile_of_call(kind, num_rows, num_slots, seg, g.mod, n);
   const int rt = gemm_tile(cfg).rows;
   // every segment's last tile may be partial
-  const int64_t row_tiles = std::min<int64_t>(num_rows, (int64_t)num_rows / rt + groups);
-  return gemm_launch(g, n, row_tiles, num_rows, num_slots, seg, i8 ? kGroupedI8 : kGroupedBf16, cfg, s);
+  const int64_t row_tiles = std::min<int64_t>(num_rows, (int64_t)num_rows / rt + segment_bound(num_rows, num_slots, seg));
+  return gemm_launch(g, n, row_tiles, num_rows, num_slots, seg, kind, cfg, s);
 }
 
 }  // namespace
+
+extern "C" int32_t lora_internal_gemm_tile(int32_t kind, int32_t num_rows, int32_t num_slots, lora_segments_t seg,
+                                           const int32_t *d_in, const int32_t *d_out, int32_t n, int32_t *rows,
+                                           int32_t *cols, double *expected_us) {
+  if (kind < kLinearI8 || kind > kGroupedI8 || num_rows < 1 || num_slots < 1 || n < 1 || n > kMaxModules) return -1;
+  GemmModule m[kMaxModules] = {};
+  for (int i = 0; i < n; ++i) {
+    m[i].kbytes = kind == kGroupedBf16 ? d_in[i] * 2 : i8_pitch(d_in[i]);
+    m[i].d_out = d_out[i];
+  }
+  const int cfg = tile_of_call((GemmKind)kind, num_rows, num_slots, seg, m, n, expected_us);
+  *rows = gemm_tile(cfg).rows;
+  *cols = gemm_tile(cfg).cols;
+  return cfg;
+}
 
 extern "C" {
 

@@ -245,6 +245,13 @@ struct GemmTile {
 };
 constexpr int kGemmTiles = 6;
 GemmTile gemm_tile(int cfg);
+// Not part of the C ABI: the tile that a call of `kind` (GemmKind) with n
+// projections of these widths takes, its rows and columns and the time that
+// the account behind the choice expects (us).  The tests of the products ask
+// it, so that each tile has a test that runs it.  -1: bad arguments.
+extern "C" int32_t lora_internal_gemm_tile(int32_t kind, int32_t num_rows, int32_t num_slots, lora_segments_t seg,
+                                           const int32_t *d_in, const int32_t *d_out, int32_t n, int32_t *rows,
+                                           int32_t *cols, double *expected_us);
 hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
 hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream);
 // The same, launch_shrink_reduce of d, and (order not null) the rows by slot

@@ -150,3 +150,35 @@ def extreme_scales(Ws):
     out = torch.ldexp(Ws, e)
     assert bool(torch.isfinite(out).all()) and bool((out.abs() > 2.0 ** -126).all())
     return out
+
+
+# The tile (rows, columns) of a product and a batch that takes it: more than one row tile and column tile, the last of
+# each partial, and enough of k that every place of the tile's ring is filled again.
+LINEAR_TILES = [((16, 64), 37, 2056, 264), ((32, 64), 260, 1032, 1032), ((64, 64), 100, 1032, 4104),
+                ((128, 96), 520, 1032, 4104), ((128, 128), 260, 1032, 8200), ((256, 256), 520, 1032, 16392),
+                ((256, 256), 1030, 2056, 8200)]
+GROUPED_TILES = [((16, 64), (21, 1, 15), 2056, 264), ((32, 64), (100, 31, 129), 1032, 1032),
+                 ((64, 64), (100, 31, 129), 1032, 2056), ((128, 96), (127, 4, 129), 1032, 6152),
+                 ((128, 128), (127, 4, 129), 1032, 8200), ((256, 256), (300, 1, 219), 1032, 12296),
+                 ((256, 256), (0, 1030, 600), 2056, 8200)]
+LINEAR_SLOTS = 5
+
+
+def tile_of(kind, rows, slots, shapes, max_segments=0):
+    """(rows, columns) of the tile that the library takes for a call of `kind` ("linear_i8", "grouped" or "grouped_i8") with
+    these (d_in, d_out)."""
+    import ctypes
+
+    import adapter_gemv_amd as lg
+    n = len(shapes)
+    ints = ctypes.c_int32 * n
+    seg = lg._Seg()
+    seg.max_segments = max_segments
+    f = lg.lib().lora_internal_gemm_tile
+    f.restype = ctypes.c_int32
+    rt, ct, us = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_double()
+    got = f(ctypes.c_int32(["linear_i8", "grouped", "grouped_i8"].index(kind)), ctypes.c_int32(rows), ctypes.c_int32(slots),
+            seg, ints(*[s[0] for s in shapes]), ints(*[s[1] for s in shapes]), ctypes.c_int32(n), ctypes.byref(rt),
+            ctypes.byref(ct), ctypes.byref(us))
+    assert got >= 0
+    return rt.value, ct.value

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 import adapter_gemv_amd as lg
+from tests.dense_cases import GROUPED_TILES, LINEAR_SLOTS, LINEAR_TILES, tile_of
 
 OK, NULL, SHAPE, RANK, ALIGN, WS, MODULE = range(7)
 P = 0x10000
@@ -217,3 +218,22 @@ def test_projections_of_two_kinds_are_refused():
             if i != j and max(i, j) >= 2:
                 with pytest.raises(TypeError, match="every projection"):
                     _linear_call({"q": a, "k": b})
+
+
+@pytest.mark.parametrize("tile,rows,d_in,d_out", LINEAR_TILES)
+def test_int8_base_batches_take_their_tile(tile, rows, d_in, d_out):
+    assert tile_of("linear_i8", rows, LINEAR_SLOTS, [(d_in, d_out)]) == tile
+    assert rows > tile[0] and rows % tile[0] and d_out > tile[1] and d_out % tile[1]
+
+
+@pytest.mark.parametrize("kind", ["grouped", "grouped_i8"])
+@pytest.mark.parametrize("tile,lengths,d_in,d_out", GROUPED_TILES)
+def test_grouped_batches_take_their_tile(kind, tile, lengths, d_in, d_out):
+    assert tile_of(kind, sum(lengths), len(lengths), [(d_in, d_out)]) == tile
+    assert max(lengths) > tile[0] and max(lengths) % tile[0] and d_out > tile[1] and d_out % tile[1]
+
+
+def test_every_tile_has_a_batch():
+    tiles = [(16, 64), (32, 64), (64, 64), (128, 96), (128, 128), (256, 256)]
+    for cases in (LINEAR_TILES, GROUPED_TILES):
+        assert sorted({c[0] for c in cases}) == tiles

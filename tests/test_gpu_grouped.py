@@ -3,8 +3,8 @@ lora_grouped_layer_i8) against the 64-bit definition."""
 import numpy as np
 import pytest
 
-from tests.dense_cases import (MODS, U, base_i8, bf16, close, close_range, extreme_rows, extreme_scales, gen, grouped_bf16,
-                               ids_of, int8_weight)
+from tests.dense_cases import (GROUPED_TILES, MODS, U, base_i8, bf16, close, close_range, extreme_rows, extreme_scales, gen,
+                               grouped_bf16, ids_of, int8_weight, tile_of)
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -352,9 +352,20 @@ def test_offsets_near_4_gib(int8):
 @pytest.mark.parametrize("lengths,rows", [((10, 10, 10), 25), ((10, 10, 10), 21), ((5, 1, 40, 9, 30), 60), ((70, 60, 90), 150),
                                           ((300, 280, 520), 700)])
 def test_rows_past_the_batch_in_segments_that_fit_touch_nothing(int8, lengths, rows):
+    stray_rows(int8, lengths, rows, {"q": (136, 200, "a"), "o": (72, 40, "o")})
+
+
+@pytest.mark.parametrize("int8", FORMS)
+@pytest.mark.parametrize("tile,lengths,rows,d_out", [((128, 128), (127, 4, 129), 200, 8200), ((256, 256), (300, 200, 260), 560, 12296)])
+def test_rows_past_the_batch_touch_nothing_on_tiles_that_store_whole_lines(int8, tile, lengths, rows, d_out):
+    assert tile_of("grouped_i8" if int8 else "grouped", rows, len(lengths), [(136, d_out)]) == tile
+    stray_rows(int8, lengths, rows, {"q": (136, d_out, "a")})
+
+
+def stray_rows(int8, lengths, rows, shapes):
     # segments of a longer, shuffled batch: those that end inside this one hold rows past it, which are skipped; no row of
     # this batch gets another row's result, the last one (and rows past it) included
-    r = Run(int8, ragged(lengths, 4), len(lengths), {"q": (136, 200, "a"), "o": (72, 40, "o")}, seed=19)
+    r = Run(int8, ragged(lengths, 4), len(lengths), shapes, seed=19)
     fit = [s for s in range(len(lengths)) if sum(lengths[:s + 1]) <= rows]
     assert any((r.ids[rows:] == s).any() for s in fit)  # stray rows are there
     for io in r.dev.values():
@@ -385,3 +396,11 @@ def test_rows_and_scales_at_the_ends_of_the_type():
     for s in (0, 1):
         ref, _ = base_i8(x, r.cpu["q"]["W"][s], r.cpu["q"]["Ws"][s])
         close_range(got[s::2], ref, 4 * U, f"slot {s}")
+
+
+@pytest.mark.parametrize("int8", FORMS)
+@pytest.mark.parametrize("tile,lengths,d_in,d_out", GROUPED_TILES)
+def test_each_tile(int8, tile, lengths, d_in, d_out):
+    # every kernel, its ring filled again and its edges partial
+    assert tile_of("grouped_i8" if int8 else "grouped", sum(lengths), len(lengths), [(d_in, d_out)]) == tile
+    Run(int8, ragged(lengths, 5), len(lengths), {"q": (d_in, d_out, "a")}, seed=len(lengths) + d_in).check()

@@ -3,8 +3,8 @@
 import numpy as np
 import pytest
 
-from tests.dense_cases import (MODS, U, base_i8, bf16, close, close_range, delta, extreme_rows, extreme_scales, gen, ids_of,
-                               int8_weight, quantise_rows)
+from tests.dense_cases import (LINEAR_SLOTS, LINEAR_TILES, MODS, U, base_i8, bf16, close, close_range, delta, extreme_rows,
+                               extreme_scales, gen, ids_of, int8_weight, quantise_rows, tile_of)
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -430,9 +430,19 @@ def test_workspace_is_not_overrun(rows):
 @pytest.mark.parametrize("rows,upto", [(100, 70), (40, 30), (300, 200), (700, 400)])
 @pytest.mark.parametrize("bound", [False, True])
 def test_rows_past_the_batch_in_segments_that_fit_touch_nothing(rows, upto, bound):
+    stray_rows(rows, upto, bound, {"q": (136, 200, "a"), "o": (72, 40, "o")})
+
+
+@pytest.mark.parametrize("tile,rows,upto,d_out", [((128, 128), 300, 200, 8200), ((256, 256), 1300, 900, 12296)])
+def test_rows_past_the_batch_touch_nothing_on_tiles_that_store_whole_lines(tile, rows, upto, d_out):
+    assert tile_of("linear_i8", upto, 5, [(136, d_out)]) == tile
+    stray_rows(rows, upto, False, {"q": (136, d_out, "a")})
+
+
+def stray_rows(rows, upto, bound, shapes):
     # segments of a longer batch: every row of this one gets its own result or none, the delta only from a segment that
     # ends inside the batch, and rows past it are left alone
-    r = Run(rows, 5, {"q": (136, 200, "a"), "o": (72, 40, "o")}, 8, "mixed", seed=36, bound=bound)
+    r = Run(rows, 5, shapes, 8, "mixed", seed=36, bound=bound)
     lg.build_segments(r.dids, r.slots, r.seg, r.ws)
     _, offs, slots, _ = r.seg.host()
     fit = [int(s) for s, end in zip(slots, offs[1:]) if end <= upto]
@@ -501,3 +511,20 @@ def test_quantiser_over_the_significands_of_amaxs_own_power_of_two(copies):
     amax = x.abs().amax(1, keepdim=True)
     want = (torch.round(127.0 * x / amax).float() * (amax.float() / 127.0)).to(torch.bfloat16)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("tile,rows,d_in,d_out", LINEAR_TILES)
+@pytest.mark.parametrize("ranks,kind,fmt", [((16, 0, 8, 5, 32), "mixed", "bf16"), ((64, 0, 33, 40, 5), "runs", "both"),
+                                            ((64, 40, 17, 64, 33), "mixed", "bf16"), ((32, 8, 24, 1, 16), "runs", "int8")])
+def test_each_tile(tile, rows, d_in, d_out, ranks, kind, fmt):
+    # every kernel of the int8 base, its ring filled again and its edges partial; ranks up to 32 and above are two of them
+    assert tile_of("linear_i8", rows, LINEAR_SLOTS, [(d_in, d_out)]) == tile
+    Run(rows, LINEAR_SLOTS, {"q": (d_in, d_out, "a")}, ranks, kind, seed=rows + d_in, fmt=fmt).check()
+
+
+def test_whole_layer_of_decode_rows():
+    # every projection on the 128-row tile, as a whole layer's decode batch takes it
+    shapes = {"q": (1032, 1032, "a"), "k": (1032, 128, "a"), "v": (1032, 128, "a"), "o": (1032, 1032, "o"),
+              "gate": (1032, 4128, "m"), "up": (1032, 4128, "m"), "down": (4128, 1032, "d")}
+    assert tile_of("linear_i8", 130, 150, [s[:2] for s in shapes.values()]) == (128, 128)
+    Run(130, 150, shapes, (64, 8, 16, 8), "distinct", seed=3).check()
