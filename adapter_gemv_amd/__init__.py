@@ -504,7 +504,10 @@ def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, 
     GroupedIO}): y[b] = W_a . x[b // rows_per_x] for the rows in a segment,
     W_a from the device table ``weights`` (pack_weights).  int8: the table's
     weights are int8 with output scales, rows of x are quantised in the call
-    and ``ws`` is needed.  See lora_grouped_layer and lora_grouped_layer_i8."""
+    and ``ws`` is needed.  The tile follows num_rows over
+    ``seg.max_segments`` (over num_slots where that is 0): state it when the
+    batch uses few of the slots.  See lora_grouped_layer and
+    lora_grouped_layer_i8."""
     import torch
     bf16 = torch.bfloat16
     arr = (_GroupedIO * 7)()
