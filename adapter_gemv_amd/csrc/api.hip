@@ -291,9 +291,8 @@ size_t lora_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_ran
   return ws_need(num_rows, num_slots, max_rank, sum_d_in);
 }
 
-// The fused layer's workspace: the shrink's partials, then one v plane
-// [num_rows][rs] per projection (256-byte aligned); at least the segment
-// builder's.
+// The int8 form's: the fused layer's, then the rows by slot and the quantised
+// rows.
 size_t lora_linear_i8_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank, int64_t sum_d_in,
                                       int32_t n_modules) {
   const size_t base = lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules);
@@ -310,6 +309,9 @@ size_t lora_grouped_workspace_bytes(int32_t num_rows, int32_t num_slots, int64_t
   return a > b ? a : b;
 }
 
+// The fused layer's workspace: the shrink's partials, then one v plane
+// [num_rows][rs] per projection (256-byte aligned); at least the segment
+// builder's.
 size_t lora_linear_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank, int64_t sum_d_in,
                                    int32_t n_modules) {
   if (num_rows < 0 || num_slots < 1 || max_rank < 1 || max_rank > LORA_MAX_RANK || sum_d_in < 0 || n_modules < 1 ||
@@ -686,11 +688,15 @@ struct QuantInputs {
 // twice the smallest that holds an average group are left out, and the largest
 // is for groups of more than 128 rows (16 slots x 128 rows on 8192 x 8192, W
 // from HBM once: 254 us with 128 rows a tile, 287 with 256, int8; the account
-// knows no HBM).  Measured against it (us): 128 rows on a whole layer's 84000
-// outputs, 195 expected and 207 measured by 128 columns, 293 and 250 by 96;
-// 256 rows on 18432 outputs, 89 and 68 by 96 columns (384 blocks on 512
-// places), 109 and 87 by 128 (288 on 256); 8 experts x 16 rows on average on 2
-// x 28672 outputs, 590 and 630 by 32 rows, 752 and 780 by 16.
+// knows no HBM).  Measured against it (us), base alone: 128 rows on a whole
+// layer's 84000 outputs, 195 expected and 207 to 216 measured by 128 columns,
+// 293 and 250 by 96; 256 rows on 18432 outputs, 90 and 59 to 68 by 96 columns
+// (384 blocks on 512 places), 109 and 87 by 128 (288 on 256); 8 experts x 16
+// rows on average on 2 x 28672 outputs, 590 and 622 by 32 rows, 752 and 780 by
+// 16.  With a delta it takes the blocks' waits for the adapters and not the
+// bytes of their B, which every tile reads: the whole layer with 128 adapters of
+// rank 64 (1.4 GB of B) 224 and 449, the 256 rows with about 100 of rank 32 98
+// and 85.
 constexpr int kComputeUnits = 256;
 constexpr double kUnitBytesPerUs = 45000;
 

@@ -55,12 +55,17 @@ __global__ __launch_bounds__(256) void quantize_reduce_kernel(LayerDesc d, Quant
 //    4 waves, 2 stages, two blocks (see pick_gemm).  A whole layer's int8 base and delta: [676
 //    and 712], 128 columns with 5 stages 683, 256 bytes x 2 stages 692, 2
 //    stages and two blocks 746, 64 columns 732, 256 columns 780.
-//  * 256 x 256 on 4 waves of 128 x 128 (gemm_block): 8192 x 8192 x 8192 bf16 860
-//    to 900 us (1.22 to 1.28 PFLOP/s; torch.mm 800), 16384 of
-//    each 1.41 to 1.46 PFLOP/s (1.58), int8 with the quantiser 2.6 POP/s
-//    (2.38).  The counters show the matrix cores busy for 71% of the cycles of
-//    a prefill at the 1.8 GHz its power leaves.  8 waves of 128 x 64 with no
-//    operands ahead: 1.05 PFLOP/s on the grouped prefill against 1.2.
+//  * 256 x 256 on 4 waves of 128 x 128 (gemm_block): 8192 x 8192 x 8192 bf16 758
+//    us (1.45 PFLOP/s; torch.mm on the same card 674), 16384 of each 6.04 ms
+//    (1.46 PFLOP/s; 5.50), int8 with the quantiser 446 us and 3.20 ms (2.47 and
+//    2.75 POP/s; 441 us and 3.68 ms).  The counters show the matrix cores busy for 70% of the
+//    cycles of a prefill at the 1.8 GHz its power leaves.  8 waves of 128 x 64
+//    with no operands ahead: 1.05 PFLOP/s on the grouped prefill against 1.2.
+//  * Registers: every kernel fits but the 256 x 256 ones, whose sums and operands
+//    fill both files, and the 128 x 128 one at ranks above 32.  Spilled before
+//    the main loop and read back in the epilogue: int8 base above rank 32, 33
+//    (136 bytes a lane; its product takes 4.35 ms of a rank 64 prefill, 4.04 at
+//    rank 16); grouped int8 3, grouped bf16 1; the 128 x 128 one 1.
 //                                           I8  RT   NC  WR WC WK  KB  S EU
 template <bool I8> using Cfg16 = GemmCfg<I8, 16, 64, 1, 1, 4, 512, 2, 2>;
 template <bool I8> using Cfg32 = GemmCfg<I8, 32, 64, 1, 1, 4, 256, 3, 2>;

@@ -219,18 +219,6 @@ __device__ __forceinline__ void mma_drain() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// The delta of one 16-row tile on top of its finished base sums acc[.] (4
-// consecutive outputs of a lane's row per column tile, columns n0 + 16 nt).
-// For each adapter among the 16 rows in turn, B_a's rows are the matrix-core A
-// operand and all 16 rows' v the B operand; the columns of that adapter's rows
-// are then added and the others dropped (selected, not multiplied by zero: a
-// non-finite factor of one row's adapter must not reach the others).  v, fp32,
-// enters as bf16 hi + lo (2^-16 relative).  The B of the next adapters is
-// requested before the current one's products (AHEAD).
-// An int8 B (values exact in bf16) comes in the same 16-byte loads: the piece
-// that holds a lane's 8 values, of which it keeps its half; the output scales
-// come one per lane and are handed round.
-
 // Hold results of the matrix cores until they may be read: the compiler counts
 // the wait states on one of the paths that lead to the read only, so a branch
 // between them can leave too few (seen as wrong first elements of a tile).
@@ -339,6 +327,17 @@ __device__ __forceinline__ void use_b(const RowInfo &ri, const V8Split (&v)[KT],
     for (int i = 0; i < 4; ++i) acc[nt][i] = mine ? fmaf(t[nt][i], sc[nt][i], acc[nt][i]) : acc[nt][i];
 }
 
+// The delta of one 16-row tile on top of its finished base sums acc[.] (4
+// consecutive outputs of a lane's row per column tile, columns n0 + 16 nt).
+// For each adapter among the 16 rows in turn, B_a's rows are the matrix-core A
+// operand and all 16 rows' v the B operand; the columns of that adapter's rows
+// are then added and the others dropped (selected, not multiplied by zero: a
+// non-finite factor of one row's adapter must not reach the others).  v, fp32,
+// enters as bf16 hi + lo (2^-16 relative).  The B of the next adapters is
+// requested before the current one's products (AHEAD).
+// An int8 B (values exact in bf16) comes in the same 16-byte loads: the piece
+// that holds a lane's 8 values, of which it keeps its half; the output scales
+// come one per lane and are handed round.
 // AHEAD == 1: f[0] may hold the last row tile's adapter, which is then not
 // loaded again.
 template <int DT, int KT, int AHEAD>

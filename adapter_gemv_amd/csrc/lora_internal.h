@@ -260,7 +260,7 @@ hipError_t launch_quantize_reduce(const LayerDesc &d, const QuantDesc &q, const 
                                   hipStream_t stream);
 // Batches of at least this many rows are multiplied in the order of their
 // slots: 16 rows of a tile then have few adapters between them.  4096 rows over
-// 64 adapters of rank 64, q/o of 8192, int8 base: 1894 -> 644 us; 256 Zipf rows
+// 64 adapters of rank 64, q/o of 8192, int8 base: 1846 -> 634 us; 256 Zipf rows
 // over about 100 adapters 155 -> 144; a different adapter for each of 128 rows
 // 643 -> 647 (left in their order when the caller's bound says so).
 constexpr int kOrderRows = 64;
