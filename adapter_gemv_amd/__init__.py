@@ -23,7 +23,9 @@ __all__ = [
     "decode_layer_launches", "layer_shrink", "layer_expand", "pack_table", "STATIC_SCRATCH_BYTES",
     "status_string", "MAX_RANK", "host_lib", "LinearIO", "LinearQ4IO", "Q4_GROUP", "MASK_INT8_ITEMS", "module_mask",
     "LinearI8IO", "linear_i8_workspace_bytes", "GroupedIO", "grouped_layer", "grouped_workspace_bytes", "pack_weights",
-    "WEIGHT_ENTRY_DTYPE", "I8_MAX_IN",
+    "WEIGHT_ENTRY_DTYPE", "I8_MAX_IN", "LinearQ4GIO", "linear_q4g_workspace_bytes", "GatedIO", "GatedQ4GIO", "gated_layer",
+    "gated_workspace_bytes", "grouped_layer_q4g", "grouped_gated_layer", "grouped_gated_layer_q4g", "pack_weights_q4g",
+    "WEIGHT_Q4G_ENTRY_DTYPE", "Q4_GROUPS", "ACTIVATIONS",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,6 +40,10 @@ TABLE_ENTRY_DTYPE = np.dtype([("A", "<u8"), ("B", "<u8"), ("rank", "<i4"), ("sca
 # lora_weight_entry_t, 32 bytes
 WEIGHT_ENTRY_DTYPE = np.dtype([("W", "<u8"), ("Ws", "<u8"), ("ldw", "<i8"), ("reserved", "<i8")])
 assert WEIGHT_ENTRY_DTYPE.itemsize == 32
+# lora_weight_q4g_entry_t, 32 bytes
+WEIGHT_Q4G_ENTRY_DTYPE = np.dtype([("W", "<u8"), ("Ws", "<u8"), ("ldw", "<i8"), ("lds", "<i8")])
+Q4_GROUPS = (32, 64, 128)  # inputs that share a scale in the _q4g calls
+ACTIVATIONS = ("silu", "gelu_tanh")  # lora_activation_t, in order
 I8_MAX_IN = 131072  # LORA_I8_MAX_IN
 FORMAT_BF16, FORMAT_INT8_ROWS = 0, 1  # lora_factor_format_t
 assert TABLE_ENTRY_DTYPE.itemsize == 32
@@ -78,6 +84,27 @@ class _LinI8IO(ctypes.Structure):
 class _GroupedIO(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
                 ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("rows_per_x", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _LinQ4GIO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("Wq", ctypes.c_void_p), ("ldwq", ctypes.c_int64),
+                ("Ws", ctypes.c_void_p), ("lds", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _GatedIO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("Wg", ctypes.c_void_p), ("ldwg", ctypes.c_int64),
+                ("Wu", ctypes.c_void_p), ("ldwu", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("d_in", ctypes.c_int32), ("d_ff", ctypes.c_int32)]
+
+
+class _GatedQ4GIO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("Wgq", ctypes.c_void_p), ("ldwg", ctypes.c_int64),
+                ("Wgs", ctypes.c_void_p), ("ldsg", ctypes.c_int64), ("Wuq", ctypes.c_void_p), ("ldwu", ctypes.c_int64),
+                ("Wus", ctypes.c_void_p), ("ldsu", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("d_in", ctypes.c_int32), ("d_ff", ctypes.c_int32), ("group", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
 
 
@@ -139,6 +166,22 @@ def lib() -> ctypes.CDLL:
         L.lora_grouped_layer.argtypes = [ctypes.POINTER(_GroupedIO), u32, i32, vp, i32, _Seg, vp]
         L.lora_grouped_layer_i8.restype = st
         L.lora_grouped_layer_i8.argtypes = [ctypes.POINTER(_GroupedIO), u32, i32, vp, i32, _Seg, vp, sz, vp]
+        L.lora_linear_q4g_workspace_bytes.restype = sz
+        L.lora_linear_q4g_workspace_bytes.argtypes = [i32, i32, i32, i64, i32]
+        L.lora_linear_layer_q4g.restype = st
+        L.lora_linear_layer_q4g.argtypes = [ctypes.POINTER(_LinQ4GIO), u32, i32, vp, vp, i32, _Seg, i32, vp, sz, vp]
+        L.lora_gated_workspace_bytes.restype = sz
+        L.lora_gated_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.lora_gated_layer.restype = st
+        L.lora_gated_layer.argtypes = [ctypes.POINTER(_GatedIO), i32, i32, vp, vp, i32, _Seg, i32, vp, sz, vp]
+        L.lora_gated_layer_q4g.restype = st
+        L.lora_gated_layer_q4g.argtypes = [ctypes.POINTER(_GatedQ4GIO), i32, i32, vp, vp, i32, _Seg, i32, vp, sz, vp]
+        L.lora_grouped_layer_q4g.restype = st
+        L.lora_grouped_layer_q4g.argtypes = [ctypes.POINTER(_GroupedIO), u32, i32, vp, i32, i32, _Seg, vp]
+        L.lora_grouped_gated_layer.restype = st
+        L.lora_grouped_gated_layer.argtypes = [ctypes.POINTER(_GroupedIO), i32, i32, vp, i32, _Seg, vp]
+        L.lora_grouped_gated_layer_q4g.restype = st
+        L.lora_grouped_gated_layer_q4g.argtypes = [ctypes.POINTER(_GroupedIO), i32, i32, vp, i32, i32, _Seg, vp]
         L.lora_form_batch.restype = st
         L.lora_form_batch.argtypes = [vp, i32, vp, ctypes.c_float, i32, i32, i32, i32, vp, vp]
         _lib = L
@@ -339,6 +382,47 @@ class LinearI8IO:
         self.d_out = int(Wq.shape[0] if d_out is None else d_out)
 
 
+class LinearQ4GIO:
+    """One projection for linear_layer with a 4-bit base in groups of ``group``
+    (32, 64 or 128) inputs: x [rows, >= d_in] bf16, Wq uint8 [d_out,
+    >= d_in / 2] (packed as for LinearQ4IO, row stride a multiple of 16), Ws
+    float32 [d_out, >= d_in / group], y [rows, >= d_out] bf16 (written).  Every
+    projection of a call has the same group."""
+
+    def __init__(self, x, Wq, Ws, y, group, d_in=None, d_out=None):
+        self.x, self.Wq, self.Ws, self.y, self.group = x, Wq, Ws, y, int(group)
+        self.d_in = int(x.shape[1] if d_in is None else d_in)
+        self.d_out = int(Wq.shape[0] if d_out is None else d_out)
+
+
+def linear_q4g_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, sum_d_in: int, n_modules: int) -> int:
+    return int(lib().lora_linear_q4g_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules))
+
+
+class GatedIO:
+    """The gate and up projections for gated_layer: x [rows, >= d_in], Wg and Wu
+    [d_ff, >= d_in] (the base weights), h [rows, >= d_ff] (written), bf16."""
+
+    def __init__(self, x, Wg, Wu, h, d_in=None, d_ff=None):
+        self.x, self.Wg, self.Wu, self.h = x, Wg, Wu, h
+        self.d_in = int(x.shape[1] if d_in is None else d_in)
+        self.d_ff = int(Wg.shape[0] if d_ff is None else d_ff)
+
+
+class GatedQ4GIO:
+    """The same with 4-bit base weights: Wgq, Wgs and Wuq, Wus as LinearQ4GIO's
+    Wq, Ws."""
+
+    def __init__(self, x, Wgq, Wgs, Wuq, Wus, h, group, d_in=None, d_ff=None):
+        self.x, self.Wgq, self.Wgs, self.Wuq, self.Wus, self.h, self.group = x, Wgq, Wgs, Wuq, Wus, h, int(group)
+        self.d_in = int(x.shape[1] if d_in is None else d_in)
+        self.d_ff = int(Wgq.shape[0] if d_ff is None else d_ff)
+
+
+def gated_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, d_in: int) -> int:
+    return int(lib().lora_gated_workspace_bytes(num_rows, num_slots, max_rank, d_in))
+
+
 def linear_i8_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, sum_d_in: int, n_modules: int) -> int:
     return int(lib().lora_linear_i8_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules))
 
@@ -348,6 +432,7 @@ def linear_workspace_bytes(num_rows: int, num_slots: int, max_rank: int, sum_d_i
 
 
 _LIN_I8_PACK = struct.Struct("qqqqqqqii")
+_LIN_Q4G_PACK = struct.Struct("qqqqqqqqiiii")
 _GROUPED_PACK = struct.Struct("qqqqiiii")
 assert _LIN_I8_PACK.size == ctypes.sizeof(_LinI8IO) and _GROUPED_PACK.size == ctypes.sizeof(_GroupedIO)
 
@@ -360,6 +445,56 @@ def _one_device(dev, tensors, what):
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError(f"{what}: the tensors are on more than one device")
+
+
+def _row_ids(row_adapter, num_rows):
+    """The device of a call's row ids (int32, one per row)."""
+    import torch
+    if type(row_adapter) is not torch.Tensor or row_adapter.dtype is not torch.int32 or not row_adapter.is_cuda or \
+            row_adapter.stride() != (1,):
+        _need(row_adapter, torch.int32, "row_adapter", 1)
+    if row_adapter.size(0) < num_rows:
+        raise ValueError("row_adapter: fewer ids than num_rows")
+    dev = row_adapter.get_device()
+    if dev < 0:
+        raise ValueError("row_adapter must be on the GPU")
+    return dev
+
+
+def _q4_weight(Wq, Ws, d_in, d_out, group, dev, name, fields):
+    """(address, bytes per row, scales' address, scales per row) of a 4-bit weight."""
+    import torch
+    if group not in Q4_GROUPS:
+        raise ValueError(f"{name}: group must be one of {Q4_GROUPS}")
+    if d_in % group:
+        raise ValueError(f"{name}: d_in must be a multiple of the group")
+    wp, ldw = _rows(Wq, torch.uint8, d_out, d_in // 2, dev, name, fields[0])
+    sp, lds = _rows(Ws, torch.float32, d_out, d_in // group, dev, name, fields[1])
+    return wp, ldw, sp, lds
+
+
+def _linear_q4g_array(ios, num_rows, row_adapter, rest):
+    import torch
+    bf16 = torch.bfloat16
+    dev = _row_ids(row_adapter, num_rows)
+    arr = (_LinQ4GIO * 7)()
+    mask, group = 0, 0
+    for i, name in enumerate(MODULES):
+        io = ios.get(name)
+        if io is None:
+            continue
+        if not isinstance(io, LinearQ4GIO):
+            raise TypeError(_ONE_KIND)
+        if group and io.group != group:
+            raise ValueError("linear_layer: every projection has the same group")
+        group = io.group
+        xp, ldx = _rows(io.x, bf16, num_rows, io.d_in, dev, name, "x")
+        yp, ldy = _rows(io.y, bf16, num_rows, io.d_out, dev, name, "y")
+        weight = _q4_weight(io.Wq, io.Ws, io.d_in, io.d_out, group, dev, name, ("Wq", "Ws"))
+        _LIN_Q4G_PACK.pack_into(arr, i * _LIN_Q4G_PACK.size, xp, ldx, *weight, yp, ldy, io.d_in, io.d_out, group, 0)
+        mask |= 1 << i
+    _one_device(dev, rest, "linear_layer")
+    return arr, mask
 
 
 def _linear_i8_array(ios, num_rows, row_adapter, rest):
@@ -377,8 +512,7 @@ def _linear_i8_array(ios, num_rows, row_adapter, rest):
         if io is None:
             continue
         if not isinstance(io, LinearI8IO):
-            raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every "
-                            "projection LinearI8IO")
+            raise TypeError(_ONE_KIND)
         Ws, d_out = io.Ws, io.d_out
         xp, ldx = _rows(io.x, bf16, num_rows, io.d_in, dev, name, "x")
         yp, ldy = _rows(io.y, bf16, num_rows, d_out, dev, name, "y")
@@ -394,25 +528,31 @@ def _linear_i8_array(ios, num_rows, row_adapter, rest):
     return arr, mask
 
 
-_LINEAR_KINDS = {LinearIO: (_LinIO, ""), LinearQ4IO: (_LinQ4IO, "_q4"), LinearI8IO: (_LinI8IO, "_i8")}
+_LINEAR_KINDS = {LinearIO: (_LinIO, ""), LinearQ4IO: (_LinQ4IO, "_q4"), LinearI8IO: (_LinI8IO, "_i8"),
+                 LinearQ4GIO: (_LinQ4GIO, "_q4g")}
+_ONE_KIND = ("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every projection LinearI8IO, "
+             "or every projection LinearQ4GIO")
 
 
 def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws, stream=None, module_mask=None,
                  _fn="lora_linear_layer"):
     """Base projection + delta of every projection in ``ios`` ({name:
-    LinearIO}, or {name: LinearQ4IO} for 4-bit or {name: LinearI8IO} for int8
-    base weights); see lora_linear_layer, lora_linear_layer_q4 and
-    lora_linear_layer_i8."""
+    LinearIO}, or {name: LinearQ4IO} or {name: LinearQ4GIO} for 4-bit or
+    {name: LinearI8IO} for int8 base weights); see lora_linear_layer,
+    lora_linear_layer_q4, lora_linear_layer_q4g and lora_linear_layer_i8."""
     import torch
     if type(row_adapter) is not torch.Tensor or row_adapter.dtype is not torch.int32 or not row_adapter.is_cuda or \
             row_adapter.stride() != (1,):
         _need(row_adapter, torch.int32, "row_adapter", 1)
     # any object with its attributes is a bf16 projection, as for the other layer calls
-    kind = next((k for k in (LinearQ4IO, LinearI8IO) if any(isinstance(io, k) for io in ios.values())), LinearIO)
+    kind = next((k for k in (LinearQ4IO, LinearI8IO, LinearQ4GIO) if any(isinstance(io, k) for io in ios.values())), LinearIO)
     cstruct, suffix = _LINEAR_KINDS[kind]
-    if kind is LinearI8IO:
+    if kind is LinearI8IO or kind is LinearQ4GIO:
         _slot_table(table, num_slots, "table")
-        arr, mask = _linear_i8_array(ios, num_rows, row_adapter, (table, ws, seg.perm))
+        array = _linear_i8_array if kind is LinearI8IO else _linear_q4g_array
+        if kind is LinearQ4GIO and _fn != "lora_linear_layer":
+            raise TypeError("linear_shrink, linear_expand: not for LinearQ4GIO")
+        arr, mask = array(ios, num_rows, row_adapter, (table, ws, seg.perm))
         _fn += suffix
         _check(getattr(lib(), _fn)(arr, mask if module_mask is None else module_mask, num_rows, _ptr(row_adapter),
                                    _ptr(table), num_slots, seg.c(), max_rank, _ptr(ws),
@@ -425,8 +565,7 @@ def linear_layer(ios, num_rows, row_adapter, table, num_slots, seg, max_rank, ws
         if io is None:
             continue
         if kind is not LinearIO and not isinstance(io, kind):
-            raise TypeError("linear_layer: every projection LinearIO, or every projection LinearQ4IO, or every "
-                            "projection LinearI8IO")
+            raise TypeError(_ONE_KIND)
         for t, what in ((io.x, "x"), (io.y, "y")) + (((io.W, "W"),) if kind is LinearIO else ()):
             _need(t, torch.bfloat16, f"{name}.{what}", 2)
         if io.x.shape[0] < num_rows or io.y.shape[0] < num_rows:
@@ -537,6 +676,109 @@ def grouped_layer(ios, num_rows, weights, num_slots, seg, ws=None, stream=None, 
     else:
         _check(lib().lora_grouped_layer(arr, mask, num_rows, _ptr(weights), num_slots, seg.c(), _stream(stream)),
                "lora_grouped_layer")
+
+
+def _activation(name) -> int:
+    try:
+        return ACTIVATIONS.index(name)
+    except ValueError:
+        raise ValueError(f"activation must be one of {ACTIVATIONS}") from None
+
+
+def gated_layer(io, num_rows, row_adapter, table, num_slots, seg, max_rank, ws, stream=None, activation="silu"):
+    """The gated half of a feed-forward block: h = act(gate) * up, both
+    projections with the rows' adapters (table columns "gate" and "up").  ``io``:
+    GatedIO, or GatedQ4GIO for 4-bit base weights; ``activation``: one of
+    ACTIVATIONS; ``ws``: gated_workspace_bytes.  See lora_gated_layer and
+    lora_gated_layer_q4g."""
+    import torch
+    bf16 = torch.bfloat16
+    act = _activation(activation)
+    dev = _row_ids(row_adapter, num_rows)
+    _slot_table(table, num_slots, "table")
+    xp, ldx = _rows(io.x, bf16, num_rows, io.d_in, dev, "gated_layer", "x")
+    hp, ldh = _rows(io.h, bf16, num_rows, io.d_ff, dev, "gated_layer", "h")
+    if isinstance(io, GatedQ4GIO):
+        gate = _q4_weight(io.Wgq, io.Wgs, io.d_in, io.d_ff, io.group, dev, "gated_layer", ("Wgq", "Wgs"))
+        up = _q4_weight(io.Wuq, io.Wus, io.d_in, io.d_ff, io.group, dev, "gated_layer", ("Wuq", "Wus"))
+        arg, fn = _GatedQ4GIO(xp, ldx, *gate, *up, hp, ldh, io.d_in, io.d_ff, io.group, 0), "lora_gated_layer_q4g"
+    else:
+        gate = _rows(io.Wg, bf16, io.d_ff, io.d_in, dev, "gated_layer", "Wg")
+        up = _rows(io.Wu, bf16, io.d_ff, io.d_in, dev, "gated_layer", "Wu")
+        arg, fn = _GatedIO(xp, ldx, *gate, *up, hp, ldh, io.d_in, io.d_ff), "lora_gated_layer"
+    _one_device(dev, (table, ws, seg.perm), "gated_layer")
+    _check(getattr(lib(), fn)(arg, act, num_rows, _ptr(row_adapter), _ptr(table), num_slots, seg.c(), max_rank, _ptr(ws),
+                              ws.numel() * ws.element_size(), _stream(stream)), fn)
+
+
+def pack_weights_q4g(W_ptrs, ldw, Ws_ptrs, lds) -> np.ndarray:
+    """Host bytes of a table of lora_weight_q4g_entry_t; arrays of shape
+    [num_slots, 7]: device addresses of the packed weights (0: none), bytes per
+    row, addresses of their group scales, floats per row of those."""
+    W = np.asarray(W_ptrs, np.uint64)
+    t = np.zeros(W.shape, WEIGHT_Q4G_ENTRY_DTYPE)
+    t["W"] = W
+    t["ldw"] = np.asarray(ldw, np.int64)
+    t["Ws"] = np.asarray(Ws_ptrs, np.uint64)
+    t["lds"] = np.asarray(lds, np.int64)
+    return t
+
+
+_GATE = MODULES.index("gate")
+
+
+def _grouped_array(ios, num_rows, weights, num_slots, seg, what):
+    import torch
+    bf16 = torch.bfloat16
+    arr = (_GroupedIO * 7)()
+    mask = 0
+    dev = weights.get_device()
+    if dev < 0:
+        raise ValueError("weights must be on the GPU")
+    _slot_table(weights, num_slots, "weights")
+    for i, name in enumerate(MODULES):
+        io = ios.get(name)
+        if io is None:
+            continue
+        fan = io.rows_per_x
+        if fan < 1:
+            raise ValueError(f"{name}: rows_per_x must be >= 1")
+        xp, ldx = _rows(io.x, bf16, -(-num_rows // fan), io.d_in, dev, name, "x")
+        yp, ldy = _rows(io.y, bf16, num_rows, io.d_out, dev, name, "y")
+        _GROUPED_PACK.pack_into(arr, i * _GROUPED_PACK.size, xp, ldx, yp, ldy, io.d_in, io.d_out, fan, 0)
+        mask |= 1 << i
+    _one_device(dev, (seg.perm,), what)
+    return arr, mask
+
+
+def grouped_layer_q4g(ios, num_rows, weights, num_slots, seg, group, stream=None, module_mask=None):
+    """grouped_layer with 4-bit weights and a scale per group of ``group`` (32, 64
+    or 128) inputs from the device table ``weights`` (pack_weights_q4g); see
+    lora_grouped_layer_q4g."""
+    arr, mask = _grouped_array(ios, num_rows, weights, num_slots, seg, "grouped_layer_q4g")
+    _check(lib().lora_grouped_layer_q4g(arr, mask if module_mask is None else module_mask, num_rows, _ptr(weights), num_slots,
+                                        group, seg.c(), _stream(stream)), "lora_grouped_layer_q4g")
+
+
+def grouped_gated_layer(io, num_rows, weights, num_slots, seg, stream=None, activation="silu"):
+    """The gated half of a feed-forward block with a whole gate and up weight per
+    slot: io.y[b] = act(Wg_a . x) * (Wu_a . x), x = io.x[b // rows_per_x], for the
+    rows in a segment.  ``io``: GroupedIO whose y is h; ``weights``: the device
+    table (pack_weights), columns "gate" and "up".  State ``seg.max_segments`` as
+    for grouped_layer.  See lora_grouped_gated_layer."""
+    act = _activation(activation)
+    arr, _ = _grouped_array({"gate": io}, num_rows, weights, num_slots, seg, "grouped_gated_layer")
+    _check(lib().lora_grouped_gated_layer(arr[_GATE], act, num_rows, _ptr(weights), num_slots, seg.c(), _stream(stream)),
+           "lora_grouped_gated_layer")
+
+
+def grouped_gated_layer_q4g(io, num_rows, weights, num_slots, seg, group, stream=None, activation="silu"):
+    """grouped_gated_layer with 4-bit weights (pack_weights_q4g); see
+    lora_grouped_gated_layer_q4g."""
+    act = _activation(activation)
+    arr, _ = _grouped_array({"gate": io}, num_rows, weights, num_slots, seg, "grouped_gated_layer_q4g")
+    _check(lib().lora_grouped_gated_layer_q4g(arr[_GATE], act, num_rows, _ptr(weights), num_slots, group, seg.c(), _stream(stream)),
+           "lora_grouped_gated_layer_q4g")
 
 
 def build_segments(row_adapter, num_slots: int, seg: Segments, ws, stream=None):

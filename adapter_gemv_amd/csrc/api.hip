@@ -710,22 +710,24 @@ double row_tiles_expected(int64_t rows, int64_t groups, int t) {
   return (double)groups * (1 + std::max(0.0, 0.5 - (t - per) / (3.4 * spread)));
 }
 
-int pick_gemm(int64_t rows, int64_t groups, int adapters, const GemmModule *m, int n, double *expected_us) {
+int pick_gemm(GemmKind kind, int64_t rows, int64_t groups, int adapters, const GemmModule *m, int n, double *expected_us) {
   const int64_t per = (rows + groups - 1) / groups;
+  const int tiles = gemm_tiles(kind);
+  const double w_share = is_q4(kind) ? 0.25 : 1;  // bytes of W for one of x
   int fit = 0;
-  while (fit + 1 < kGemmTiles && gemm_tile(fit).rows < per) ++fit;
+  while (fit + 1 < tiles && gemm_tile(kind, fit).rows < per) ++fit;
   int best = 0;
   double least = 0;
-  for (int cfg = 0; cfg < kGemmTiles; ++cfg) {
-    const GemmTile t = gemm_tile(cfg);
-    if (cfg > 0 && (t.rows > 2 * gemm_tile(fit).rows || (t.rows > 128 && per <= 128))) continue;
+  for (int cfg = 0; cfg < tiles; ++cfg) {
+    const GemmTile t = gemm_tile(kind, cfg);
+    if (cfg > 0 && (t.rows > 2 * gemm_tile(kind, fit).rows || (t.rows > 128 && per <= 128))) continue;
     const double rt = row_tiles_expected(rows, groups, t.rows);
     double blocks = 0;
     for (int i = 0; i < n; ++i) blocks += rt * ((m[i].d_out + t.cols - 1) / t.cols);
     const double share = std::min((double)t.per_unit, std::ceil(blocks / kComputeUnits));
     double sum = 0, longest = 0;
     for (int i = 0; i < n; ++i) {
-      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + share * (t.rows + t.cols) * (double)m[i].kbytes / kUnitBytesPerUs;
+      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + share * (t.rows + t.wcols * w_share) * (double)m[i].kbytes / kUnitBytesPerUs;
       sum += rt * ((m[i].d_out + t.cols - 1) / t.cols) * one;
       longest = std::max(longest, one);
     }
@@ -750,9 +752,9 @@ bool rows_by_slot(int num_rows, const lora_segments_t &seg) {
 int tile_of_call(GemmKind kind, int num_rows, int num_slots, const lora_segments_t &seg, const GemmModule *m, int n,
                  double *expected_us = nullptr) {
   const int segs = segment_bound(num_rows, num_slots, seg);
-  if (kind != kLinearI8) return pick_gemm(num_rows, segs, 0, m, n, expected_us);
+  if (!has_delta(kind)) return pick_gemm(kind, num_rows, segs, 0, m, n, expected_us);
   const int adapters = rows_by_slot(num_rows, seg) ? (int)std::min<int64_t>(segs, 1 + 16 * (int64_t)segs / num_rows) : segs;
-  return pick_gemm(num_rows, 1, adapters, m, n, expected_us);
+  return pick_gemm(kind, num_rows, 1, adapters, m, n, expected_us);
 }
 
 // Number the blocks of n projections (g.mod[0..n), longest d_in first: a
@@ -762,7 +764,7 @@ int tile_of_call(GemmKind kind, int num_rows, int num_slots, const lora_segments
 lora_status_t gemm_launch(GemmDesc &g, int n, int64_t row_tiles, int num_rows, int num_slots,
                           const lora_segments_t &seg, GemmKind kind, int cfg, hipStream_t s) {
   std::stable_sort(g.mod, g.mod + n, [](const GemmModule &a, const GemmModule &b) { return a.d_in > b.d_in; });
-  const GemmTile tile = gemm_tile(cfg);
+  const GemmTile tile = gemm_tile(kind, cfg);
   int64_t blocks = 0;
   for (int i = 0; i < n; ++i) {
     g.mod[i].n_tiles = (g.mod[i].d_out + tile.cols - 1) / tile.cols;
@@ -869,7 +871,7 @@ lora_status_t linear_phase(bool do_shrink, bool do_fused, const IO *io, uint32_t
       gm.rows_per_x = 1;
     }
     const int cfg = tile_of_call(kLinearI8, num_rows, num_slots, seg, g.mod, n);
-    g.row_tiles = (num_rows + gemm_tile(cfg).rows - 1) / gemm_tile(cfg).rows;
+    g.row_tiles = (num_rows + gemm_tile(kLinearI8, cfg).rows - 1) / gemm_tile(kLinearI8, cfg).rows;
     g.rs = rs;
     g.max_rank = max_rank;
     g.ids = row_adapter;
@@ -976,22 +978,38 @@ lora_status_t lora_linear_expand_q4(const lora_linear_q4_io_t *io, uint32_t modu
 
 namespace {
 
-// The checks, the quantiser (int8) and the launch of the grouped products.
-lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
-                           const lora_weight_entry_t *weights, int32_t num_slots, const lora_segments_t &seg, void *ws,
-                           size_t ws_bytes, void *stream) {
+// log2 of a group of 4-bit weights, -1 for a length that is none.
+int group_log(int32_t group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
+
+// The activation's constants (gate_act); false for one that is none.
+bool set_activation(GemmDesc &g, int32_t activation) {
+  if (activation != LORA_ACT_SILU && activation != LORA_ACT_GELU_TANH) return false;
+  const double c1 = 1.5957691216057308;  // 2 sqrt(2 / pi)
+  g.act_c1 = activation == LORA_ACT_SILU ? 1.f : (float)c1;
+  g.act_c3 = activation == LORA_ACT_SILU ? 0.f : (float)(0.044715 * c1);
+  return true;
+}
+
+// The checks, the quantiser (int8) and the launch of the grouped products; the
+// gated kinds take one io (gate's and up's) and a mask of gate alone.
+lora_status_t grouped_call(GemmKind kind, const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
+                           const void *weights, int32_t num_slots, const lora_segments_t &seg, void *ws,
+                           size_t ws_bytes, void *stream, int32_t group = 0, int32_t activation = LORA_ACT_SILU) {
+  const bool i8 = kind == kGroupedI8;
   if (!io || !weights) return LORA_ERR_NULL;
   lora_status_t st = check_segments(seg);
   if (st != LORA_OK) return st;
   if (module_mask == 0 || module_mask >= (1u << LORA_NUM_MODULES)) return LORA_ERR_MODULE;
   if (num_rows < 0 || num_slots < 1) return LORA_ERR_SHAPE;
   GemmDesc g{};
+  if (is_q4(kind) && group_log(group) < 0) return LORA_ERR_SHAPE;
+  if (is_gated(kind) && !set_activation(g, activation)) return LORA_ERR_SHAPE;
   QuantInputs quant;
   int n = 0;
   int64_t sum_d_in = 0;
   for (int c = 0; c < LORA_NUM_MODULES; ++c) {
     if (!(module_mask & (1u << c))) continue;
-    const lora_grouped_io_t &m = io[c];
+    const lora_grouped_io_t &m = is_gated(kind) ? *io : io[c];
     if (!m.x || !m.y) return LORA_ERR_NULL;
     if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.rows_per_x < 1 || m.ldx > kMaxDim ||
         m.ldy > kMaxDim)
@@ -999,6 +1017,7 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
     if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || !aligned16(m.x) || !aligned16(m.y))
       return LORA_ERR_ALIGN;
     if (i8 && m.d_in > LORA_I8_MAX_IN) return LORA_ERR_SHAPE;
+    if (is_q4(kind) && m.d_in % group) return LORA_ERR_ALIGN;
     const int64_t x_rows = ((int64_t)num_rows + m.rows_per_x - 1) / m.rows_per_x;
     if (!fits_u32(x_rows, m.ldx) || !fits_u32(num_rows, m.ldy)) return LORA_ERR_SHAPE;
     GemmModule &gm = g.mod[n];
@@ -1019,6 +1038,8 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
     gm.d_out = m.d_out;
     gm.col = c;
     gm.rows_per_x = m.rows_per_x;
+    gm.group_log = is_q4(kind) ? group_log(group) : 0;
+    if (is_gated(kind)) g.mod[1].col = LORA_UP;
     sum_d_in += m.d_in;
     ++n;
   }
@@ -1033,13 +1054,113 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
     st = launched(launch_quantize(quant.d, s));
     if (st != LORA_OK) return st;
   }
-  g.weights = weights;
-  const GemmKind kind = i8 ? kGroupedI8 : kGroupedBf16;
+  g.weights = static_cast<const lora_weight_entry_t *>(weights);
   const int cfg = tile_of_call(kind, num_rows, num_slots, seg, g.mod, n);
-  const int rt = gemm_tile(cfg).rows;
+  const int rt = gemm_tile(kind, cfg).rows;
   // every segment's last tile may be partial
   const int64_t row_tiles = std::min<int64_t>(num_rows, (int64_t)num_rows / rt + segment_bound(num_rows, num_slots, seg));
   return gemm_launch(g, n, row_tiles, num_rows, num_slots, seg, kind, cfg, s);
+}
+
+// One projection of a call with a base weight and adapters, bf16 (group 0) or
+// 4-bit.
+lora_status_t check_adapted(const LinearArgs &m, bool q4, int32_t group) {
+  if (!m.x || !m.y || !m.W || (q4 && !m.Ws)) return LORA_ERR_NULL;
+  if (q4 && group_log(group) < 0) return LORA_ERR_SHAPE;
+  if (m.d_in <= 0 || m.d_out <= 0 || m.ldx < m.d_in || m.ldy < m.d_out || m.ldx > kMaxDim || m.ldy > kMaxDim ||
+      m.ldw > kMaxDim || m.ldws > kMaxDim)
+    return LORA_ERR_SHAPE;
+  if ((m.d_in & 7) || (m.d_out & 7) || (m.ldx & 7) || (m.ldy & 7) || !aligned16(m.x) || !aligned16(m.y) || !aligned16(m.W))
+    return LORA_ERR_ALIGN;
+  if (q4 ? (m.d_in % group) || (m.ldw & 15) || ((uintptr_t)m.Ws & 3) : (m.ldw & 7) != 0) return LORA_ERR_ALIGN;
+  if (q4 ? m.ldw < m.d_in / 2 || m.ldws < m.d_in / group : m.ldw < m.d_in) return LORA_ERR_SHAPE;
+  // the weight, its scales and a B of the largest rank below 4 GiB
+  const int64_t most = (int64_t)0xFFFFFF00 / m.d_out;
+  if (m.ldw > (q4 ? most : most / 2) || m.ldws > most / 4 || most < 2 * LORA_MAX_RANK) return LORA_ERR_SHAPE;
+  return LORA_OK;
+}
+
+// Base products with adapters by the kernels of gemm_items.h: the grouped shrink
+// of the n projections, one v plane each with the rows by slot, and the product
+// (gated: one of both projections).
+lora_status_t adapted_call(GemmKind kind, const LinearArgs *la, const int *cols, int n, bool int8_items, int32_t group,
+                           int32_t activation, int32_t num_rows, const int32_t *row_adapter,
+                           const lora_adapter_entry_t *table, int32_t num_slots, const lora_segments_t &seg,
+                           int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
+  if (!table) return LORA_ERR_NULL;
+  lora_status_t st = check_segments(seg);
+  if (st != LORA_OK) return st;
+  GemmDesc g{};
+  if (!set_activation(g, activation)) return LORA_ERR_SHAPE;
+  if (num_rows < 0 || num_slots < 1) return LORA_ERR_SHAPE;
+  if (max_rank < 1 || max_rank > LORA_MAX_RANK) return LORA_ERR_RANK;
+  if (num_rows > 0 && !row_adapter) return LORA_ERR_NULL;
+  ModuleArgs ms[LORA_NUM_MODULES];
+  int64_t sum_d_in = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!fits_u32(num_rows, la[i].ldx) || !fits_u32(num_rows, la[i].ldy)) return LORA_ERR_SHAPE;
+    ms[i] = ModuleArgs{la[i].x, la[i].ldx, la[i].y, la[i].ldy, la[i].d_in, la[i].d_out, cols[i], int8_items};
+    sum_d_in += la[i].d_in;
+  }
+  st = check_ws(ws, ws_bytes, lora_linear_q4g_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n), &ws);
+  if (st != LORA_OK) return st;
+  const int rs = partial_row_stride(max_rank);
+  if ((int64_t)num_rows * rs * 4 > (int64_t)0xFFFFFF00) return LORA_ERR_SHAPE;
+  if (num_rows == 0) return LORA_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float *vplanes = reinterpret_cast<float *>(static_cast<char *>(ws) +
+                                             ((partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255));
+  int32_t *by_slot = nullptr;
+  if (rows_by_slot(num_rows, seg))
+    by_slot = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n));
+  st = launch_phase(true, ms, n, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws, nullptr, 0, s);
+  if (st != LORA_OK) return st;
+  LayerDesc d;
+  fill_desc(d, ms, n, true, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws);
+  d.v_out = vplanes;
+  d.ldv = rs;
+  st = launched(launch_quantize_reduce(d, QuantDesc{}, row_adapter, by_slot, s));
+  if (st != LORA_OK) return st;
+  for (int i = 0; i < n; ++i) {
+    GemmModule &gm = g.mod[i];
+    gm.x = la[i].x;
+    gm.ldx = la[i].ldx * 2;
+    gm.x_bytes = (uint32_t)(num_rows * la[i].ldx * 2);
+    gm.W = static_cast<const uint8_t *>(la[i].W);
+    gm.ldw = is_q4(kind) ? la[i].ldw : la[i].ldw * 2;
+    gm.Ws = la[i].Ws;
+    gm.ldws = la[i].ldws;
+    gm.group_log = is_q4(kind) ? group_log(group) : 0;
+    gm.y = static_cast<uint16_t *>(la[i].y);
+    gm.ldy = la[i].ldy;
+    gm.v = vplanes + (int64_t)i * num_rows * rs;
+    gm.kbytes = la[i].d_in * 2;
+    gm.d_in = la[i].d_in;
+    gm.d_out = la[i].d_out;
+    gm.col = cols[i];
+    gm.rows_per_x = 1;
+  }
+  const int products = is_gated(kind) ? 1 : n;
+  const int cfg = tile_of_call(kind, num_rows, num_slots, seg, g.mod, products);
+  g.row_tiles = (num_rows + gemm_tile(kind, cfg).rows - 1) / gemm_tile(kind, cfg).rows;
+  g.rs = rs;
+  g.max_rank = max_rank;
+  g.ids = row_adapter;
+  g.order = by_slot;
+  g.table = table;
+  return gemm_launch(g, products, g.row_tiles, num_rows, num_slots, seg, kind, cfg, s);
+}
+
+lora_status_t gated_call(GemmKind kind, const LinearArgs (&la)[2], int32_t group, int32_t activation, int32_t num_rows,
+                         const int32_t *row_adapter, const lora_adapter_entry_t *table, int32_t num_slots,
+                         const lora_segments_t &seg, int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
+  const int cols[2] = {LORA_GATE, LORA_UP};
+  for (const LinearArgs &m : la) {
+    const lora_status_t st = check_adapted(m, is_q4(kind), group);
+    if (st != LORA_OK) return st;
+  }
+  return adapted_call(kind, la, cols, 2, false, group, activation, num_rows, row_adapter, table, num_slots, seg, max_rank, ws,
+                      ws_bytes, stream);
 }
 
 }  // namespace
@@ -1047,15 +1168,15 @@ lora_status_t grouped_call(bool i8, const lora_grouped_io_t *io, uint32_t module
 extern "C" int32_t lora_internal_gemm_tile(int32_t kind, int32_t num_rows, int32_t num_slots, lora_segments_t seg,
                                            const int32_t *d_in, const int32_t *d_out, int32_t n, int32_t *rows,
                                            int32_t *cols, double *expected_us) {
-  if (kind < kLinearI8 || kind > kGroupedI8 || num_rows < 1 || num_slots < 1 || n < 1 || n > kMaxModules) return -1;
+  if (kind < kLinearI8 || kind > kGroupedGatedQ4 || num_rows < 1 || num_slots < 1 || n < 1 || n > kMaxModules) return -1;
   GemmModule m[kMaxModules] = {};
   for (int i = 0; i < n; ++i) {
-    m[i].kbytes = kind == kGroupedBf16 ? d_in[i] * 2 : i8_pitch(d_in[i]);
+    m[i].kbytes = kind == kLinearI8 || kind == kGroupedI8 ? i8_pitch(d_in[i]) : d_in[i] * 2;
     m[i].d_out = d_out[i];
   }
   const int cfg = tile_of_call((GemmKind)kind, num_rows, num_slots, seg, m, n, expected_us);
-  *rows = gemm_tile(cfg).rows;
-  *cols = gemm_tile(cfg).cols;
+  *rows = gemm_tile((GemmKind)kind, cfg).rows;
+  *cols = gemm_tile((GemmKind)kind, cfg).cols;
   return cfg;
 }
 
@@ -1087,13 +1208,91 @@ lora_status_t lora_linear_expand_i8(const lora_linear_i8_io_t *io, uint32_t modu
 lora_status_t lora_grouped_layer(const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
                                  const lora_weight_entry_t *weights, int32_t num_slots, lora_segments_t seg,
                                  void *stream) {
-  return grouped_call(false, io, module_mask, num_rows, weights, num_slots, seg, nullptr, 0, stream);
+  return grouped_call(kGroupedBf16, io, module_mask, num_rows, weights, num_slots, seg, nullptr, 0, stream);
 }
 
 lora_status_t lora_grouped_layer_i8(const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
                                     const lora_weight_entry_t *weights, int32_t num_slots, lora_segments_t seg,
                                     void *ws, size_t ws_bytes, void *stream) {
-  return grouped_call(true, io, module_mask, num_rows, weights, num_slots, seg, ws, ws_bytes, stream);
+  return grouped_call(kGroupedI8, io, module_mask, num_rows, weights, num_slots, seg, ws, ws_bytes, stream);
+}
+
+lora_status_t lora_grouped_layer_q4g(const lora_grouped_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                     const lora_weight_q4g_entry_t *weights, int32_t num_slots, int32_t group,
+                                     lora_segments_t seg, void *stream) {
+  return grouped_call(kGroupedQ4, io, module_mask, num_rows, weights, num_slots, seg, nullptr, 0, stream, group);
+}
+
+lora_status_t lora_grouped_gated_layer(const lora_grouped_io_t *io, int32_t activation, int32_t num_rows,
+                                       const lora_weight_entry_t *weights, int32_t num_slots, lora_segments_t seg,
+                                       void *stream) {
+  return grouped_call(kGroupedGatedBf16, io, 1u << LORA_GATE, num_rows, weights, num_slots, seg, nullptr, 0, stream, 0,
+                      activation);
+}
+
+lora_status_t lora_grouped_gated_layer_q4g(const lora_grouped_io_t *io, int32_t activation, int32_t num_rows,
+                                           const lora_weight_q4g_entry_t *weights, int32_t num_slots, int32_t group,
+                                           lora_segments_t seg, void *stream) {
+  return grouped_call(kGroupedGatedQ4, io, 1u << LORA_GATE, num_rows, weights, num_slots, seg, nullptr, 0, stream, group,
+                      activation);
+}
+
+size_t lora_linear_q4g_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank, int64_t sum_d_in,
+                                       int32_t n_modules) {
+  const size_t base = lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules);
+  if (base == 0) return 0;
+  const size_t need = linear_v_end(num_rows, max_rank, sum_d_in, n_modules) + order_ws_bytes(num_rows);
+  return need > base ? need : base;
+}
+
+size_t lora_gated_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank, int32_t d_in) {
+  return lora_linear_q4g_workspace_bytes(num_rows, num_slots, max_rank, 2 * (int64_t)d_in, 2);
+}
+
+lora_status_t lora_linear_layer_q4g(const lora_linear_q4g_io_t *io, uint32_t module_mask, int32_t num_rows,
+                                    const int32_t *row_adapter, const lora_adapter_entry_t *table, int32_t num_slots,
+                                    lora_segments_t seg, int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
+  if (!io) return LORA_ERR_NULL;
+  const bool int8_items = (module_mask & LORA_MASK_INT8_ITEMS) != 0;
+  module_mask &= ~LORA_MASK_INT8_ITEMS;
+  if (module_mask == 0 || module_mask >= (1u << LORA_NUM_MODULES)) return LORA_ERR_MODULE;
+  LinearArgs la[LORA_NUM_MODULES];
+  int cols[LORA_NUM_MODULES], n = 0, group = 0;
+  for (int c = 0; c < LORA_NUM_MODULES; ++c) {
+    if (!(module_mask & (1u << c))) continue;
+    const lora_linear_q4g_io_t &m = io[c];
+    if (n > 0 && m.group != group) return LORA_ERR_SHAPE;
+    group = m.group;
+    la[n] = LinearArgs{m.x, m.ldx, m.Wq, m.ldwq, static_cast<const float *>(m.Ws), m.lds, m.y, m.ldy, m.d_in, m.d_out};
+    const lora_status_t st = check_adapted(la[n], true, group);
+    if (st != LORA_OK) return st;
+    cols[n++] = c;
+  }
+  return adapted_call(kLinearQ4, la, cols, n, int8_items, group, LORA_ACT_SILU, num_rows, row_adapter, table, num_slots,
+                      seg, max_rank, ws, ws_bytes, stream);
+}
+
+lora_status_t lora_gated_layer(const lora_gated_io_t *io, int32_t activation, int32_t num_rows,
+                               const int32_t *row_adapter, const lora_adapter_entry_t *table, int32_t num_slots,
+                               lora_segments_t seg, int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
+  if (!io) return LORA_ERR_NULL;
+  const lora_gated_io_t &m = *io;
+  const LinearArgs la[2] = {{m.x, m.ldx, m.Wg, m.ldwg, nullptr, 0, m.h, m.ldh, m.d_in, m.d_ff},
+                            {m.x, m.ldx, m.Wu, m.ldwu, nullptr, 0, m.h, m.ldh, m.d_in, m.d_ff}};
+  return gated_call(kGatedBf16, la, 0, activation, num_rows, row_adapter, table, num_slots, seg, max_rank, ws, ws_bytes,
+                    stream);
+}
+
+lora_status_t lora_gated_layer_q4g(const lora_gated_q4g_io_t *io, int32_t activation, int32_t num_rows,
+                                   const int32_t *row_adapter, const lora_adapter_entry_t *table, int32_t num_slots,
+                                   lora_segments_t seg, int32_t max_rank, void *ws, size_t ws_bytes, void *stream) {
+  if (!io) return LORA_ERR_NULL;
+  const lora_gated_q4g_io_t &m = *io;
+  const LinearArgs la[2] = {
+      {m.x, m.ldx, m.Wgq, m.ldwg, static_cast<const float *>(m.Wgs), m.ldsg, m.h, m.ldh, m.d_in, m.d_ff},
+      {m.x, m.ldx, m.Wuq, m.ldwu, static_cast<const float *>(m.Wus), m.ldsu, m.h, m.ldh, m.d_in, m.d_ff}};
+  return gated_call(kGatedQ4, la, m.group, activation, num_rows, row_adapter, table, num_slots, seg, max_rank, ws, ws_bytes,
+                    stream);
 }
 
 }  // extern "C"

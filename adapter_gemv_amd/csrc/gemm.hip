@@ -92,14 +92,11 @@ void pick(const GemmDesc &d, int cfg, int blocks, hipStream_t s) {
 
 }  // namespace
 
-namespace {
-template <class C>
-constexpr GemmTile tile_of(double fixed) {
-  return {C::RT, C::NC, 160 * 1024 / C::LDS, fixed, 0.3 * C::MT * C::NTE / C::DT};
-}
-}  // namespace
+int gemm_tiles(GemmKind kind) { return kind <= kGroupedI8 ? kGemmTiles : kind <= kGroupedGatedBf16 ? gated_tiles() : q4_tiles(); }
 
-GemmTile gemm_tile(int cfg) {
+GemmTile gemm_tile(GemmKind kind, int cfg) {
+  if (kind > kGroupedGatedBf16) return q4_tile(kind >= kGatedQ4, cfg);
+  if (kind > kGroupedI8) return gated_tile(cfg);
   switch (cfg) {
     case 0: return tile_of<Cfg16<true>>(6);
     case 1: return tile_of<Cfg32<true>>(6);
@@ -118,7 +115,12 @@ hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hi
       else pick<true, false, 2>(d, cfg, blocks, stream);
       break;
     case kGroupedBf16: pick<false, true, 0>(d, cfg, blocks, stream); break;
-    default: pick<true, true, 0>(d, cfg, blocks, stream); break;
+    case kGroupedI8: pick<true, true, 0>(d, cfg, blocks, stream); break;
+    case kGatedBf16:
+    case kGroupedGatedBf16: launch_gated(d, kind, cfg, blocks, stream); break;
+    case kLinearQ4:
+    case kGroupedQ4: launch_q4(d, kind, cfg, blocks, stream); break;
+    default: launch_gated_q4(d, kind, cfg, blocks, stream); break;
   }
   return hipGetLastError();
 }

@@ -4,7 +4,14 @@
 //     with q_b, s_b the row quantised to int8 (quantize_rows_kernel) and
 //     v[b] = A_a.x[b] from the grouped shrink;
 //   * the dense products grouped by slot (lora_grouped_layer, _i8):
-//       y[b] = bf16( W_a . x[b / rows_per_x] ),  a = the row's slot.
+//       y[b] = bf16( W_a . x[b / rows_per_x] ),  a = the row's slot;
+//   * either with 4-bit weights W[n][k] = s[n][k / G] q[n][k] and bf16 rows
+//     (lora_linear_layer_q4g, lora_grouped_layer_q4g);
+//   * the gated half of a feed-forward block (lora_gated_layer,
+//     lora_grouped_gated_layer, and _q4g):
+//       h[b] = bf16( act(g) u ),  g and u the sums of gate and up as above: half
+//     of a block's rows of W are gate's, half up's, and a wave holds both sums of
+//     an output.
 //
 // One block computes RT rows x NC output columns over the whole input range.
 // A product of 16-byte pieces looks the same to memory and LDS for either
@@ -35,27 +42,40 @@
 // rows a slot 690 us, 6.2 TB/s); many rows, the matrix cores (gemm.hip).
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace lora {
 
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 
-template <bool I8_, int RT_, int NC_, int WR_, int WC_, int WK_, int KB_, int S_, int EU_, bool PIPE_ = false>
+template <bool I8_, int RT_, int NC_, int WR_, int WC_, int WK_, int KB_, int S_, int EU_, bool PIPE_ = false,
+          bool Q4_ = false, bool GATED_ = false>
 struct GemmCfg {
+  static constexpr bool Q4 = Q4_;                      // 4-bit W, a scale per output and group of inputs; bf16 x
+  static constexpr bool GATED = GATED_;                // the first half of the columns is gate's, the second up's
   static constexpr bool PIPE = PIPE_;                  // operands one step ahead in registers
   static constexpr bool I8 = I8_;
-  static constexpr int RT = RT_, NC = NC_;             // rows and columns of a block
+  static constexpr int RT = RT_, NC = NC_;             // rows and columns (of both halves) of a block
+  static constexpr int HC = GATED_ ? NC_ / 2 : NC_;    // output columns
   static constexpr int WR = WR_, WC = WC_, WK = WK_;   // wave grid: rows, columns, k
-  static constexpr int KB = KB_, S = S_;               // bytes of k per stage, stages
+  static constexpr int KB = KB_, S = S_;               // bytes of k per stage (of x), stages
+  static constexpr int WKB = Q4_ ? KB / 4 : KB;        // the same of W
   static constexpr int EU = EU_;                       // waves per SIMD it is compiled for
   static constexpr int NW = WR * WC * WK, THREADS = NW * 64;
   static constexpr int MT = RT / WR / 16, NT = NC / WC / 16;  // 16 x 16 tiles of a wave
-  static constexpr int NTE = NT >= WK ? NT / WK : 1;   // column tiles a wave finishes (epilogue)
+  // Column tiles a wave finishes (epilogue); gated: as many of each half.
+  static constexpr int NTE = GATED_ ? (NT / 2 >= WK ? NT / 2 / WK : 1) : NT >= WK ? NT / WK : 1;
+  static constexpr int FIN = GATED_ ? 2 * NTE : NTE;   // their sums
   static constexpr int PIECES = KB / 16;
   static constexpr int SWZ = PIECES >= 16 ? 15 : 7;    // rows whose pieces are moved against one another
-  static constexpr int XL = RT * KB / 1024 / NW, WL = NC * KB / 1024 / NW;  // loads per wave and stage
-  static constexpr int XBYTES = RT * KB, STAGE = (RT + NC) * KB;
+  static constexpr int WPIECES = WKB / 16;
+  static constexpr int WSWZ = WPIECES >= 16 ? 15 : WPIECES - 1;
+  static constexpr int XL = RT * KB / 1024 / NW, WL = NC * WKB / 1024 / NW;  // loads per wave and stage
+  // 4-bit: room for the scales of a stage in the shortest groups, and their loads of 64 per wave.
+  static constexpr int SBYTES = Q4_ ? NC * (KB / 64) * 4 : 0, SL = SBYTES / 256 / NW;
+  static constexpr int XBYTES = RT * KB, WBYTES = NC * WKB, STAGE = XBYTES + WBYTES + SBYTES;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
   // A wave of at least 64 finished columns turns its outputs round in LDS and
   // stores whole lines; 8-byte pieces of 16 rows at a time cost a 256 x 256
@@ -63,7 +83,8 @@ struct GemmCfg {
   static constexpr bool TURN = NTE >= 4;
   static constexpr int YROW = NTE * 32 + 16;           // bytes of an output row in LDS
   static constexpr int YWAVE = TURN ? MT * 16 * YROW : 0;
-  static constexpr int TAIL = RED + 32 * RT + NW * YWAVE;  // and the rows' descriptions, when the ring is done
+  static constexpr int INFO = (GATED_ ? 64 : 32) * RT;  // the rows' descriptions (gated: of both projections)
+  static constexpr int TAIL = RED + INFO + NW * YWAVE;  // and the rows' descriptions, when the ring is done
   static constexpr int RING = PIPE ? 5 * XBYTES : S * STAGE;  // pipelined: five places of one operand's stage
   static constexpr int LDS = RING > TAIL ? RING : TAIL;
   static constexpr int DT = NTE < 4 ? NTE : 4;         // column tiles finished at a time
@@ -71,11 +92,19 @@ struct GemmCfg {
   // all differ, and a wave waits for each adapter in turn; the rows of a
   // prefill tile share one, which is kept from row tile to row tile instead.
   static constexpr int AHEAD = RT >= 256 ? 1 : 4;
-  static_assert(XL >= 1 && WL >= 1 && XL * NW * 1024 == RT * KB && WL * NW * 1024 == NC * KB, "loads per wave");
+  static_assert(XL >= 1 && WL >= 1 && XL * NW * 1024 == RT * KB && WL * NW * 1024 == WBYTES, "loads per wave");
+  static_assert(!Q4_ || (SL >= 1 && SL * NW * 256 == SBYTES && !I8_ && !PIPE_), "4-bit: scales per wave");
+  static_assert(!GATED_ || (NT % 2 == 0 && NW % 2 == 0 && HC % 16 == 0 && !I8_), "gated: the waves split the halves");
   static_assert(KB % (64 * WK) == 0 && KB >= 128, "k steps per wave");
-  static_assert((S - 1) * (XL + WL) < 64, "the load counter holds the stages in flight");
+  static_assert((S - 1) * (XL + WL + SL) < 64, "the load counter holds the stages in flight");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
+
+// What the account of the tiles (api.hip) knows of one.
+template <class C>
+constexpr GemmTile tile_of(double fixed) {
+  return {C::RT, C::HC, C::NC, 160 * 1024 / C::LDS, fixed, 0.3 * C::MT * C::NTE / C::DT * (C::GATED ? 2 : 1)};
+}
 
 __device__ __forceinline__ const GemmDesc &gemm_desc() {
   return *(const GemmDesc *)(const void *)__builtin_amdgcn_kernarg_segment_ptr();
@@ -92,6 +121,14 @@ __device__ __forceinline__ u32x4 rsrc_words(const void *base, uint32_t bytes) {
 // (out-of-range lanes write zeros).  Counted by vmcnt; waits are the caller's.
 __device__ __forceinline__ void dma16(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "memory", "m0");
+}
+
+// 4 bytes per lane, to LDS at lds + 4 * lane.
+__device__ __forceinline__ void dma4(u32x4 r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(r), "s"(soff)
                : "memory", "m0");
@@ -184,6 +221,35 @@ __device__ __forceinline__ void patch_order(int lin, int row_tiles, int col_tile
   const int gr = min(patch, row_tiles - group * patch);
   *ct = in / gr;
   *rt = group * patch + in - *ct * gr;
+}
+
+// A slot's weight in the device table, checked.
+struct GemmWeight {
+  const uint8_t *W;
+  const float *Ws;
+  int64_t ldw, lds;  // bytes; floats (4-bit)
+  bool ok;
+};
+template <class C>
+__device__ __forceinline__ GemmWeight load_weight(const GemmDesc &d, const GemmModule &m, int slot, int col) {
+  static_assert(sizeof(lora_weight_q4g_entry_t) == sizeof(lora_weight_entry_t), "one table stride");
+  const lora_weight_q4g_entry_t raw = reinterpret_cast<const lora_weight_q4g_entry_t *>(d.weights)[(int64_t)slot * kMaxModules + col];
+  auto wide = [](int64_t v) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(uint32_t)((uint64_t)v >> 32)) << 32) |
+                     (uint32_t)uniform((int)(uint32_t)v));
+  };
+  GemmWeight r{uniform(static_cast<const uint8_t *>(raw.W)), nullptr, wide(raw.ldw), 0, false};
+  const int64_t most = (int64_t)0xFFFFFF00 / m.d_out;  // bytes of a row
+  if constexpr (C::Q4) {
+    r.Ws = uniform(raw.Ws);
+    r.lds = wide(raw.lds);
+    r.ok = ((uintptr_t)r.W & 15) == 0 && r.ldw >= m.d_in / 2 && r.ldw % 16 == 0 && r.ldw <= most && r.Ws != nullptr &&
+           ((uintptr_t)r.Ws & 3) == 0 && r.lds >= (m.d_in >> m.group_log) && r.lds <= most / 4;
+  } else {
+    r.ok = ((uintptr_t)r.W & 15) == 0 && r.ldw >= m.d_in && r.ldw % 8 == 0 && r.ldw <= most / 2;
+    r.ldw *= 2;
+  }
+  return r;
 }
 
 template <bool I8>
@@ -389,6 +455,29 @@ __device__ __forceinline__ u32x2 pack_out(f32x4_t o) {
   else return u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
 }
 
+// Eight 4-bit weights (value j in bits 4j .. 4j+3, two's complement) as sixteenths
+// in bf16: the conversion gives q / 16 in fp32, whose upper half is exact.  One
+// operation a value and one a pair, against two and one with integers.
+__device__ __forceinline__ u32x4 q4x8_sixteenths(uint32_t q) {
+  const uint32_t odd = q >> 4;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = __builtin_amdgcn_perm(__float_as_uint(__builtin_amdgcn_cvt_off_f32_i4(odd >> (8 * i))),
+                                 __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4(q >> (8 * i))), 0x07060302u);
+  return u32x4{o[0], o[1], o[2], o[3]};
+}
+
+// act(z) = z sigma(z (c1 + c3 z^2)): SiLU with c1 = 1, c3 = 0; GELU in its tanh form
+// with c1 = 2 sqrt(2 / pi), c3 = 0.044715 c1, since (1 + tanh(t)) / 2 = sigma(2t).
+// The square is bounded so that 0 * z^2 stays 0; at 1e30 sigma is 0 or 1 already.
+// exp and the reciprocal are the hardware's, within 2^-21 relative together: a
+// 2^13th of the output's rounding.
+__device__ __forceinline__ float gate_act(float z, float c1, float c3) {
+  const float t = z * fmaf(c3, fminf(z * z, 1e30f), c1);
+  return z * __builtin_amdgcn_rcpf(1.f + __expf(-t));
+}
+
 // KT: 32-wide steps of the ranks of a delta (1: ranks up to 32, 2: up to 64; 0: no delta).
 template <class C, bool GROUPED, int KT>
 __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
@@ -403,13 +492,14 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   for (int k = 1; k < kMaxModules; ++k)
     if (k < d.n_active && (int)blockIdx.x >= d.mod[k].block_base) mi = k;
   const GemmModule m = gemm_desc().mod[mi];
+  const int half = C::GATED ? w / (C::NW / 2) : 0;  // whose rows of W this wave loads: gate's, up's
   const int local = (int)blockIdx.x - m.block_base;
 
   // the block's rows and columns
   int row0, rows, ct, slot = 0;
   const uint8_t *W;
   const float *Ws;
-  int64_t ldw;
+  int64_t ldw, lds_ = 0;  // of W, bytes; of 4-bit scales, floats
   if constexpr (GROUPED) {
     const int nseg = min(uniform(*d.num_segments), d.max_seg);
     if (blockIdx.x == 0 && w == 0)  // segments that do not fit the batch, counted once per call
@@ -434,22 +524,42 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     row0 = tile.pos0 + rt * C::RT;
     rows = min(C::RT, tile.rows - rt * C::RT);
     slot = tile.slot;
-    const lora_weight_entry_t raw = d.weights[(int64_t)slot * kMaxModules + m.col];
-    W = uniform(static_cast<const uint8_t *>(raw.W));
-    Ws = uniform(raw.Ws);
-    const int64_t ld = raw.ldw;
-    ldw = (int64_t)(((uint64_t)(uint32_t)uniform((int)(uint32_t)((uint64_t)ld >> 32)) << 32) |
-                    (uint32_t)uniform((int)(uint32_t)ld));
-    if (W == nullptr) return;  // this slot has no weight for the projection: its rows stay as they are
-    const int elt = C::I8 ? 1 : 2;
-    const bool ok = ((uintptr_t)W & 15) == 0 && ldw >= (C::I8 ? (m.d_in + 15) & ~15 : m.d_in) && ldw % (16 / elt) == 0 &&
-                    ldw <= (int64_t)0xFFFFFF00 / elt / m.d_out &&
-                    (!C::I8 || (Ws != nullptr && ((uintptr_t)Ws & 15) == 0));
-    if (!ok) {
-      if (rt == 0 && ct == 0 && t == 0) atomicAdd(d.status, 1);
-      return;
+    if constexpr (C::GATED || C::Q4) {
+      const GemmWeight own = load_weight<C>(d, m, slot, C::GATED ? gemm_desc().mod[half].col : m.col);
+      bool there = own.W != nullptr, ok = own.ok;
+      if constexpr (C::GATED) {  // gate and up: both or neither
+        const GemmWeight other = load_weight<C>(d, m, slot, gemm_desc().mod[1 - half].col);
+        if (there != (other.W != nullptr)) ok = false;
+        there |= other.W != nullptr;
+        ok &= other.ok;
+      }
+      if (!there) return;
+      if (!ok) {
+        if (rt == 0 && ct == 0 && t == 0) atomicAdd(d.status, 1);
+        return;
+      }
+      W = own.W;
+      Ws = own.Ws;
+      ldw = own.ldw;
+      lds_ = own.lds;
+    } else {
+      const lora_weight_entry_t raw = d.weights[(int64_t)slot * kMaxModules + m.col];
+      W = uniform(static_cast<const uint8_t *>(raw.W));
+      Ws = uniform(raw.Ws);
+      const int64_t ld = raw.ldw;
+      ldw = (int64_t)(((uint64_t)(uint32_t)uniform((int)(uint32_t)((uint64_t)ld >> 32)) << 32) |
+                      (uint32_t)uniform((int)(uint32_t)ld));
+      if (W == nullptr) return;  // this slot has no weight for the projection: its rows stay as they are
+      const int elt = C::I8 ? 1 : 2;
+      const bool ok = ((uintptr_t)W & 15) == 0 && ldw >= (C::I8 ? (m.d_in + 15) & ~15 : m.d_in) && ldw % (16 / elt) == 0 &&
+                      ldw <= (int64_t)0xFFFFFF00 / elt / m.d_out &&
+                      (!C::I8 || (Ws != nullptr && ((uintptr_t)Ws & 15) == 0));
+      if (!ok) {
+        if (rt == 0 && ct == 0 && t == 0) atomicAdd(d.status, 1);
+        return;
+      }
+      ldw *= elt;
     }
-    ldw *= elt;
   } else {
     int rt;
     if constexpr (C::RT >= 128) {
@@ -460,11 +570,20 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     }
     row0 = rt * C::RT;
     rows = min(C::RT, d.num_rows - row0);
-    W = m.W;
-    Ws = m.Ws;
-    ldw = m.ldw;
+    if constexpr (C::GATED) {
+      const GemmModule &mine = gemm_desc().mod[half];
+      W = mine.W;
+      Ws = mine.Ws;
+      ldw = mine.ldw;
+      lds_ = mine.ldws;
+    } else {
+      W = m.W;
+      Ws = m.Ws;
+      ldw = m.ldw;
+      lds_ = m.ldws;
+    }
   }
-  const int n0 = ct * C::NC;
+  const int n0 = ct * C::HC;
 
   // ---- this lane's pieces of a stage: offsets of the rows it loads
   // (an index past the batch is moved into it for the load; load_info drops its row)
@@ -476,6 +595,12 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   constexpr int RPI = 1024 / C::KB > 0 ? 1024 / C::KB : 1;  // rows per load instruction
   static_assert(C::KB <= 1024, "a load instruction covers whole rows");
   const int lrow = lane / C::PIECES, lslot = lane % C::PIECES;
+  constexpr int WRPI = 1024 / C::WKB;
+  const int wlrow = lane / C::WPIECES, wslot = lane % C::WPIECES;
+  // the row of W, in LDS, of a lane's i-th load, and where in LDS the load goes
+  auto wload = [&](int i) { return C::GATED ? w * C::WL + i : i * C::NW + w; };
+  auto wload_s = [&](int i) { return C::GATED ? w * C::SL + i : i * C::NW + w; };
+  auto wrow_of = [&](int i) { return wload(i) * WRPI + wlrow; };
   uint32_t xoff[C::XL], woff[C::WL];
 #pragma unroll
   for (int i = 0; i < C::XL; ++i) {
@@ -485,12 +610,30 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
     else if (d.order) b = (int)min((unsigned)d.order[b], (unsigned)(d.num_rows - 1));
     xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
+    if constexpr (C::Q4 || C::GATED) xoff[i] = r < rows ? xoff[i] : kOutOfRange;  // or nothing: zeros, no fetch
   }
 #pragma unroll
   for (int i = 0; i < C::WL; ++i) {
-    const int r = (i * C::NW + w) * RPI + lrow;
-    const int n = min(n0 + r, m.d_out - 1);
-    woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
+    const int r = wrow_of(i);
+    const int n = min(n0 + r - half * C::HC, m.d_out - 1);
+    woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((wslot ^ (r & C::WSWZ)) * 16);
+  }
+  // 4-bit: the scales of a stage, [half][group][column] in LDS
+  const int glog = C::Q4 ? m.group_log : 0;
+  const u32x4 rsc = rsrc_words(C::Q4 ? Ws : nullptr, C::Q4 ? (uint32_t)((lds_ * (m.d_out - 1) + (m.d_in >> glog)) * 4) : 0u);
+  if constexpr (C::Q4) asm volatile("s_nop 4" : : "s"(rsc));
+  constexpr int SLN = C::SL > 0 ? C::SL : 1;
+  uint32_t soffs[SLN];
+  int sgrp[SLN];
+  if constexpr (C::Q4) {
+#pragma unroll
+    for (int i = 0; i < C::SL; ++i) {
+      const int j = (C::GATED ? (w % (C::NW / 2)) * C::SL + i : i * C::NW + w) * 64 + lane;
+      const int n = min(n0 + j % C::HC, m.d_out - 1);
+      sgrp[i] = j / C::HC;
+      soffs[i] = (uint32_t)(((int64_t)n * lds_ + sgrp[i]) * 4);
+      if (sgrp[i] > 0 && (sgrp[i] << glog) >= C::KB / 2) sgrp[i] = 1 << 28;  // none in a stage of this group
+    }
   }
 
   const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
@@ -509,32 +652,44 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
       for (int i = 0; i < C::XL; ++i) {
         const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & C::SWZ);
-        dma16(rx, piece * 16 < left ? xoff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
+        const bool on = piece * 16 < left && (!(C::Q4 || C::GATED) || xoff[i] != kOutOfRange);
+        dma16(rx, on ? xoff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
       }
     }
   };
   auto issue_w = [&](int r, uint32_t at) {
-    const uint32_t soff = (uint32_t)(r * C::KB);
-    const int left = m.kbytes - r * C::KB;
-    at += lds_base + (uint32_t)w * 1024;
+    const uint32_t soff = (uint32_t)(r * C::WKB);
+    const int left = (C::Q4 ? m.kbytes / 4 : m.kbytes) - r * C::WKB;
+    at += lds_base;
     if (r < full) {
 #pragma unroll
-      for (int i = 0; i < C::WL; ++i) dma16(rw, woff[i], soff, at + i * C::NW * 1024);
+      for (int i = 0; i < C::WL; ++i) dma16(rw, woff[i], soff, at + (uint32_t)wload(i) * 1024);
     } else {
 #pragma unroll
       for (int i = 0; i < C::WL; ++i) {
-        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & C::SWZ);
-        dma16(rw, piece * 16 < left ? woff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
+        const int piece = wslot ^ (wrow_of(i) & C::WSWZ);
+        dma16(rw, piece * 16 < left ? woff[i] + soff : kOutOfRange, 0, at + (uint32_t)wload(i) * 1024);
       }
+    }
+  };
+  auto issue_s = [&](int r, uint32_t at) {
+    if constexpr (C::Q4) {
+      const int g0 = (r * (C::KB / 2)) >> glog, last = m.d_in >> glog;
+#pragma unroll
+      for (int i = 0; i < C::SL; ++i)
+        dma4(rsc, r < rounds && g0 + sgrp[i] < last ? soffs[i] + (uint32_t)g0 * 4 : kOutOfRange, 0,
+             lds_base + at + (uint32_t)wload_s(i) * 256);
     }
   };
   auto issue = [&](int r, uint32_t buf) {
     issue_x(r, buf);
     issue_w(r, buf + C::XBYTES);
+    issue_s(r, buf + C::XBYTES + C::WBYTES);
   };
 
   // this thread's row of the tile (loaded while the first stages are on their way)
-  RowInfo mine{};
+  RowInfo mine{}, mine_up{};
+  (void)mine_up;
   auto load_info = [&]() {
     if (t >= C::RT) return;
     const int at = row0 + min(t, rows - 1);
@@ -543,7 +698,8 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const bool in = (unsigned)b < (unsigned)d.num_rows;  // a stray index (segments of another batch) touches nothing
     mine.b = in && t < rows ? b : -1;
     if constexpr (C::I8) mine.xs = m.xs[in ? (GROUPED ? b / m.rows_per_x : b) : 0];
-    mine.a = -1;
+    mine.a = mine_up.a = -1;
+    mine_up.b = mine.b;
     if constexpr (DELTA) {
       // segments come in ascending slot order: later slots were dropped by the
       // build, or their segments do not fit the batch and have no v
@@ -551,14 +707,18 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
       const int a = mine.b >= 0 ? d.ids[mine.b] : -1;
       if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
-        const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + m.col];
-        if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
-          mine.a = a;
-          mine.rank = e.rank;
-          mine.fmt = e.format;
-          mine.scale = e.scale;
-          mine.B = static_cast<const uint8_t *>(e.B);
-        }
+        auto fill = [&](RowInfo &ri, int col) {
+          const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + col];
+          if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
+            ri.a = a;
+            ri.rank = e.rank;
+            ri.fmt = e.format;
+            ri.scale = e.scale;
+            ri.B = static_cast<const uint8_t *>(e.B);
+          }
+        };
+        fill(mine, m.col);
+        if constexpr (C::GATED) fill(mine_up, gemm_desc().mod[1].col);
       }
     }
   };
@@ -570,7 +730,10 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] = acc_t{0, 0, 0, 0};
 
   constexpr int KS = C::KB / 64 / C::WK;  // matrix-core steps of a wave per stage
-  const int xrow = (wr * C::MT * 16 + r_in) * C::KB, wrow = C::XBYTES + (wc * C::NT * 16 + r_in) * C::KB;
+  // the first row of this wave's column tiles in LDS (gated: of its tiles of each half), and of tile nt from there
+  const int xrow = (wr * C::MT * 16 + r_in) * C::KB;
+  const int wrow = C::XBYTES + (wc * (C::GATED ? C::NT / 2 : C::NT) * 16 + r_in) * C::WKB;
+  auto wtile = [](int nt) constexpr { return (C::GATED && nt >= C::NT / 2 ? C::HC + (nt - C::NT / 2) * 16 : nt * 16) * C::WKB; };
   if constexpr (C::PIPE) {
     // The ring has five places of one operand's stage.  In round r: w(r) and
     // x(r) in A and B (the first step's operands already in registers), w(r+1)
@@ -596,15 +759,15 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt) xa[mt] = *(const u32x4 *)(lds + B + xrow + mt * 16 * C::KB + s0);
 #pragma unroll
-    for (int nt = 0; nt < C::NT; ++nt) wa[nt] = *(const u32x4 *)(lds + A + wrow0 + nt * 16 * C::KB + s0);
+    for (int nt = 0; nt < C::NT; ++nt) wa[nt] = *(const u32x4 *)(lds + A + wrow0 + wtile(nt) + s0);
     auto round = [&](int r, bool fast) {
       const uint32_t soff = (uint32_t)((r + 2) * C::KB);
       if (!fast) issue_w(r + 2, E);
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i) {
         if (i < C::MT) xb[i] = *(const u32x4 *)(lds + B + xrow + i * 16 * C::KB + s1);
-        else wb[i - C::MT] = *(const u32x4 *)(lds + A + wrow0 + (i - C::MT) * 16 * C::KB + s1);
-        if (fast && (i & 1) == 0) dma16(rw, woff[i / 2], soff, lds_base + E + (uint32_t)w * 1024 + i / 2 * C::NW * 1024);
+        else wb[i - C::MT] = *(const u32x4 *)(lds + A + wrow0 + wtile(i - C::MT) + s1);
+        if (fast && (i & 1) == 0) dma16(rw, woff[i / 2], soff, lds_base + E + (uint32_t)wload(i / 2) * 1024);
 #pragma unroll
         for (int k = i * PER; k < (i + 1) * PER; ++k) mma_acc(wa[k / C::MT], xa[k % C::MT], acc[k / C::MT][k % C::MT]);
         __builtin_amdgcn_sched_barrier(0);
@@ -614,7 +777,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i) {
         if (i < C::MT) xa[i] = *(const u32x4 *)(lds + D + xrow + i * 16 * C::KB + s0);
-        else wa[i - C::MT] = *(const u32x4 *)(lds + Cc + wrow0 + (i - C::MT) * 16 * C::KB + s0);
+        else wa[i - C::MT] = *(const u32x4 *)(lds + Cc + wrow0 + wtile(i - C::MT) + s0);
         if (fast && (i & 1) == 0) dma16(rx, xoff[i / 2], soff, lds_base + A + (uint32_t)w * 1024 + i / 2 * C::NW * 1024);
 #pragma unroll
         for (int k = i * PER; k < (i + 1) * PER; ++k) mma_acc(wb[k / C::MT], xb[k % C::MT], acc[k / C::MT][k % C::MT]);
@@ -647,12 +810,64 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       put += C::STAGE;
     }
     load_info();
-    for (int r = 0; r < rounds; ++r) {
-      stage_barrier<(C::S - 2) * (C::XL + C::WL)>();
+    auto next_stage = [&](int r) {  // its place in LDS; the loads of a later one are on their way
+      stage_barrier<(C::S - 2) * (C::XL + C::WL + C::SL)>();
       issue(stage_of(r + C::S - 1), put);
       put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
       const uint8_t *buf = lds + get;
       get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
+      return buf;
+    };
+    if constexpr (C::Q4) {
+      // A wave multiplies CH steps of 32 inputs that share their scales, then adds
+      // the products to the sums with them: s * sum_k 16 (q / 16) x, each product
+      // exact, the scale in fp32.  CH is as long as the group and the wave's part of
+      // a stage allow, or one step.
+      auto product = [&](auto chain) {
+        constexpr int CH = decltype(chain)::value;
+        for (int r = 0; r < rounds; ++r) {
+          const uint8_t *buf = next_stage(r);
+#pragma unroll
+          for (int c = 0; c < KS / CH; ++c) {
+            u32x4 xo[CH][C::MT];
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+              for (int mt = 0; mt < C::MT; ++mt)
+                xo[i][mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB +
+                                             ((((wk * KS + c * CH + i) * 4 + g) ^ (r_in & C::SWZ)) * 16));
+            const int grp = ((wk * KS + c * CH) * 32) >> glog;  // of the stage
+#pragma unroll
+            for (int nt = 0; nt < C::NT; ++nt) {
+              const int hf = C::GATED && nt >= C::NT / 2, col = wtile(nt) / C::WKB - hf * C::HC + wc * (C::GATED ? C::NT / 2 : C::NT) * 16;
+              const f32x4_t sc = *(const f32x4_t *)(buf + C::XBYTES + C::WBYTES + hf * (C::SBYTES / 2) +
+                                                    (grp * C::HC + col + g * 4) * 4);
+              u32x4 wo[CH];
+#pragma unroll
+              for (int i = 0; i < CH; ++i)
+                wo[i] = q4x8_sixteenths(*(const uint32_t *)(buf + wrow + wtile(nt) +
+                                                            ((wk * KS + c * CH + i) ^ (r_in & C::WSWZ)) * 16 + g * 4));
+#pragma unroll
+              for (int mt = 0; mt < C::MT; ++mt) {
+                f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < CH; ++i) p = mma(wo[i], xo[i][mt], p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[nt][mt][i] = fmaf(p[i], sc[i], acc[nt][mt][i]);
+              }
+            }
+          }
+        }
+      };
+      constexpr int CH = KS < 4 ? KS : 4;
+      if ((32 * CH) >> glog <= 1) product(std::integral_constant<int, CH>{});
+      else product(std::integral_constant<int, 1>{});
+#pragma unroll
+      for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] *= 16.f;
+    } else for (int r = 0; r < rounds; ++r) {
+      const uint8_t *buf = next_stage(r);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & C::SWZ)) * 16;
@@ -660,7 +875,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt) xo[mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + slot16);
 #pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt) wo[nt] = *(const u32x4 *)(buf + wrow + nt * 16 * C::KB + slot16);
+        for (int nt = 0; nt < C::NT; ++nt) wo[nt] = *(const u32x4 *)(buf + wrow + wtile(nt) + slot16);
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -672,7 +887,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 
   // ---- sums of the k waves; the rows' descriptions
   int et0 = 0;  // first column tile this wave finishes
-  acc_t fin[C::NTE][C::MT];
+  acc_t fin[C::FIN][C::MT];
   RowInfo *info = reinterpret_cast<RowInfo *>(lds + C::RED);
   if (t < C::RT) {
     if constexpr (C::I8) {
@@ -680,6 +895,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       mine.xs = __builtin_amdgcn_frexp_mantf(mine.xs) / 127.f;
     }
     info[t] = mine;
+    if constexpr (C::GATED) info[C::RT + t] = mine_up;
   }
   if constexpr (C::WK > 1) {
     acc_t *red = reinterpret_cast<acc_t *>(lds);
@@ -691,21 +907,22 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         red[(((wk * C::WR * C::WC + grp) * C::NT + nt) * C::MT + mt) * 64 + lane] = acc[nt][mt];
     __syncthreads();
     et0 = wk * C::NTE;
-    if (et0 >= C::NT) return;
+    if (et0 >= (C::GATED ? C::NT / 2 : C::NT)) return;
 #pragma unroll
-    for (int e = 0; e < C::NTE; ++e)
+    for (int e = 0; e < C::FIN; ++e)
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) {
+        const int nt = et0 + (e >= C::NTE ? C::NT / 2 + e - C::NTE : e);
         acc_t s = acc_t{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < C::WK; ++k)
-          s += red[(((k * C::WR * C::WC + grp) * C::NT + et0 + e) * C::MT + mt) * 64 + lane];
+          s += red[(((k * C::WR * C::WC + grp) * C::NT + nt) * C::MT + mt) * 64 + lane];
         fin[e][mt] = s;
       }
   } else {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < C::NTE; ++e)
+    for (int e = 0; e < C::FIN; ++e)
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) fin[e][mt] = acc[e][mt];
   }
@@ -716,8 +933,80 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   // scale of 2^121, a scale of 2^-140); without it sum * s lies between 2^-8 and
   // 2^24, and the three roundings are the same.  The output's power of two apart
   // as well cost the prefills 2.5% (4465 -> 4575 us).
-  uint8_t *yw = lds + C::RED + 32 * C::RT + w * C::YWAVE;
+  uint8_t *yw = lds + C::RED + C::INFO + w * C::YWAVE;
   (void)yw;
+  constexpr int WNT = C::GATED ? C::NT / 2 : C::NT;  // column tiles of a wave's output
+  // v of a row's adapter, scaled, as bf16 hi + lo
+  auto load_v = [&](const float *plane, const RowInfo &ri, V8Split *v) {
+    constexpr int K = DELTA ? KT : 1;
+    const float *src = plane + (int64_t)ri.b * d.rs + g * 8;
+    f32x4_t raw[K][2];
+#pragma unroll
+    for (int ks = 0; ks < K; ++ks) {
+      const bool von = ks * 32 + g * 8 < ri.rank;
+      raw[ks][0] = von ? *(const f32x4_t *)(src + ks * 32) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      raw[ks][1] = von ? *(const f32x4_t *)(src + ks * 32 + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int ks = 0; ks < K; ++ks) {
+      float vv[8];
+      const int j0 = ks * 32 + g * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vv[i] = j0 + i < ri.rank ? raw[ks][i / 4][i % 4] * ri.scale : 0.f;
+      v[ks] = split_v8(vv);
+    }
+  };
+  // DT column tiles of a row, packed and stored (TURN: put into LDS)
+  auto put_out = [&](int mt, int e0, int nw0, int b, const f32x4_t *out) {
+    if constexpr (C::TURN) {
+      uint8_t *at = yw + (mt * 16 + r_in) * C::YROW + e0 * 32 + g * 8;
+#pragma unroll
+      for (int e = 0; e < C::DT; ++e)
+        *(u32x2 *)(at + e * 32) = pack_out<C>(out[e]);
+    } else if (b >= 0) {
+      uint16_t *y = m.y + (int64_t)b * m.ldy;
+#pragma unroll
+      for (int e = 0; e < C::DT; ++e) {
+        const int n = nw0 + e * 16 + g * 4;
+        if (n < m.d_out)
+          *(u32x2 *)(y + n) = pack_out<C>(out[e]);
+      }
+    }
+  };
+  if constexpr (C::GATED) {
+    const GemmModule &up = gemm_desc().mod[1];
+#pragma unroll
+    for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
+      const int nw0 = n0 + (wc * WNT + et0 + e0) * 16;
+      BFrag<C::DT, DELTA ? KT : 1> bg[C::AHEAD], bu[C::AHEAD];
+      (void)bg;
+      (void)bu;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
+        const int r = (wr * C::MT + mt) * 16 + r_in;
+        const RowInfo ri = info[r];
+        f32x4_t out[C::DT], by[C::DT];
+#pragma unroll
+        for (int e = 0; e < C::DT; ++e) {
+          out[e] = fin[e0 + e][mt];
+          by[e] = fin[C::NTE + e0 + e][mt];
+        }
+        if constexpr (DELTA) {
+          V8Split v[KT];
+          load_v(m.v, ri, v);
+          add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bg, out);
+          const RowInfo ru = info[C::RT + r];
+          load_v(up.v, ru, v);
+          add_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, bu, by);
+        }
+#pragma unroll
+        for (int e = 0; e < C::DT; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[e][i] = gate_act(out[e][i], d.act_c1, d.act_c3) * by[e][i];
+        put_out(mt, e0, nw0, ri.b, out);
+      }
+    }
+  } else {
 #pragma unroll
   for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
     const int nw0 = n0 + (wc * C::NT + et0 + e0) * 16;  // first column
@@ -747,43 +1036,16 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       }
       if constexpr (DELTA) {
         V8Split v[KT];
-        const float *src = m.v + (int64_t)ri.b * d.rs + g * 8;
-        f32x4_t raw[KT][2];
-#pragma unroll
-        for (int ks = 0; ks < KT; ++ks) {
-          const bool von = ks * 32 + g * 8 < ri.rank;
-          raw[ks][0] = von ? *(const f32x4_t *)(src + ks * 32) : f32x4_t{0.f, 0.f, 0.f, 0.f};
-          raw[ks][1] = von ? *(const f32x4_t *)(src + ks * 32 + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
-        }
-#pragma unroll
-        for (int ks = 0; ks < KT; ++ks) {
-          float vv[8];
-          const int j0 = ks * 32 + g * 8;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) vv[i] = j0 + i < ri.rank ? raw[ks][i / 4][i % 4] * ri.scale : 0.f;
-          v[ks] = split_v8(vv);
-        }
+        load_v(m.v, ri, v);
         add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
       }
-      if constexpr (C::TURN) {
-        uint8_t *at = yw + (mt * 16 + r_in) * C::YROW + e0 * 32 + g * 8;
-#pragma unroll
-        for (int e = 0; e < C::DT; ++e)
-          *(u32x2 *)(at + e * 32) = pack_out<C>(out[e]);
-      } else if (ri.b >= 0) {
-        uint16_t *y = m.y + (int64_t)ri.b * m.ldy;
-#pragma unroll
-        for (int e = 0; e < C::DT; ++e) {
-          const int n = nw0 + e * 16 + g * 4;
-          if (n < m.d_out)
-            *(u32x2 *)(y + n) = pack_out<C>(out[e]);
-        }
-      }
+      put_out(mt, e0, nw0, ri.b, out);
     }
+  }
   }
   if constexpr (C::TURN) {  // the wave's own rows of LDS: no barrier
     constexpr int PPR = C::NTE * 2, STEPS = C::MT * 16 * PPR / 64;  // 16-byte pieces of a row; stores
-    const int nw0 = n0 + (wc * C::NT + et0) * 16;
+    const int nw0 = n0 + (wc * WNT + et0) * 16;
 #pragma unroll 4
     for (int i = 0; i < STEPS; ++i) {
       const int at = i * 64 + lane, lr = at / PPR, piece = at % PPR;

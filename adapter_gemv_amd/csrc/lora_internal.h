@@ -182,7 +182,7 @@ struct GemmModule {
   const float *xs;      // int8: largest magnitude of each row of x (127 times its scale)
   const uint8_t *W;     // base weight [d_out] rows (not grouped)
   int64_t ldw;          // bytes
-  const float *Ws;      // int8: scale of each output
+  const float *Ws;      // int8: scale of each output; 4-bit: group scales
   uint16_t *y;
   int64_t ldy;
   const float *v;       // delta: [num_rows][rs], unscaled rank-r vectors
@@ -194,6 +194,8 @@ struct GemmModule {
   int32_t n_tiles;      // column tiles
   int32_t block_base;   // first block of this module
   int32_t rows_per_x;   // grouped: rows of the batch that share one row of x
+  int32_t group_log;    // 4-bit: log2 of the inputs that share a scale
+  int64_t ldws;         // 4-bit: floats per row of Ws [d_out][ldws]
 };
 
 struct GemmDesc {
@@ -213,7 +215,8 @@ struct GemmDesc {
   const int32_t *num_segments;
   int32_t *status;
   const lora_adapter_entry_t *table;    // delta
-  const lora_weight_entry_t *weights;   // grouped
+  const lora_weight_entry_t *weights;   // grouped (4-bit: lora_weight_q4g_entry_t)
+  float act_c1, act_c3; // gated: act(z) = z sigma(z (c1 + c3 z^2)); mod[0] is gate, mod[1] up, n_active 1
 };
 
 // Rows of up to kMaxModules distinct inputs to quantise.
@@ -235,16 +238,29 @@ struct QuantDesc {
   int32_t blocks;
 };
 
-enum GemmKind { kLinearI8 = 0, kGroupedBf16 = 1, kGroupedI8 = 2 };
+enum GemmKind {
+  kLinearI8 = 0, kGroupedBf16 = 1, kGroupedI8 = 2,
+  kGatedBf16 = 3, kGroupedGatedBf16 = 4,                                 // gated.hip
+  kLinearQ4 = 5, kGroupedQ4 = 6, kGatedQ4 = 7, kGroupedGatedQ4 = 8       // q4.hip, gated_q4.hip
+};
+constexpr bool has_delta(GemmKind k) { return k == kLinearI8 || k == kGatedBf16 || k == kLinearQ4 || k == kGatedQ4; }
+constexpr bool is_q4(GemmKind k) { return k >= kLinearQ4; }
+constexpr bool is_gated(GemmKind k) { return k == kGatedBf16 || k == kGroupedGatedBf16 || k >= kGatedQ4; }
 // Tile configurations by rows per block; index into gemm_tile().
 struct GemmTile {
-  int rows, cols;
+  int rows, cols;  // of the output
+  int wcols;       // rows of W (gated: of both)
   int per_unit;   // blocks that a compute unit holds (their LDS)
   double fixed;   // us from a block's start to its first product, and of its end
   double per_adapter;  // us of its end for each adapter among 16 rows (its waves' row tiles in turn)
 };
 constexpr int kGemmTiles = 6;
-GemmTile gemm_tile(int cfg);
+int gemm_tiles(GemmKind kind);
+GemmTile gemm_tile(GemmKind kind, int cfg);
+int gated_tiles();
+GemmTile gated_tile(int cfg);
+int q4_tiles();
+GemmTile q4_tile(bool gated, int cfg);
 // Not part of the C ABI: the tile that a call of `kind` (GemmKind) with n
 // projections of these widths takes, its rows and columns and the time that
 // the account behind the choice expects (us).  The tests of the products ask
@@ -253,6 +269,9 @@ extern "C" int32_t lora_internal_gemm_tile(int32_t kind, int32_t num_rows, int32
                                            const int32_t *d_in, const int32_t *d_out, int32_t n, int32_t *rows,
                                            int32_t *cols, double *expected_us);
 hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
+void launch_gated(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
+void launch_q4(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
+void launch_gated_q4(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
 hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream);
 // The same, launch_shrink_reduce of d, and (order not null) the rows by slot
 // into order[num_rows], in one launch.

@@ -597,6 +597,165 @@ lora_status_t lora_linear_expand_i8(const lora_linear_i8_io_t *io, uint32_t modu
                                     lora_segments_t seg, int32_t max_rank, void *ws,
                                     size_t ws_bytes, void *stream);
 
+/* One projection of a layer with a 4-bit base weight in groups of a stated
+ * length, for lora_linear_layer_q4g.  W[n][k] = Ws[n][k / group] * q[n][k], q as
+ * in lora_linear_q4_io_t (with group 128 the two hold the same weight). */
+typedef struct lora_linear_q4g_io {
+  const void *x;  /* device, bf16 [num_rows][ldx]                            */
+  int64_t ldx;
+  const void *Wq; /* device, uint8 [d_out][ldwq]: packed 4-bit weights      */
+  int64_t ldwq;   /* bytes per row: >= d_in / 2, a multiple of 16           */
+  const void *Ws; /* device, fp32 [d_out][lds]: the group scales            */
+  int64_t lds;    /* floats per row: >= d_in / group                        */
+  void *y;        /* device, bf16 [num_rows][ldy]: written, W.x + delta     */
+  int64_t ldy;
+  int32_t d_in;   /* a multiple of group                                    */
+  int32_t d_out;
+  int32_t group;    /* inputs that share a scale: 32, 64 or 128             */
+  int32_t reserved; /* set to 0 */
+} lora_linear_q4g_io_t;
+
+/*
+ * lora_linear_q4g_workspace_bytes -- workspace of lora_linear_layer_q4g for
+ * n_modules projections whose d_in sum to sum_d_in (also enough for
+ * lora_build_segments with the same rows and slots).  0 for bad arguments.
+ */
+size_t lora_linear_q4g_workspace_bytes(int32_t num_rows, int32_t num_slots,
+                                       int32_t max_rank, int64_t sum_d_in,
+                                       int32_t n_modules);
+
+/*
+ * lora_linear_layer_q4g -- lora_linear_layer_q4 for groups of 32, 64 or 128
+ * inputs and with a tile that follows the batch, from one decode row to a
+ * prefill (lora_linear_layer_q4 multiplies 128 rows at a time for any batch):
+ *     y[b] = bf16_rne( W . x[b] + scale_a * B_a . (A_a . x[b]) ).
+ * Each 4-bit value is exact on the matrix cores, each group's sum meets its
+ * scale once, in fp32.  Source: as lora_linear_layer_q4.  Every projection of a
+ * call has the same group.  A row of x that holds an infinity or a NaN reaches
+ * no other row.  Three launches on `stream`: the grouped shrink, the sum of its
+ * partials, one product.  Results are bit-reproducible; the order of a sum
+ * depends on the tile, so a row's bits may differ between batches.
+ * row_adapter and seg belong together, as for lora_linear_layer_i8.  y overlaps
+ * no input.
+ *
+ *   io           array of LORA_NUM_MODULES entries, read where module_mask
+ *                has a bit: x, Wq, y 16-byte aligned, Ws 4-byte aligned; d_out,
+ *                ldx, ldy multiples of 8; Wq and Ws below 4 GiB
+ *   ws, ws_bytes at least lora_linear_q4g_workspace_bytes(...)
+ *   other arguments as for lora_linear_layer.
+ *
+ * Errors: those of lora_linear_layer; LORA_ERR_NULL for a null Wq or Ws,
+ * LORA_ERR_ALIGN for a d_in that is not a multiple of group or an ldwq that is
+ * not a multiple of 16, LORA_ERR_SHAPE for a group that is none of the three or
+ * not the same in every projection, ldwq < d_in / 2, lds < d_in / group, a
+ * leading dimension above 2^29 or a d_out of 2^25 and more.
+ */
+lora_status_t lora_linear_layer_q4g(const lora_linear_q4g_io_t *io, uint32_t module_mask,
+                                    int32_t num_rows, const int32_t *row_adapter,
+                                    const lora_adapter_entry_t *table, int32_t num_slots,
+                                    lora_segments_t seg, int32_t max_rank, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/*
+ * The activation of a gated feed-forward block, sigma(z) = 1 / (1 + exp(-z)):
+ *   LORA_ACT_SILU       z sigma(z)
+ *   LORA_ACT_GELU_TANH  z sigma(2 sqrt(2 / pi) (z + 0.044715 z^3)), which is
+ *                       GELU in its tanh form
+ */
+typedef enum lora_activation { LORA_ACT_SILU = 0, LORA_ACT_GELU_TANH = 1 } lora_activation_t;
+
+/* The gate and up projections of a layer's feed-forward block, for
+ * lora_gated_layer. */
+typedef struct lora_gated_io {
+  const void *x;  /* device, bf16 [num_rows][ldx]                            */
+  int64_t ldx;
+  const void *Wg; /* device, bf16 [d_ff][ldwg]: gate's base weight           */
+  int64_t ldwg;
+  const void *Wu; /* device, bf16 [d_ff][ldwu]: up's base weight             */
+  int64_t ldwu;
+  void *h;        /* device, bf16 [num_rows][ldh]: written                   */
+  int64_t ldh;
+  int32_t d_in;
+  int32_t d_ff;
+} lora_gated_io_t;
+
+/* The same with 4-bit base weights, for lora_gated_layer_q4g; each weight as in
+ * lora_linear_q4g_io_t. */
+typedef struct lora_gated_q4g_io {
+  const void *x;
+  int64_t ldx;
+  const void *Wgq; /* gate: packed 4-bit weights and group scales            */
+  int64_t ldwg;
+  const void *Wgs;
+  int64_t ldsg;
+  const void *Wuq; /* up */
+  int64_t ldwu;
+  const void *Wus;
+  int64_t ldsu;
+  void *h;
+  int64_t ldh;
+  int32_t d_in;     /* a multiple of group */
+  int32_t d_ff;
+  int32_t group;    /* 32, 64 or 128 */
+  int32_t reserved; /* set to 0 */
+} lora_gated_q4g_io_t;
+
+/*
+ * lora_gated_workspace_bytes -- workspace of lora_gated_layer and
+ * lora_gated_layer_q4g (also enough for lora_build_segments with the same rows
+ * and slots).  0 for bad arguments.
+ */
+size_t lora_gated_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t max_rank,
+                                  int32_t d_in);
+
+/*
+ * lora_gated_layer -- the gated half of a layer's feed-forward block, base
+ * projections, adapter deltas, activation and product together:
+ *     g = Wg . x[b] + scale_a * Bg_a . (Ag_a . x[b])        table column LORA_GATE
+ *     u = Wu . x[b] + scale_a * Bu_a . (Au_a . x[b])        table column LORA_UP
+ *     h[b] = bf16_rne( act(g) * u )
+ * a = row_adapter[b] (rows whose id is negative or >= num_slots have the base
+ * terms only, and so has a projection whose entry has rank 0).  g, u and the
+ * activation stay in fp32; h is what lora_linear_layer takes as the down
+ * projection's x.  Source: "m07 -- Multi-Adapter (LoRA) Serving", "2. Scale
+ * Numbers" (gate, up 8192->28672 and down as three of a layer's seven
+ * projections) and "6. Deep Dive A" (the base term shared by the batch, the
+ * adapter term per row); the activation between them is not on the pages.
+ * z = -infinity gives NaN (as -infinity times 0 does).  Three launches on
+ * `stream`: the grouped shrink of both projections, the sum of its partials,
+ * one product that reads each weight and x once and writes h alone.  Any batch,
+ * from one decode row to a prefill: the tile follows the number of rows.
+ * Results are bit-reproducible.  row_adapter and seg belong together, as for
+ * lora_linear_layer_i8.  h overlaps no input.
+ *
+ *   io           x, Wg, Wu, h 16-byte aligned; d_in, d_ff and the leading
+ *                dimensions multiples of 8; each weight below 4 GiB
+ *   activation   a lora_activation_t
+ *   ws, ws_bytes at least lora_gated_workspace_bytes(...)
+ *   other arguments as for lora_linear_layer.
+ *
+ * Errors: LORA_ERR_NULL, LORA_ERR_SHAPE (sizes, an unknown activation, a leading
+ * dimension above 2^29 or a d_ff of 2^25 and more), LORA_ERR_ALIGN,
+ * LORA_ERR_RANK, LORA_ERR_WORKSPACE, LORA_ERR_LAUNCH.
+ */
+lora_status_t lora_gated_layer(const lora_gated_io_t *io, int32_t activation, int32_t num_rows,
+                               const int32_t *row_adapter, const lora_adapter_entry_t *table,
+                               int32_t num_slots, lora_segments_t seg, int32_t max_rank, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/*
+ * lora_gated_layer_q4g -- lora_gated_layer with 4-bit base weights, as in
+ * lora_linear_layer_q4g.  Wgs and Wus 4-byte aligned.
+ * Errors: those of lora_gated_layer; LORA_ERR_ALIGN for a d_in that is not a
+ * multiple of group or a weight's leading dimension that is not a multiple of 16
+ * bytes, LORA_ERR_SHAPE for a group that is none of the three.
+ */
+lora_status_t lora_gated_layer_q4g(const lora_gated_q4g_io_t *io, int32_t activation,
+                                   int32_t num_rows, const int32_t *row_adapter,
+                                   const lora_adapter_entry_t *table, int32_t num_slots,
+                                   lora_segments_t seg, int32_t max_rank, void *ws,
+                                   size_t ws_bytes, void *stream);
+
 /*
  * One entry of the device-resident table of dense weights: the whole weight of
  * one slot for one projection ("m07 ...", "9. Bottlenecks and Evolution": a hot
@@ -619,6 +778,21 @@ typedef struct lora_weight_entry {
   int64_t ldw;
   int64_t reserved; /* set to 0 */
 } lora_weight_entry_t;
+
+/* The same for 4-bit weights (lora_grouped_layer_q4g,
+ * lora_grouped_gated_layer_q4g), 32 bytes.
+ *   W    device, uint8 [d_out][ldw], 16-byte aligned, q as in
+ *        lora_linear_q4_io_t; NULL as above
+ *   Ws   device, fp32 [d_out][lds], 4-byte aligned: the group scales
+ *   ldw  bytes per row: >= d_in / 2, a multiple of 16
+ *   lds  floats per row: >= d_in / group
+ * W and Ws stay below 4 GiB. */
+typedef struct lora_weight_q4g_entry {
+  const void *W;
+  const float *Ws;
+  int64_t ldw;
+  int64_t lds;
+} lora_weight_q4g_entry_t;
 
 /* One projection of a layer for the grouped products. */
 typedef struct lora_grouped_io {
@@ -692,6 +866,45 @@ lora_status_t lora_grouped_layer_i8(const lora_grouped_io_t *io, uint32_t module
                                     int32_t num_rows, const lora_weight_entry_t *weights,
                                     int32_t num_slots, lora_segments_t seg, void *ws,
                                     size_t ws_bytes, void *stream);
+
+/*
+ * lora_grouped_layer_q4g -- lora_grouped_layer with 4-bit weights, one fp32 scale
+ * per output and group of 32, 64 or 128 inputs, and bf16 rows:
+ *     y[b][n] = bf16_rne( sum_k Ws_a[n][k / group] q_a[n][k] x[b / rows_per_x][k] ).
+ * No workspace; one launch; Speed as for lora_grouped_layer.
+ *   weights  device lora_weight_q4g_entry_t [num_slots * 7]
+ * Errors: those of lora_grouped_layer, LORA_ERR_SHAPE for a group that is none of
+ * the three, LORA_ERR_ALIGN for a d_in that is not a multiple of group.
+ */
+lora_status_t lora_grouped_layer_q4g(const lora_grouped_io_t *io, uint32_t module_mask,
+                                     int32_t num_rows, const lora_weight_q4g_entry_t *weights,
+                                     int32_t num_slots, int32_t group, lora_segments_t seg,
+                                     void *stream);
+
+/*
+ * lora_grouped_gated_layer -- the gated half of a feed-forward block with a
+ * whole gate and up weight per slot (merged adapters, experts):
+ *     h[b] = bf16_rne( act(Wg_a . x) * (Wu_a . x) ),  x = x[b / rows_per_x],
+ * for every row in a segment, a its slot; rows in no segment are not touched.
+ * Activation, rounding and range as for lora_gated_layer; segments, Speed and
+ * errors in device data as for lora_grouped_layer, except that a slot has both
+ * weights or neither: one without the other is a device-data error, counted
+ * once per segment.  No workspace; one launch.  h overlaps no input.
+ *
+ *   io       one lora_grouped_io_t: y is h, d_out d_ff
+ *   weights  device lora_weight_entry_t [num_slots * 7], columns LORA_GATE and
+ *            LORA_UP
+ * Errors: those of lora_grouped_layer, LORA_ERR_SHAPE for an unknown activation.
+ */
+lora_status_t lora_grouped_gated_layer(const lora_grouped_io_t *io, int32_t activation,
+                                       int32_t num_rows, const lora_weight_entry_t *weights,
+                                       int32_t num_slots, lora_segments_t seg, void *stream);
+
+/* The same with 4-bit weights, as in lora_grouped_layer_q4g. */
+lora_status_t lora_grouped_gated_layer_q4g(const lora_grouped_io_t *io, int32_t activation,
+                                           int32_t num_rows, const lora_weight_q4g_entry_t *weights,
+                                           int32_t num_slots, int32_t group, lora_segments_t seg,
+                                           void *stream);
 
 /* Most adapters one row may carry in lora_apply_layer_stacked. */
 #define LORA_MAX_STACK 8

@@ -1,0 +1,91 @@
+"""Inputs and 64-bit references of the 4-bit products with stated groups and the
+gated half of a feed-forward block (no test functions here).  Everything is
+torch on the CPU; the GPU tests move it over.
+
+Tolerances (u = 2^-24, half a step of fp32), beside those of dense_cases:
+  * 4-bit sums: q x is exact in fp32; the n products of a sum and the groups'
+    scales round at most n + 3 times in a row, twice u each where the matrix
+    cores cut: 2 (n + 4) u of the sum of magnitudes;
+  * activation: z sigma(t), t = z (c1 + c3 z^2).  Its derivative is at most 1.13
+    in magnitude for both kinds, so an error dz of z is at most 1.13 dz of act.
+    t's own roundings are 4 u |t| (three operations and the product with log2 e
+    that the exponential makes), of which sigma takes over (1 - sigma) relatively;
+    the exponential, the sum and the reciprocal add a unit of the last place each
+    (2 u): act_rel = (4 |t| (1 - sigma) + 8) u, doubled for the hardware's
+    exponential.  Below t = -87 the exponential passes 2^125 and sigma, at most
+    2^-125, may come out as 0;
+  * h = act(z) u: 1.13 dz |u| + (|act| + 1.13 dz) du, act_rel |h|, one product.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from tests.dense_cases import U
+
+GROUPS = (32, 64, 128)
+ACTS = ("silu", "gelu_tanh")
+
+
+def q4_weight(gen, d_out, d_in, group, pad=0, spad=0):
+    """(Wq uint8 [d_out, pitch], Ws fp32 [d_out, groups + spad], W fp64): every value from -8 to 7, junk in what no
+    weight lies in."""
+    q = torch.randint(-8, 8, (d_out, d_in), generator=gen, dtype=torch.int32)
+    pitch = -(-(d_in // 2) // 16) * 16 + pad
+    Wq = torch.randint(0, 256, (d_out, pitch), generator=gen, dtype=torch.int32).to(torch.uint8)
+    Wq[:, :d_in // 2] = ((q[:, 0::2] & 15) | ((q[:, 1::2] & 15) << 4)).to(torch.uint8)
+    n = d_in // group
+    Ws = torch.full((d_out, n + spad), float("nan"))
+    Ws[:, :n] = (torch.rand(d_out, n, generator=gen) + 0.25) * 0.3 * d_in ** -0.5
+    Ws[:, :n][torch.rand(d_out, n, generator=gen) < 0.1] *= -1
+    W = q.double() * Ws[:, :n].double().repeat_interleave(group, 1)
+    return Wq, Ws, W
+
+
+def q4_sums(x, W):
+    """(y, slack) of the 4-bit product in fp64."""
+    x = x.double()
+    return x @ W.t(), 2 * (W.shape[1] + 4) * U * (x.abs() @ W.abs().t())
+
+
+def act64(kind, z):
+    """(act, t) in fp64."""
+    z = z.double()
+    t = z if kind == "silu" else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    return z * torch.sigmoid(t), t
+
+
+def gated(kind, z, dz, u, du):
+    """(h, slack) from the projections and their slacks."""
+    a, t = act64(kind, z)
+    h = a * u
+    rel = 2 * (4 * t.abs() * torch.sigmoid(-t) + 8) * U
+    rel = torch.where(t < -87, torch.zeros_like(rel), rel)
+    slack = 1.13 * dz * u.abs() + (a.abs() + 1.13 * dz) * du + (rel + U) * h.abs() + z.abs() * u.abs() * 2.0 ** -125
+    return h, slack
+
+
+# The tile (rows, columns of the output) that a call takes: (kind, tile, lengths of the segments or rows, d_in, d_out).
+# More than one row tile and column tile, the last of each partial, and enough of k that the tile's ring is filled again.
+KINDS = ("linear_i8", "grouped", "grouped_i8", "gated", "grouped_gated", "linear_q4g", "grouped_q4g", "gated_q4g",
+         "grouped_gated_q4g")
+
+
+def tile_of(kind, rows, slots, shapes, max_segments=0):
+    """(rows, columns) of the tile that the library takes for a call of `kind` with these (d_in, d_out)."""
+    import ctypes
+
+    import adapter_gemv_amd as lg
+    n = len(shapes)
+    ints = ctypes.c_int32 * n
+    seg = lg._Seg()
+    seg.max_segments = max_segments
+    f = lg.lib().lora_internal_gemm_tile
+    f.restype = ctypes.c_int32
+    rt, ct, us = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_double()
+    got = f(ctypes.c_int32(KINDS.index(kind)), ctypes.c_int32(rows), ctypes.c_int32(slots), seg,
+            ints(*[s[0] for s in shapes]), ints(*[s[1] for s in shapes]), ctypes.c_int32(n), ctypes.byref(rt),
+            ctypes.byref(ct), ctypes.byref(us))
+    assert got >= 0
+    return rt.value, ct.value
