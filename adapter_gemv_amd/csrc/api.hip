@@ -1080,9 +1080,10 @@ lora_status_t check_adapted(const LinearArgs &m, bool q4, int32_t group) {
   return LORA_OK;
 }
 
-// Base products with adapters by the kernels of gemm_items.h: the grouped shrink
-// of the n projections, one v plane each with the rows by slot, and the product
-// (gated: one of both projections).
+// Base products with adapters by the kernels of gemm_items.h: v of the n
+// projections with the rows' order and descriptions (rows.hip; a few rows in one
+// launch, else behind the grouped shrink), and the product (gated: one of both
+// projections).
 lora_status_t adapted_call(GemmKind kind, const LinearArgs *la, const int *cols, int n, bool int8_items, int32_t group,
                            int32_t activation, int32_t num_rows, const int32_t *row_adapter,
                            const lora_adapter_entry_t *table, int32_t num_slots, const lora_segments_t &seg,
@@ -1110,16 +1111,20 @@ lora_status_t adapted_call(GemmKind kind, const LinearArgs *la, const int *cols,
   hipStream_t s = static_cast<hipStream_t>(stream);
   float *vplanes = reinterpret_cast<float *>(static_cast<char *>(ws) +
                                              ((partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255));
-  int32_t *by_slot = nullptr;
-  if (rows_by_slot(num_rows, seg))
-    by_slot = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n));
-  st = launch_phase(true, ms, n, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws, nullptr, 0, s);
-  if (st != LORA_OK) return st;
-  LayerDesc d;
-  fill_desc(d, ms, n, true, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws);
-  d.v_out = vplanes;
-  d.ldv = rs;
-  st = launched(launch_quantize_reduce(d, QuantDesc{}, row_adapter, by_slot, s));
+  char *behind = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
+  const bool few = num_rows <= kFewRows;
+  RowsDesc rows{};
+  if (rows_by_slot(num_rows, seg)) rows.order = reinterpret_cast<int32_t *>(behind);
+  rows.info = reinterpret_cast<RowInfo *>(behind + order_ws_bytes(num_rows));
+  rows.ids = row_adapter;
+  if (!few) {
+    st = launch_phase(true, ms, n, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws, nullptr, 0, s);
+    if (st != LORA_OK) return st;
+  }
+  fill_desc(rows.L, ms, n, true, num_rows, num_slots, max_rank, LORA_NUM_MODULES, table, seg, ws);
+  rows.L.v_out = vplanes;
+  rows.L.ldv = rs;
+  st = launched(launch_rows(rows, few, s));
   if (st != LORA_OK) return st;
   for (int i = 0; i < n; ++i) {
     GemmModule &gm = g.mod[i];
@@ -1134,6 +1139,7 @@ lora_status_t adapted_call(GemmKind kind, const LinearArgs *la, const int *cols,
     gm.y = static_cast<uint16_t *>(la[i].y);
     gm.ldy = la[i].ldy;
     gm.v = vplanes + (int64_t)i * num_rows * rs;
+    gm.info = rows.info + (int64_t)i * num_rows;
     gm.kbytes = la[i].d_in * 2;
     gm.d_in = la[i].d_in;
     gm.d_out = la[i].d_out;
@@ -1145,9 +1151,7 @@ lora_status_t adapted_call(GemmKind kind, const LinearArgs *la, const int *cols,
   g.row_tiles = (num_rows + gemm_tile(kind, cfg).rows - 1) / gemm_tile(kind, cfg).rows;
   g.rs = rs;
   g.max_rank = max_rank;
-  g.ids = row_adapter;
-  g.order = by_slot;
-  g.table = table;
+  g.order = rows.order;
   return gemm_launch(g, products, g.row_tiles, num_rows, num_slots, seg, kind, cfg, s);
 }
 
@@ -1241,7 +1245,8 @@ size_t lora_linear_q4g_workspace_bytes(int32_t num_rows, int32_t num_slots, int3
                                        int32_t n_modules) {
   const size_t base = lora_linear_workspace_bytes(num_rows, num_slots, max_rank, sum_d_in, n_modules);
   if (base == 0) return 0;
-  const size_t need = linear_v_end(num_rows, max_rank, sum_d_in, n_modules) + order_ws_bytes(num_rows);
+  const size_t need = linear_v_end(num_rows, max_rank, sum_d_in, n_modules) + order_ws_bytes(num_rows) +
+                      (size_t)n_modules * num_rows * sizeof(RowInfo);
   return need > base ? need : base;
 }
 

@@ -230,6 +230,14 @@ __device__ __forceinline__ const T *uniform(const T *p) {
   return (const T *)(uintptr_t)(((uint64_t)hi << 32) | lo);
 }
 
+// The segments, of a build for more rows than the batch only those that end in it.
+__device__ __forceinline__ int fitting_segments(const int32_t *num_segments, int max_seg, const int32_t *offsets,
+                                                int num_rows) {
+  int n = min(*num_segments, max_seg);
+  while (n > 0 && offsets[n] > num_rows) --n;
+  return n;
+}
+
 // Validated segment of a block: slot, first sorted row and length; false
 // (and the status word counted once) when the segments do not fit this batch.
 __device__ __forceinline__ bool load_segment(const LayerDesc &d, int s, bool count, int *a, int *pos0, int *len) {

@@ -64,7 +64,8 @@ struct GemmCfg {
   static constexpr int WKB = Q4_ ? KB / 4 : KB;        // the same of W
   static constexpr int EU = EU_;                       // waves per SIMD it is compiled for
   static constexpr int NW = WR * WC * WK, THREADS = NW * 64;
-  static constexpr int MT = RT / WR / 16, NT = NC / WC / 16;  // 16 x 16 tiles of a wave
+  static constexpr int MT = RT < 16 ? 1 : RT / WR / 16, NT = NC / WC / 16;  // 16 x 16 tiles of a wave
+  static constexpr int IR = RT < 16 ? 16 : RT;         // rows of the matrix cores' tiles (beyond RT: never stored)
   // Column tiles a wave finishes (epilogue); gated: as many of each half.
   static constexpr int NTE = GATED_ ? (NT / 2 >= WK ? NT / 2 / WK : 1) : NT >= WK ? NT / WK : 1;
   static constexpr int FIN = GATED_ ? 2 * NTE : NTE;   // their sums
@@ -72,10 +73,11 @@ struct GemmCfg {
   static constexpr int SWZ = PIECES >= 16 ? 15 : 7;    // rows whose pieces are moved against one another
   static constexpr int WPIECES = WKB / 16;
   static constexpr int WSWZ = WPIECES >= 16 ? 15 : WPIECES - 1;
-  static constexpr int XL = RT * KB / 1024 / NW, WL = NC * WKB / 1024 / NW;  // loads per wave and stage
-  // 4-bit: room for the scales of a stage in the shortest groups, and their loads of 64 per wave.
-  static constexpr int SBYTES = Q4_ ? NC * (KB / 64) * 4 : 0, SL = SBYTES / 256 / NW;
-  static constexpr int XBYTES = RT * KB, WBYTES = NC * WKB, STAGE = XBYTES + WBYTES + SBYTES;
+  static constexpr int XI = RT * KB / 1024;            // load instructions of x per stage; fewer than waves: some twice
+  static constexpr int XL = XI < NW ? 1 : XI / NW, WL = NC * WKB / 1024 / NW;  // loads per wave and stage
+  // 4-bit: the scales of 16 groups of each row of W, and the loads of them per wave.
+  static constexpr int SBYTES = Q4_ ? NC * 16 * 4 : 0, SL = SBYTES / 256 / NW;
+  static constexpr int XBYTES = RT * KB, WBYTES = NC * WKB, STAGE = XBYTES + WBYTES;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
   // A wave of at least 64 finished columns turns its outputs round in LDS and
   // stores whole lines; 8-byte pieces of 16 rows at a time cost a 256 x 256
@@ -83,17 +85,18 @@ struct GemmCfg {
   static constexpr bool TURN = NTE >= 4;
   static constexpr int YROW = NTE * 32 + 16;           // bytes of an output row in LDS
   static constexpr int YWAVE = TURN ? MT * 16 * YROW : 0;
-  static constexpr int INFO = (GATED_ ? 64 : 32) * RT;  // the rows' descriptions (gated: of both projections)
+  static constexpr int INFO = (GATED_ ? 64 : 32) * IR;  // the rows' descriptions (gated: of both projections)
   static constexpr int TAIL = RED + INFO + NW * YWAVE;  // and the rows' descriptions, when the ring is done
-  static constexpr int RING = PIPE ? 5 * XBYTES : S * STAGE;  // pipelined: five places of one operand's stage
+  static constexpr int RING = PIPE ? 5 * XBYTES : S * (STAGE + SBYTES);  // pipelined: five places of one operand's stage
   static constexpr int LDS = RING > TAIL ? RING : TAIL;
   static constexpr int DT = NTE < 4 ? NTE : 4;         // column tiles finished at a time
   // Adapters whose B is in flight or in use (delta): rows of one decode tile
   // all differ, and a wave waits for each adapter in turn; the rows of a
   // prefill tile share one, which is kept from row tile to row tile instead.
   static constexpr int AHEAD = RT >= 256 ? 1 : 4;
-  static_assert(XL >= 1 && WL >= 1 && XL * NW * 1024 == RT * KB && WL * NW * 1024 == WBYTES, "loads per wave");
-  static_assert(!Q4_ || (SL >= 1 && SL * NW * 256 == SBYTES && !I8_ && !PIPE_), "4-bit: scales per wave");
+  static_assert(WL >= 1 && XI * 1024 == RT * KB && (XI < NW ? NW % XI == 0 : XL * NW == XI) && WL * NW * 1024 == WBYTES, "loads per wave");
+  static_assert(!Q4_ || (SL >= 1 && SL * NW * 256 == SBYTES && KB <= 1024 && !I8_ && !PIPE_), "4-bit: scales per wave");
+  static_assert(RT >= 16 || (Q4_ && WR == 1 && (RT & (RT - 1)) == 0), "fewer rows than a matrix-core tile");
   static_assert(!GATED_ || (NT % 2 == 0 && NW % 2 == 0 && HC % 16 == 0 && !I8_), "gated: the waves split the halves");
   static_assert(KB % (64 * WK) == 0 && KB >= 128, "k steps per wave");
   static_assert((S - 1) * (XL + WL + SL) < 64, "the load counter holds the stages in flight");
@@ -297,26 +300,6 @@ __device__ __forceinline__ void mma_settle(f32x4_t (&t)[N]) {
   else asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
 }
 
-// The segments, of a build for more rows than the batch only those that end in it.
-__device__ __forceinline__ int fitting_segments(const int32_t *num_segments, int max_seg, const int32_t *offsets,
-                                                int num_rows) {
-  int n = min(*num_segments, max_seg);
-  while (n > 0 && offsets[n] > num_rows) --n;
-  return n;
-}
-
-// A row of the block's tile, in LDS for the epilogue.
-struct RowInfo {
-  const uint8_t *B;      // its adapter's B
-  int32_t a;             // and slot (-1: none)
-  int32_t rank;
-  int16_t fmt, xe;
-  float scale;
-  float xs;              // int8: the row's scale is xs * 2^xe
-  int32_t b;             // its place in the batch (-1: none, not stored)
-};
-static_assert(sizeof(RowInfo) == 32, "RowInfo");
-
 // The B of one adapter for DT column tiles: values and output scales.
 template <int DT, int KT>
 struct BFrag {
@@ -406,41 +389,60 @@ __device__ __forceinline__ void use_b(const RowInfo &ri, const V8Split (&v)[KT],
 // come one per lane and are handed round.
 // AHEAD == 1: f[0] may hold the last row tile's adapter, which is then not
 // loaded again.
-template <int DT, int KT, int AHEAD>
-__device__ __forceinline__ void add_delta(const GemmModule &m, const RowInfo &ri, const V8Split (&v)[KT], int n0,
-                                          BFrag<DT, KT> (&f)[AHEAD], f32x4_t (&acc)[DT]) {
-  uint64_t todo = __ballot(ri.a >= 0) & 0xffffull;
-  auto next = [&](bool *on) {  // a row of the next adapter
+// The rows of 16 whose adapter has not been met yet.
+struct DeltaRows {
+  uint64_t todo;
+  __device__ __forceinline__ int next(const RowInfo &ri, bool *on) {  // a row of the next adapter
     *on = todo != 0;
     const int l = *on ? __builtin_ctzll(todo) : 0;
     todo &= ~__ballot(ri.a == __builtin_amdgcn_readlane(ri.a, l));
     return l;
-  };
-  bool on;
+  }
+};
+__device__ __forceinline__ DeltaRows delta_rows(const RowInfo &ri) { return DeltaRows{__ballot(ri.a >= 0) & 0xffffull}; }
+
+// Request the B of the first AHEAD adapters; then add them and the others.
+template <int DT, int KT, int AHEAD>
+__device__ __forceinline__ void begin_delta(const GemmModule &m, const RowInfo &ri, int n0, DeltaRows &rows,
+                                            BFrag<DT, KT> (&f)[AHEAD]) {
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    bool on;
+    const int l = rows.next(ri, &on);
+    load_b(m, ri, l, on, n0, f[k]);
+  }
+}
+template <int DT, int KT, int AHEAD>
+__device__ __forceinline__ void finish_delta(const GemmModule &m, const RowInfo &ri, const V8Split (&v)[KT], int n0,
+                                             DeltaRows &rows, BFrag<DT, KT> (&f)[AHEAD], f32x4_t (&acc)[DT]) {
+  for (bool more = true; more;) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (f[k].a < 0) {
+        more = false;
+        break;
+      }
+      use_b(ri, v, f[k], acc);
+      bool on;
+      const int l = rows.next(ri, &on);
+      load_b(m, ri, l, on, n0, f[k]);
+    }
+  }
+}
+template <int DT, int KT, int AHEAD>
+__device__ __forceinline__ void add_delta(const GemmModule &m, const RowInfo &ri, const V8Split (&v)[KT], int n0,
+                                          BFrag<DT, KT> (&f)[AHEAD], f32x4_t (&acc)[DT]) {
+  DeltaRows rows = delta_rows(ri);
   if constexpr (AHEAD == 1) {
-    while (todo) {
-      const int l = next(&on);
+    while (rows.todo) {
+      bool on;
+      const int l = rows.next(ri, &on);
       if (__builtin_amdgcn_readlane(ri.a, l) != f[0].a) load_b(m, ri, l, true, n0, f[0]);
       use_b(ri, v, f[0], acc);
     }
   } else {
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int l = next(&on);
-      load_b(m, ri, l, on, n0, f[k]);
-    }
-    for (bool more = true; more;) {
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        if (f[k].a < 0) {
-          more = false;
-          break;
-        }
-        use_b(ri, v, f[k], acc);
-        const int l = next(&on);
-        load_b(m, ri, l, on, n0, f[k]);
-      }
-    }
+    begin_delta(m, ri, n0, rows, f);
+    finish_delta(m, ri, v, n0, rows, f, acc);
   }
 }
 
@@ -455,17 +457,23 @@ __device__ __forceinline__ u32x2 pack_out(f32x4_t o) {
   else return u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
 }
 
-// Eight 4-bit weights (value j in bits 4j .. 4j+3, two's complement) as sixteenths
-// in bf16: the conversion gives q / 16 in fp32, whose upper half is exact.  One
-// operation a value and one a pair, against two and one with integers.
-__device__ __forceinline__ u32x4 q4x8_sixteenths(uint32_t q) {
-  const uint32_t odd = q >> 4;
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = __builtin_amdgcn_perm(__float_as_uint(__builtin_amdgcn_cvt_off_f32_i4(odd >> (8 * i))),
-                                 __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4(q >> (8 * i))), 0x07060302u);
-  return u32x4{o[0], o[1], o[2], o[3]};
+// Eight 4-bit weights (value j in bits 4j .. 4j+3, two's complement) as bf16
+// values (24 + q) / 16, in the order 0 4 1 5 2 6 3 7: with its top bit turned a
+// weight is q + 8, which in the upper four bits of the significand of 1.0 makes 1 +
+// (q + 8) / 16.  Two values at a time take a shift and one operation (and, then
+// exclusive or with 1.5), eight for a register; converting each value took 15.
+// The sum over them is (sum q x + 24 sum x) / 16, so it starts from -24/16 sum x,
+// one matrix-core step for every tile of the same x.  Its rounding is that of 24
+// + |q| instead of |q|, at most 39/8 times more of an fp32 sum.
+constexpr uint32_t kQ4Less = 0xBFC0BFC0u;  // -24/16 twice
+__device__ __forceinline__ u32x4 q4x8_shifted(uint32_t q) {
+  auto two = [](uint32_t v) { return (v & 0x00780078u) ^ 0x3FC03FC0u; };
+  return u32x4{two(q << 3), two(q >> 1), two(q >> 5), two(q >> 9)};
+}
+// Eight bf16 values in that order.
+__device__ __forceinline__ u32x4 pairs_apart(u32x4 x) {
+  return u32x4{__builtin_amdgcn_perm(x.z, x.x, 0x05040100u), __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
+               __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
 }
 
 // act(z) = z sigma(z (c1 + c3 z^2)): SiLU with c1 = 1, c3 = 0; GELU in its tanh form
@@ -494,6 +502,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   const GemmModule m = gemm_desc().mod[mi];
   const int half = C::GATED ? w / (C::NW / 2) : 0;  // whose rows of W this wave loads: gate's, up's
   const int local = (int)blockIdx.x - m.block_base;
+
+  // a few rows: v and B are requested before and right behind the main loop
+  constexpr bool EARLY = DELTA && (C::Q4 || C::GATED) && C::MT == 1 && C::NTE == C::DT;
 
   // the block's rows and columns
   int row0, rows, ct, slot = 0;
@@ -587,6 +598,41 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 
   // ---- this lane's pieces of a stage: offsets of the rows it loads
   // (an index past the batch is moved into it for the load; load_info drops its row)
+  // this thread's row of the tile: its description (rows.hip) in two pieces, or (grouped) its row
+  RowInfo mine{};
+  u32x4 desc[C::GATED ? 2 : 1][2];
+  int prow = 0;
+  (void)mine;
+  (void)desc;
+  (void)prow;
+  f32x4_t vraw[C::GATED ? 2 : 1][DELTA ? KT : 1][2];
+  (void)vraw;
+  if constexpr (C::Q4 || C::GATED) {
+    const int at = row0 + min(t, rows - 1);
+    if constexpr (GROUPED) {
+      prow = d.perm[at];
+    } else {
+#pragma unroll
+      for (int k = 0; k < (C::GATED ? 2 : 1); ++k) {
+        const u32x4 *src = reinterpret_cast<const u32x4 *>((k == 0 ? m.info : gemm_desc().mod[1].info) + at);
+        desc[k][0] = src[0];
+        desc[k][1] = src[1];
+      }
+      if constexpr (EARLY) {
+        const int64_t row = (int64_t)(row0 + min(r_in, rows - 1)) * d.rs;
+#pragma unroll
+        for (int ks = 0; ks < KT; ++ks) {
+          const int j = min(ks * 32 + g * 8, d.rs - 8);  // columns past the rank are not used
+          vraw[0][ks][0] = *(const f32x4_t *)(m.v + row + j);
+          vraw[0][ks][1] = *(const f32x4_t *)(m.v + row + j + 4);
+          if constexpr (C::GATED) {
+            vraw[1][ks][0] = *(const f32x4_t *)(gemm_desc().mod[1].v + row + j);
+            vraw[1][ks][1] = *(const f32x4_t *)(gemm_desc().mod[1].v + row + j + 4);
+          }
+        }
+      }
+    }
+  }
   const u32x4 rx = rsrc_words(m.x, m.x_bytes);
   const u32x4 rw = rsrc_words(W, (uint32_t)(ldw * m.d_out));
   // the resources are written by vector instructions; the assembly that reads
@@ -602,9 +648,10 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   auto wload_s = [&](int i) { return C::GATED ? w * C::SL + i : i * C::NW + w; };
   auto wrow_of = [&](int i) { return wload(i) * WRPI + wlrow; };
   uint32_t xoff[C::XL], woff[C::WL];
+  auto xload = [&](int i) { return C::XI < C::NW ? w % C::XI : i * C::NW + w; };
 #pragma unroll
   for (int i = 0; i < C::XL; ++i) {
-    const int r = (i * C::NW + w) * RPI + lrow;
+    const int r = xload(i) * RPI + lrow;
     const int rr = min(r, rows - 1);  // past the tile: its last row again (never stored)
     int b = row0 + rr;
     if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
@@ -618,21 +665,21 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const int n = min(n0 + r - half * C::HC, m.d_out - 1);
     woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((wslot ^ (r & C::WSWZ)) * 16);
   }
-  // 4-bit: the scales of a stage, [half][group][column] in LDS
+  // 4-bit: the scales of 16 groups (a batch), 64 consecutive bytes of each row of
+  // Ws; in LDS [4 rows][group][row], so that a lane reads its four outputs' in one.
+  // (A stage's own, 4 to 32 bytes of a row each time: every load instruction met
+  // 64 lines, 7 to 36 us of the calls below.)
   const int glog = C::Q4 ? m.group_log : 0;
   const u32x4 rsc = rsrc_words(C::Q4 ? Ws : nullptr, C::Q4 ? (uint32_t)((lds_ * (m.d_out - 1) + (m.d_in >> glog)) * 4) : 0u);
   if constexpr (C::Q4) asm volatile("s_nop 4" : : "s"(rsc));
   constexpr int SLN = C::SL > 0 ? C::SL : 1;
   uint32_t soffs[SLN];
-  int sgrp[SLN];
+  auto sgroup = [&](int i) { return (lane >> 2) ^ (wload_s(i) & 3); };
   if constexpr (C::Q4) {
 #pragma unroll
     for (int i = 0; i < C::SL; ++i) {
-      const int j = (C::GATED ? (w % (C::NW / 2)) * C::SL + i : i * C::NW + w) * 64 + lane;
-      const int n = min(n0 + j % C::HC, m.d_out - 1);
-      sgrp[i] = j / C::HC;
-      soffs[i] = (uint32_t)(((int64_t)n * lds_ + sgrp[i]) * 4);
-      if (sgrp[i] > 0 && (sgrp[i] << glog) >= C::KB / 2) sgrp[i] = 1 << 28;  // none in a stage of this group
+      const int n = min(n0 + wload_s(i) * 4 + (lane & 3) - half * C::HC, m.d_out - 1);
+      soffs[i] = (uint32_t)(((int64_t)n * lds_ + sgroup(i)) * 4);
     }
   }
 
@@ -644,16 +691,16 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   auto issue_x = [&](int r, uint32_t at) {
     const uint32_t soff = (uint32_t)(r * C::KB);
     const int left = m.kbytes - r * C::KB;
-    at += lds_base + (uint32_t)w * 1024;
+    at += lds_base;
     if (r < full) {
 #pragma unroll
-      for (int i = 0; i < C::XL; ++i) dma16(rx, xoff[i], soff, at + i * C::NW * 1024);
+      for (int i = 0; i < C::XL; ++i) dma16(rx, xoff[i], soff, at + (uint32_t)xload(i) * 1024);
     } else {
 #pragma unroll
       for (int i = 0; i < C::XL; ++i) {
-        const int piece = lslot ^ (((i * C::NW + w) * RPI + lrow) & C::SWZ);
+        const int piece = lslot ^ ((xload(i) * RPI + lrow) & C::SWZ);
         const bool on = piece * 16 < left && (!(C::Q4 || C::GATED) || xoff[i] != kOutOfRange);
-        dma16(rx, on ? xoff[i] + soff : kOutOfRange, 0, at + i * C::NW * 1024);
+        dma16(rx, on ? xoff[i] + soff : kOutOfRange, 0, at + (uint32_t)xload(i) * 1024);
       }
     }
   };
@@ -672,25 +719,30 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       }
     }
   };
-  auto issue_s = [&](int r, uint32_t at) {
-    if constexpr (C::Q4) {
-      const int g0 = (r * (C::KB / 2)) >> glog, last = m.d_in >> glog;
+  // A stage's batch of scales goes with the first stage that needs it, before its
+  // operands (loads complete in order).  A place for each of the stages under way:
+  // none of them can need the batch whose place is taken.
+  auto batch_of = [&](int r) { return ((r * (C::KB / 2)) >> glog) >> 4; };
+  int s_batch = -1, s_put = 0;
+  auto issue_s = [&](int r) {
+    const int batch = batch_of(r);
+    if (r >= rounds || batch == s_batch) return;
+    s_batch = batch;
 #pragma unroll
-      for (int i = 0; i < C::SL; ++i)
-        dma4(rsc, r < rounds && g0 + sgrp[i] < last ? soffs[i] + (uint32_t)g0 * 4 : kOutOfRange, 0,
-             lds_base + at + (uint32_t)wload_s(i) * 256);
-    }
+    for (int i = 0; i < C::SL; ++i)
+      dma4(rsc, batch * 16 + sgroup(i) < (m.d_in >> glog) ? soffs[i] + (uint32_t)batch * 64 : kOutOfRange, 0,
+           lds_base + C::S * C::STAGE + s_put + (uint32_t)wload_s(i) * 256);
+    s_put = s_put + C::SBYTES == C::S * C::SBYTES ? 0 : s_put + C::SBYTES;
   };
   auto issue = [&](int r, uint32_t buf) {
+    if constexpr (C::Q4) issue_s(r);
     issue_x(r, buf);
     issue_w(r, buf + C::XBYTES);
-    issue_s(r, buf + C::XBYTES + C::WBYTES);
   };
 
   // this thread's row of the tile (loaded while the first stages are on their way)
-  RowInfo mine{}, mine_up{};
-  (void)mine_up;
   auto load_info = [&]() {
+    if constexpr (C::Q4 || C::GATED) return;
     if (t >= C::RT) return;
     const int at = row0 + min(t, rows - 1);
     const int32_t *order = GROUPED ? d.perm : d.order;
@@ -698,8 +750,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const bool in = (unsigned)b < (unsigned)d.num_rows;  // a stray index (segments of another batch) touches nothing
     mine.b = in && t < rows ? b : -1;
     if constexpr (C::I8) mine.xs = m.xs[in ? (GROUPED ? b / m.rows_per_x : b) : 0];
-    mine.a = mine_up.a = -1;
-    mine_up.b = mine.b;
+    mine.a = -1;
     if constexpr (DELTA) {
       // segments come in ascending slot order: later slots were dropped by the
       // build, or their segments do not fit the batch and have no v
@@ -707,18 +758,14 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
       const int a = mine.b >= 0 ? d.ids[mine.b] : -1;
       if ((unsigned)a < (unsigned)d.num_slots && a <= last_slot) {
-        auto fill = [&](RowInfo &ri, int col) {
-          const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + col];
-          if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
-            ri.a = a;
-            ri.rank = e.rank;
-            ri.fmt = e.format;
-            ri.scale = e.scale;
-            ri.B = static_cast<const uint8_t *>(e.B);
-          }
-        };
-        fill(mine, m.col);
-        if constexpr (C::GATED) fill(mine_up, gemm_desc().mod[1].col);
+        const lora_adapter_entry_t e = d.table[(int64_t)a * kMaxModules + m.col];
+        if (entry_ok(e, d.max_rank)) {  // a malformed entry: counted by the shrink
+          mine.a = a;
+          mine.rank = e.rank;
+          mine.fmt = e.format;
+          mine.scale = e.scale;
+          mine.B = static_cast<const uint8_t *>(e.B);
+        }
       }
     }
   };
@@ -731,8 +778,10 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 
   constexpr int KS = C::KB / 64 / C::WK;  // matrix-core steps of a wave per stage
   // the first row of this wave's column tiles in LDS (gated: of its tiles of each half), and of tile nt from there
-  const int xrow = (wr * C::MT * 16 + r_in) * C::KB;
-  const int wrow = C::XBYTES + (wc * (C::GATED ? C::NT / 2 : C::NT) * 16 + r_in) * C::WKB;
+  const int xin = C::RT < 16 ? r_in & (C::RT - 1) : r_in;  // fewer rows than a tile: each several times
+  const int xrow = (wr * C::MT * 16 + xin) * C::KB;
+  const int wcol = wc * (C::GATED ? C::NT / 2 : C::NT) * 16;
+  const int wrow = C::XBYTES + (wcol + r_in) * C::WKB;
   auto wtile = [](int nt) constexpr { return (C::GATED && nt >= C::NT / 2 ? C::HC + (nt - C::NT / 2) * 16 : nt * 16) * C::WKB; };
   if constexpr (C::PIPE) {
     // The ring has five places of one operand's stage.  In round r: w(r) and
@@ -810,53 +859,78 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       put += C::STAGE;
     }
     load_info();
-    auto next_stage = [&](int r) {  // its place in LDS; the loads of a later one are on their way
-      stage_barrier<(C::S - 2) * (C::XL + C::WL + C::SL)>();
-      issue(stage_of(r + C::S - 1), put);
-      put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
+    auto wait_stage = [&]() { stage_barrier<(C::S - 2) * (C::XL + C::WL)>(); };
+    auto take_stage = [&]() {  // its place in LDS
       const uint8_t *buf = lds + get;
       get = get + C::STAGE == C::S * C::STAGE ? 0 : get + C::STAGE;
       return buf;
     };
+    auto refill = [&](int r) {  // the loads of a later stage, to the place of the one before r
+      issue(stage_of(r + C::S - 1), put);
+      put = put + C::STAGE == C::S * C::STAGE ? 0 : put + C::STAGE;
+    };
     if constexpr (C::Q4) {
       // A wave multiplies CH steps of 32 inputs that share their scales, then adds
-      // the products to the sums with them: s * sum_k 16 (q / 16) x, each product
+      // the products to the sums with them: s * sum_k (q / 16) x, each product
       // exact, the scale in fp32.  CH is as long as the group and the wave's part of
       // a stage allow, or one step.
+      const u32x4 less = u32x4{kQ4Less, kQ4Less, kQ4Less, kQ4Less};
+      int now = -1, s_get = 0;  // the batch of scales in use and its place
+      auto scales_of = [&](int stage) {
+        if (batch_of(stage) != now) {
+          if (now >= 0) s_get = s_get + C::SBYTES == C::S * C::SBYTES ? 0 : s_get + C::SBYTES;
+          now = batch_of(stage);
+        }
+        return lds + C::S * C::STAGE + s_get + g * 256 + wcol * 64;
+      };
+      auto read_x = [&](const uint8_t *buf, int i, int mt) {
+        return *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + ((((wk * KS + i) * 4 + g) ^ (xin & C::SWZ)) * 16));
+      };
+      auto read_w = [&](const uint8_t *buf, int i, int nt) {
+        return *(const uint32_t *)(buf + wrow + wtile(nt) + ((wk * KS + i) ^ (r_in & C::WSWZ)) * 16 + g * 4);
+      };
+      // steps c * CH .. of the stage in buf
+      auto multiply = [&](auto chain, int c, int stage, const uint8_t *scales, const uint8_t *buf) {
+        constexpr int CH = decltype(chain)::value;
+        const int grp = ((stage * (C::KB / 2) + (wk * KS + c * CH) * 32) >> glog) & 15;
+        const uint8_t *sc_at = scales + ((grp ^ g) * 16);
+        u32x4 xo[CH][C::MT];
+        f32x4_t start[C::MT];
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) {
+          start[mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            xo[i][mt] = pairs_apart(read_x(buf, c * CH + i, mt));
+            start[mt] = mma(less, xo[i][mt], start[mt]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt) {
+          const f32x4_t sc = *(const f32x4_t *)(sc_at + wtile(nt) / C::WKB * 64);
+          u32x4 wo[CH];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) wo[i] = q4x8_shifted(read_w(buf, c * CH + i, nt));
+#pragma unroll
+          for (int mt = 0; mt < C::MT; ++mt) {
+            f32x4_t p = start[mt];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) p = mma(wo[i], xo[i][mt], p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][mt][i] = fmaf(p[i], sc[i], acc[nt][mt][i]);
+          }
+        }
+      };
       auto product = [&](auto chain) {
         constexpr int CH = decltype(chain)::value;
         for (int r = 0; r < rounds; ++r) {
-          const uint8_t *buf = next_stage(r);
+          wait_stage();
+          refill(r);
+          const uint8_t *buf = take_stage();
+          const int stage = stage_of(r);
+          const uint8_t *scales = scales_of(stage);
 #pragma unroll
-          for (int c = 0; c < KS / CH; ++c) {
-            u32x4 xo[CH][C::MT];
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-              for (int mt = 0; mt < C::MT; ++mt)
-                xo[i][mt] = *(const u32x4 *)(buf + xrow + mt * 16 * C::KB +
-                                             ((((wk * KS + c * CH + i) * 4 + g) ^ (r_in & C::SWZ)) * 16));
-            const int grp = ((wk * KS + c * CH) * 32) >> glog;  // of the stage
-#pragma unroll
-            for (int nt = 0; nt < C::NT; ++nt) {
-              const int hf = C::GATED && nt >= C::NT / 2, col = wtile(nt) / C::WKB - hf * C::HC + wc * (C::GATED ? C::NT / 2 : C::NT) * 16;
-              const f32x4_t sc = *(const f32x4_t *)(buf + C::XBYTES + C::WBYTES + hf * (C::SBYTES / 2) +
-                                                    (grp * C::HC + col + g * 4) * 4);
-              u32x4 wo[CH];
-#pragma unroll
-              for (int i = 0; i < CH; ++i)
-                wo[i] = q4x8_sixteenths(*(const uint32_t *)(buf + wrow + wtile(nt) +
-                                                            ((wk * KS + c * CH + i) ^ (r_in & C::WSWZ)) * 16 + g * 4));
-#pragma unroll
-              for (int mt = 0; mt < C::MT; ++mt) {
-                f32x4_t p = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < CH; ++i) p = mma(wo[i], xo[i][mt], p);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[nt][mt][i] = fmaf(p[i], sc[i], acc[nt][mt][i]);
-              }
-            }
-          }
+          for (int c = 0; c < KS / CH; ++c) multiply(chain, c, stage, scales, buf);
         }
       };
       constexpr int CH = KS < 4 ? KS : 4;
@@ -867,7 +941,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt) acc[nt][mt] *= 16.f;
     } else for (int r = 0; r < rounds; ++r) {
-      const uint8_t *buf = next_stage(r);
+      wait_stage();
+      refill(r);
+      const uint8_t *buf = take_stage();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const int slot16 = (((wk * KS + ks) * 4 + g) ^ (r_in & C::SWZ)) * 16;
@@ -888,14 +964,34 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   // ---- sums of the k waves; the rows' descriptions
   int et0 = 0;  // first column tile this wave finishes
   acc_t fin[C::FIN][C::MT];
+  BFrag<C::DT, DELTA ? KT : 1> ebf[C::GATED ? 2 : 1][EARLY ? C::AHEAD : 1];
+  DeltaRows erows[C::GATED ? 2 : 1];
+  (void)ebf;
+  (void)erows;
   RowInfo *info = reinterpret_cast<RowInfo *>(lds + C::RED);
-  if (t < C::RT) {
+  if constexpr (C::Q4 || C::GATED) {
+    const uint32_t none = 0xffffffffu;
+    u32x4 *put = reinterpret_cast<u32x4 *>(info);
+    if (t < C::IR) {
+#pragma unroll
+      for (int k = 0; k < (C::GATED && DELTA ? 2 : 1); ++k) {
+        u32x4 lo = u32x4{0u, 0u, none, 0u}, hi = u32x4{0u, 0u, 0u, none};  // no row, no adapter, rank 0
+        if constexpr (GROUPED) {
+          hi.w = t < rows && (unsigned)prow < (unsigned)d.num_rows ? (uint32_t)prow : none;
+        } else if (t < rows) {
+          lo = desc[k][0];
+          hi = desc[k][1];
+        }
+        put[(k * C::IR + t) * 2] = lo;
+        put[(k * C::IR + t) * 2 + 1] = hi;
+      }
+    }
+  } else if (t < C::RT) {
     if constexpr (C::I8) {
       mine.xe = (int16_t)__builtin_amdgcn_frexp_expf(mine.xs);
       mine.xs = __builtin_amdgcn_frexp_mantf(mine.xs) / 127.f;
     }
     info[t] = mine;
-    if constexpr (C::GATED) info[C::RT + t] = mine_up;
   }
   if constexpr (C::WK > 1) {
     acc_t *red = reinterpret_cast<acc_t *>(lds);
@@ -908,6 +1004,15 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     __syncthreads();
     et0 = wk * C::NTE;
     if (et0 >= (C::GATED ? C::NT / 2 : C::NT)) return;
+    if constexpr (EARLY) {
+      const int nw0 = n0 + (wc * (C::GATED ? C::NT / 2 : C::NT) + et0) * 16;
+#pragma unroll
+      for (int k = 0; k < (C::GATED ? 2 : 1); ++k) {
+        const RowInfo ri = info[k * C::IR + r_in];
+        erows[k] = delta_rows(ri);
+        begin_delta(m, ri, nw0, erows[k], ebf[k]);
+      }
+    }
 #pragma unroll
     for (int e = 0; e < C::FIN; ++e)
 #pragma unroll
@@ -937,9 +1042,19 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   (void)yw;
   constexpr int WNT = C::GATED ? C::NT / 2 : C::NT;  // column tiles of a wave's output
   // v of a row's adapter, scaled, as bf16 hi + lo
-  auto load_v = [&](const float *plane, const RowInfo &ri, V8Split *v) {
+  auto scale_v = [&](const f32x4_t (&raw)[DELTA ? KT : 1][2], const RowInfo &ri, V8Split *v) {
+#pragma unroll
+    for (int ks = 0; ks < (DELTA ? KT : 1); ++ks) {
+      float vv[8];
+      const int j0 = ks * 32 + g * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vv[i] = j0 + i < ri.rank ? raw[ks][i / 4][i % 4] * ri.scale : 0.f;
+      v[ks] = split_v8(vv);
+    }
+  };
+  auto load_v = [&](const float *row, const RowInfo &ri, V8Split *v) {
     constexpr int K = DELTA ? KT : 1;
-    const float *src = plane + (int64_t)ri.b * d.rs + g * 8;
+    const float *src = row + g * 8;
     f32x4_t raw[K][2];
 #pragma unroll
     for (int ks = 0; ks < K; ++ks) {
@@ -947,14 +1062,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       raw[ks][0] = von ? *(const f32x4_t *)(src + ks * 32) : f32x4_t{0.f, 0.f, 0.f, 0.f};
       raw[ks][1] = von ? *(const f32x4_t *)(src + ks * 32 + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-#pragma unroll
-    for (int ks = 0; ks < K; ++ks) {
-      float vv[8];
-      const int j0 = ks * 32 + g * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) vv[i] = j0 + i < ri.rank ? raw[ks][i / 4][i % 4] * ri.scale : 0.f;
-      v[ks] = split_v8(vv);
-    }
+    scale_v(raw, ri, v);
   };
   // DT column tiles of a row, packed and stored (TURN: put into LDS)
   auto put_out = [&](int mt, int e0, int nw0, int b, const f32x4_t *out) {
@@ -993,11 +1101,18 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         }
         if constexpr (DELTA) {
           V8Split v[KT];
-          load_v(m.v, ri, v);
-          add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bg, out);
-          const RowInfo ru = info[C::RT + r];
-          load_v(up.v, ru, v);
-          add_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, bu, by);
+          const RowInfo ru = info[C::IR + r];
+          if constexpr (EARLY) {
+            scale_v(vraw[0], ri, v);
+            finish_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, erows[0], ebf[0], out);
+            scale_v(vraw[1], ru, v);
+            finish_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, erows[1], ebf[1], by);
+          } else {
+            load_v(m.v + (int64_t)(row0 + r) * d.rs, ri, v);
+            add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bg, out);
+            load_v(up.v + (int64_t)(row0 + r) * d.rs, ru, v);
+            add_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, bu, by);
+          }
         }
 #pragma unroll
         for (int e = 0; e < C::DT; ++e)
@@ -1036,8 +1151,13 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       }
       if constexpr (DELTA) {
         V8Split v[KT];
-        load_v(m.v, ri, v);
-        add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
+        if constexpr (EARLY) {
+          scale_v(vraw[0], ri, v);
+          finish_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, erows[0], ebf[0], out);
+        } else {
+          load_v(m.v + (int64_t)(C::Q4 ? row0 + r : ri.b) * d.rs, ri, v);
+          add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
+        }
       }
       put_out(mt, e0, nw0, ri.b, out);
     }

@@ -174,6 +174,29 @@ struct OnePassDesc {
 
 hipError_t launch_onepass(const OnePassDesc &d, int grid, hipStream_t stream);
 
+// What the epilogue of a base product knows of a row.
+struct RowInfo {
+  const uint8_t *B;      // its adapter's B
+  int32_t a;             // and slot (-1: none)
+  int32_t rank;
+  int16_t fmt, xe;
+  float scale;
+  float xs;              // int8: the row's scale is xs * 2^xe
+  int32_t b;             // its place in the batch (-1: none, not stored)
+};
+static_assert(sizeof(RowInfo) == 32, "RowInfo");
+
+// What a product with adapters needs of the batch's rows (rows.hip): their order,
+// their descriptions and their v.
+struct RowsDesc {
+  LayerDesc L;          // first member: kernel_desc() reads it from the kernel arguments; v_out, ldv: the v planes
+  const int32_t *ids;
+  int32_t *order;       // written: the rows by slot; null: they stay in their own order
+  RowInfo *info;        // written: [n_active][num_rows], by place in that order (as the v planes)
+  int32_t rows_blocks;  // blocks that write the two
+  int32_t reduce_blocks;  // blocks that sum one projection's partials
+};
+
 // ---- Base products on the matrix cores (gemm_items.h): the int8 base
 // projection with its delta, and the dense products grouped by slot.
 struct GemmModule {
@@ -185,7 +208,8 @@ struct GemmModule {
   const float *Ws;      // int8: scale of each output; 4-bit: group scales
   uint16_t *y;
   int64_t ldy;
-  const float *v;       // delta: [num_rows][rs], unscaled rank-r vectors
+  const float *v;       // delta: [num_rows][rs], unscaled rank-r vectors (int8: by row; else by place in the order)
+  const RowInfo *info;  // delta, not int8: [num_rows], by place
   uint32_t x_bytes;     // size of x
   int32_t kbytes;       // bytes of a row of x and W that hold inputs, up to a multiple of 16
   int32_t d_in;
@@ -272,6 +296,10 @@ hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hi
 void launch_gated(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
 void launch_q4(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
 void launch_gated_q4(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
+// The rows' v, order and descriptions: from the shrink's partials, or (few: up to
+// kFewRows rows, in their own order) from x and the factors.
+hipError_t launch_rows(RowsDesc &d, bool few, hipStream_t stream);
+constexpr int kFewRows = 16;
 hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream);
 // The same, launch_shrink_reduce of d, and (order not null) the rows by slot
 // into order[num_rows], in one launch.

@@ -1,0 +1,174 @@
+// What a base product with adapters (gated.hip, q4.hip, gated_q4.hip) needs of the
+// batch's rows before it starts: v = A_a x of every projection, and of each row
+// its adapter's B, rank, scale and format.  Found here once, they cost the product
+// one load a row; found by its blocks (ids, segments, table, v: four loads that
+// wait for one another, behind the weights already requested) they held each block
+// back by 2 us before its first product and by 1 to 2 us after its last.
+#include "gemm_items.h"
+#include "shrink_reduce.h"
+
+namespace lora {
+namespace {
+
+// The slot up to which rows have their delta: segments come in ascending slot
+// order; later slots were dropped by the build, or their segments do not fit the
+// batch.
+__device__ __forceinline__ int last_slot(const LayerDesc &d) {
+  const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
+  return nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
+}
+
+__device__ __forceinline__ bool has_segment(const LayerDesc &d, int a, int last) {
+  return (unsigned)a < (unsigned)d.num_slots && a <= last;
+}
+
+__device__ __forceinline__ RowInfo describe(const LayerDesc &d, int b, int a, bool on, const lora_adapter_entry_t &e) {
+  RowInfo ri{};
+  ri.b = b;
+  ri.a = -1;
+  if (on && entry_ok(e, d.max_rank)) {  // a malformed entry gives no delta
+    ri.a = a;
+    ri.rank = e.rank;
+    ri.fmt = (int16_t)e.format;
+    ri.scale = e.scale;
+    ri.B = static_cast<const uint8_t *>(e.B);
+  }
+  return ri;
+}
+
+// Row b of the batch at `place` of its order.
+__device__ __forceinline__ void place_row(const RowsDesc &r, int place, int b, int last) {
+  const LayerDesc &d = r.L;
+  if (r.order) r.order[place] = b;
+  const bool in = (unsigned)b < (unsigned)d.num_rows;  // segments of another batch: the place holds no row
+  const int a = in ? r.ids[b] : -1;
+  const bool on = in && has_segment(d, a, last);
+  for (int m = 0; m < d.n_active; ++m) {
+    lora_adapter_entry_t e{};
+    if (on) e = d.table[(int64_t)a * d.table_cols + kernel_desc().mod[m].col];
+    r.info[(int64_t)m * d.num_rows + place] = describe(d, in ? b : -1, a, on, e);
+  }
+}
+
+// 256 rows.  By slot: first those of the segments, as the build sorted them, then
+// the rows without one in their own order; a block counts those before its own.
+__device__ __forceinline__ void rows_block(const RowsDesc &r, int block) {
+  __shared__ int wsum[4];
+  const LayerDesc &d = r.L;
+  const int t = threadIdx.x, lane = t & 63, w = wave_id();
+  const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
+  const int nvalid = nseg > 0 ? min(max(d.seg_offsets[nseg], 0), d.num_rows) : 0;
+  const int last = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
+  const int b = block * 256 + t;
+  if (!r.order) {
+    if (b < d.num_rows) place_row(r, b, b, last);
+    return;
+  }
+  if (b < nvalid) place_row(r, b, d.perm[b], last);
+  int before = 0;
+#pragma unroll 8
+  for (int i = t; i < block * 256; i += 256) before += !has_segment(d, r.ids[i], last);
+  const uint64_t mine = __ballot(b < d.num_rows && !has_segment(d, r.ids[min(b, d.num_rows - 1)], last));
+#pragma unroll
+  for (int k = 32; k >= 1; k /= 2) before += __shfl_xor(before, k, 64);
+  if (lane == 0) wsum[w] = before;
+  __syncthreads();
+  int base = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+  __syncthreads();
+  if (lane == 0) wsum[w] = __popcll(mine);
+  __syncthreads();
+  for (int k = 0; k < w; ++k) base += wsum[k];
+  const int at = nvalid + base + __popcll(mine & ((1ull << lane) - 1));
+  if ((mine >> lane & 1) && at < d.num_rows) place_row(r, at, b, last);
+}
+
+__global__ __launch_bounds__(256) void rows_kernel(RowsDesc r) {
+  int b = blockIdx.x;
+  if (b < r.rows_blocks) {
+    rows_block(r, b);
+    return;
+  }
+  b -= r.rows_blocks;
+  const int module = b / r.reduce_blocks;
+  shrink_reduce(r.L, b - module * r.reduce_blocks, module, r.order != nullptr);
+}
+
+// A few rows: a block for every row, projection and row of A, straight from the
+// ids; instead of the grouped shrink, its partials and their sum (two launches, 16
+// us of a token's 4-bit gate and up).  Rows that share an adapter read it again,
+// from L2.
+__global__ __launch_bounds__(256) void few_rows_kernel(RowsDesc r) {
+  __shared__ float red[4];
+  const LayerDesc &d = r.L;
+  const int t = threadIdx.x, lane = t & 63, w = wave_id();
+  const int per = d.num_rows * d.max_rank;
+  const int module = (int)blockIdx.x / per, rest = (int)blockIdx.x - module * per;
+  const int b = rest / d.max_rank, j = rest - b * d.max_rank;
+  const ModuleDesc m = kernel_desc().mod[module];
+  const int a = uniform(r.ids[b]);
+  const int last = uniform(last_slot(d));
+  const bool on = has_segment(d, a, last);
+  lora_adapter_entry_t e{};
+  if (on) {
+    const lora_adapter_entry_t raw = d.table[(int64_t)a * d.table_cols + m.col];
+    e.A = uniform(raw.A);
+    e.B = uniform(raw.B);
+    e.rank = uniform(raw.rank);
+    e.scale = uniform(raw.scale);
+    e.format = uniform(raw.format);
+  }
+  if (blockIdx.x == 0 && w == 0) {  // segments that do not fit the batch, once a call
+    const int nseg = min(*d.num_segments, d.max_seg);
+    for (int s = lane; s < nseg; s += 64) {
+      const int o0 = d.seg_offsets[s], o1 = d.seg_offsets[s + 1];
+      if ((unsigned)d.seg_adapter[s] >= (unsigned)d.num_slots || o0 < 0 || o1 <= o0 || o1 > d.num_rows) atomicAdd(d.status, 1);
+    }
+  }
+  if (j == 0 && t == 0) {
+    r.info[(int64_t)module * d.num_rows + b] = describe(d, b, a, on, e);
+    if (on && e.rank != 0 && !entry_ok(e, d.max_rank)) {  // counted by the slot's first row
+      bool first = true;
+      for (int k = 0; k < b; ++k) first &= r.ids[k] != a;
+      if (first) atomicAdd(d.status, 1);
+    }
+  }
+  if (!on || !entry_ok(e, d.max_rank) || j >= e.rank) return;  // (columns past the rank are not read)
+  const u32x4 *x = reinterpret_cast<const u32x4 *>(m.x + (int64_t)b * m.ldx);
+  const int n8 = m.d_in / 8;
+  float sum = 0.f, scale = 1.f;
+  if (e.format == LORA_FORMAT_BF16) {
+    const u32x4 *A = reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(e.A) + (int64_t)j * m.d_in);
+#pragma unroll 4
+    for (int i = t; i < n8; i += 256) sum = dot8_bf16(A[i], x[i], sum);
+  } else {
+    const uint8_t *A = static_cast<const uint8_t *>(e.A);
+    scale = reinterpret_cast<const float *>(A)[j];
+    const u32x2 *q = reinterpret_cast<const u32x2 *>(A + q8_values_offset(e.rank) + (int64_t)j * lda8_of(m.d_in));
+#pragma unroll 4
+    for (int i = t; i < n8; i += 256) sum = dot8_bf16(i8x8_to_bf16x8(q[i]), x[i], sum);
+  }
+#pragma unroll
+  for (int k = 32; k >= 1; k /= 2) sum += __shfl_xor(sum, k, 64);
+  if (lane == 0) red[w] = sum;
+  __syncthreads();
+  if (t == 0)
+    d.v_out[((int64_t)module * d.num_rows + b) * d.ldv + j] = ((red[0] + red[1]) + (red[2] + red[3])) * scale;
+}
+
+}  // namespace
+
+hipError_t launch_rows(RowsDesc &d, bool few, hipStream_t stream) {
+  const int64_t values = (int64_t)d.L.num_rows * d.L.max_rank;
+  if (few) {
+    few_rows_kernel<<<(unsigned)(values * d.L.n_active), 256, 0, stream>>>(d);
+    return hipGetLastError();
+  }
+  d.rows_blocks = (d.L.num_rows + 255) / 256;
+  d.reduce_blocks = (int)((values + 255) / 256);
+  const int64_t blocks = d.rows_blocks + (int64_t)d.reduce_blocks * d.L.n_active;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  rows_kernel<<<(unsigned)blocks, 256, 0, stream>>>(d);
+  return hipGetLastError();
+}
+
+}  // namespace lora

@@ -8,8 +8,9 @@ namespace lora {
 // Sum the k-chunk partials of each row in a segment into v[b][0..max_rank)
 // (zero past the entry's rank), for module `module` into the plane
 // v_out + module * num_rows * ldv; `block` counts blocks of 256 values.  The
-// LayerDesc is the kernel's first argument (kernel_desc).
-__device__ __forceinline__ void shrink_reduce(const LayerDesc &d, int block, int module) {
+// LayerDesc is the kernel's first argument (kernel_desc).  by_place: to the row's
+// place in the order of the slots instead of its place in the batch.
+__device__ __forceinline__ void shrink_reduce(const LayerDesc &d, int block, int module, bool by_place = false) {
   const int nseg = min(*d.num_segments, d.max_seg);
   if (nseg <= 0) return;
   const int nvalid = min(d.seg_offsets[nseg], d.num_rows);
@@ -34,7 +35,7 @@ __device__ __forceinline__ void shrink_reduce(const LayerDesc &d, int block, int
   if (ok && j < e.rank)
     for (int c = 0; c < m.n_chunks; ++c) sum += d.part[((int64_t)(m.part_base + c) * d.num_rows + p) * d.rs + j];
   const int b = d.perm[p];
-  if ((unsigned)b < (unsigned)d.num_rows) v_out[(int64_t)b * d.ldv + j] = sum;
+  if ((unsigned)b < (unsigned)d.num_rows) v_out[(int64_t)(by_place ? p : b) * d.ldv + j] = sum;
 }
 
 }  // namespace lora

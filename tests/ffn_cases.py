@@ -3,9 +3,12 @@ gated half of a feed-forward block (no test functions here).  Everything is
 torch on the CPU; the GPU tests move it over.
 
 Tolerances (u = 2^-24, half a step of fp32), beside those of dense_cases:
-  * 4-bit sums: q x is exact in fp32; the n products of a sum and the groups'
-    scales round at most n + 3 times in a row, twice u each where the matrix
-    cores cut: 2 (n + 4) u of the sum of magnitudes;
+  * 4-bit sums: a group's is formed as sum (24 + q) x - 24 sum x, every product
+    exact in fp32, in 2 G additions of partial sums of at most sum (|q| + 48) |x|,
+    each off by 2 u where the matrix cores cut: 2 (2 G + 4) u of that (times the
+    scale); the scaled groups are added up in at most n / 32 + 3 steps (n / 32
+    where a tile scales every 32 inputs), 2 u each of the sum of magnitudes, and
+    the sum's power of two is exact;
   * activation: z sigma(t), t = z (c1 + c3 z^2).  Its derivative is at most 1.13
     in magnitude for both kinds, so an error dz of z is at most 1.13 dz of act.
     t's own roundings are 4 u |t| (three operations and the product with log2 e
@@ -43,10 +46,12 @@ def q4_weight(gen, d_out, d_in, group, pad=0, spad=0):
     return Wq, Ws, W
 
 
-def q4_sums(x, W):
+def q4_sums(x, W, Ws, group):
     """(y, slack) of the 4-bit product in fp64."""
-    x = x.double()
-    return x @ W.t(), 2 * (W.shape[1] + 4) * U * (x.abs() @ W.abs().t())
+    x, n = x.double(), W.shape[1]
+    mag = x.abs() @ W.abs().t()
+    scales = Ws[:, :n // group].double().abs().repeat_interleave(group, 1)
+    return x @ W.t(), 2 * (2 * group + 4) * U * (mag + 48 * (x.abs() @ scales.t())) + 2 * (n // 32 + 4) * U * mag
 
 
 def act64(kind, z):

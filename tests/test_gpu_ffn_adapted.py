@@ -77,11 +77,12 @@ class Run:
             for col in ("gate", "up") if self.is_gated else (m,):
                 c = {"x": xs[share][0][:, :di], "A": [], "B": [], "scale": []}
                 if self.group:
-                    Wq, Ws, c["W"] = q4_weight(g, do, di, self.group, 2 * pad, pad // 8)
+                    Wq, Ws, W = q4_weight(g, do, di, self.group, 2 * pad, pad // 8)
+                    c["W"] = (W, Ws, self.group)
                     weights += [Wq.cuda(), Ws.cuda()]
                 else:
                     full = bf16(g, do, di + pad, std=di ** -0.5)
-                    c["W"] = full[:, :di]
+                    c["W"] = (full[:, :di],)
                     weights.append(full.cuda())
                 k = MODS.index(col)
                 for s in range(slots):
@@ -152,7 +153,7 @@ class Run:
     def sums(self, col, skip=()):
         """(projection, slack) in fp64; skip: slots that get no delta."""
         c = self.cpu[col]
-        y, slack = (q4_sums if self.group else grouped_bf16)(c["x"][:self.rows], c["W"])
+        y, slack = (q4_sums if self.group else grouped_bf16)(c["x"][:self.rows], *c["W"])
         for s in range(self.slots):
             at = np.nonzero(self.ids == s)[0]
             if len(at) and s not in skip and c["A"][s].shape[0]:

@@ -61,7 +61,7 @@ class Run:
                         full = bf16(g, do, di + pad, std=di ** -0.5)
                         W, dw, ds = full[:, :di], full.cuda(), None
                     self.keep.append((dw, ds))
-                    self.cpu[m]["W"][col, s] = W
+                    self.cpu[m]["W"][col, s] = (W, Ws, self.group) if self.group else (W,)
                     if s not in self.none:
                         c = MODS.index(col)
                         t["W"][s, c], t["ldw"][s, c] = dw.data_ptr(), dw.stride(0)
@@ -101,8 +101,8 @@ class Run:
         x = self.cpu[m]["x"][at // self.fan]
         sums = q4_sums if self.group else grouped_bf16
         if not self.is_gated:
-            return sums(x, self.cpu[m]["W"][m, s])
-        return gated(self.act, *sums(x, self.cpu[m]["W"]["gate", s]), *sums(x, self.cpu[m]["W"]["up", s]))
+            return sums(x, *self.cpu[m]["W"][m, s])
+        return gated(self.act, *sums(x, *self.cpu[m]["W"]["gate", s]), *sums(x, *self.cpu[m]["W"]["up", s]))
 
     def check(self, got=None, skip=()):
         got = self.run() if got is None else got
