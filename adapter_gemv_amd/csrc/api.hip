@@ -713,26 +713,39 @@ double row_tiles_expected(int64_t rows, int64_t groups, int t) {
 int pick_gemm(GemmKind kind, int64_t rows, int64_t groups, int adapters, const GemmModule *m, int n, double *expected_us) {
   const int64_t per = (rows + groups - 1) / groups;
   const int tiles = gemm_tiles(kind);
-  const double w_share = is_q4(kind) ? 0.25 : 1;  // bytes of W for one of x
+  // 4-bit: a quarter of the bytes of W, less time for a byte, and time for unpacking
+  // and multiplying it that the bytes do not tell: 0.32 ps per row, column and byte
+  // of x's k (fitted to blocks of 8192 inputs: 256 x 256 391 us, 128 x 128 by
+  // two 219, 64 x 256 by two 244, 32 x 128 by two 74, 16 x 64 by four 45)
+  const bool q4 = is_q4(kind);
+  auto work = [&](const GemmTile &t, double kbytes) {
+    if (!q4) return (t.rows + t.wcols) * kbytes / kUnitBytesPerUs;
+    return (0.4 * (t.rows + 0.25 * t.wcols) / kUnitBytesPerUs + 0.32e-6 * std::max(t.rows, 16) * t.wcols) * kbytes;
+  };
   int fit = 0;
   while (fit + 1 < tiles && gemm_tile(kind, fit).rows < per) ++fit;
   int best = 0;
   double least = 0;
   for (int cfg = 0; cfg < tiles; ++cfg) {
     const GemmTile t = gemm_tile(kind, cfg);
-    if (cfg > 0 && (t.rows > 2 * gemm_tile(kind, fit).rows || (t.rows > 128 && per <= 128))) continue;
+    if (cfg > 0 && (t.rows > std::max(16, 2 * gemm_tile(kind, fit).rows) || (t.rows > 128 && per <= 128))) continue;
     const double rt = row_tiles_expected(rows, groups, t.rows);
     double blocks = 0;
     for (int i = 0; i < n; ++i) blocks += rt * ((m[i].d_out + t.cols - 1) / t.cols);
     const double share = std::min((double)t.per_unit, std::ceil(blocks / kComputeUnits));
     double sum = 0, longest = 0;
     for (int i = 0; i < n; ++i) {
-      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + share * (t.rows + t.wcols * w_share) * (double)m[i].kbytes / kUnitBytesPerUs;
+      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + share * work(t, (double)m[i].kbytes);
       sum += rt * ((m[i].d_out + t.cols - 1) / t.cols) * one;
       longest = std::max(longest, one);
     }
     const double fill = blocks / (kComputeUnits * t.per_unit);  // rounds; the last of many overlaps the one before
-    const double us = std::max(longest, sum / blocks * (fill <= 2 ? std::ceil(fill) : fill + 0.4));
+    double us = std::max(longest, sum / blocks * (fill <= 2 ? std::ceil(fill) : fill + 0.4));
+    if (q4) {  // W read again for every row tile, at 5.5 TB/s: what few rows wait for
+      double bytes = 0;
+      for (int i = 0; i < n; ++i) bytes += rt * m[i].d_out * (double)m[i].kbytes / 4 * (is_gated(kind) ? 2 : 1);
+      us = std::max(us, bytes / 5.5e6);
+    }
     if (cfg == 0 || us < least) {
       best = cfg;
       least = us;
@@ -1039,6 +1052,7 @@ lora_status_t grouped_call(GemmKind kind, const lora_grouped_io_t *io, uint32_t 
     gm.col = c;
     gm.rows_per_x = m.rows_per_x;
     gm.group_log = is_q4(kind) ? group_log(group) : 0;
+    gm.row_most = (uint32_t)(0xFFFFFF00u / (uint32_t)m.d_out);
     if (is_gated(kind)) g.mod[1].col = LORA_UP;
     sum_d_in += m.d_in;
     ++n;
@@ -1112,9 +1126,9 @@ lora_status_t adapted_call(GemmKind kind, const LinearArgs *la, const int *cols,
   float *vplanes = reinterpret_cast<float *>(static_cast<char *>(ws) +
                                              ((partials_ws_bytes(num_rows, max_rank, sum_d_in) + 255) & ~(size_t)255));
   char *behind = static_cast<char *>(ws) + linear_v_end(num_rows, max_rank, sum_d_in, n);
-  const bool few = num_rows <= kFewRows;
+  const bool few = num_rows < kOrderRows && (double)num_rows * max_rank * sum_d_in * 4 <= kFewBytes;
   RowsDesc rows{};
-  if (rows_by_slot(num_rows, seg)) rows.order = reinterpret_cast<int32_t *>(behind);
+  if (!few && rows_by_slot(num_rows, seg)) rows.order = reinterpret_cast<int32_t *>(behind);
   rows.info = reinterpret_cast<RowInfo *>(behind + order_ws_bytes(num_rows));
   rows.ids = row_adapter;
   if (!few) {

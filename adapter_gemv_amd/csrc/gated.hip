@@ -15,7 +15,6 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::E
 using Gated16 = GemmCfg<false, 16, 64, 1, 1, 4, 512, 2, 2, false, false, true>;
 using Gated32 = GemmCfg<false, 32, 64, 1, 1, 4, 256, 3, 2, false, false, true>;
 using Gated64 = GemmCfg<false, 64, 64, 2, 2, 1, 256, 2, 2, false, false, true>;
-using Gated128n = GemmCfg<false, 128, 96, 4, 1, 1, 128, 2, 2, false, false, true>;
 using Gated128 = GemmCfg<false, 128, 128, 4, 2, 1, 128, 4, 2, false, false, true>;
 using Gated256 = GemmCfg<false, 256, 256, 2, 2, 1, 128, 2, 1, true, false, true>;
 
@@ -28,15 +27,14 @@ void launch(const GemmDesc &d, GemmKind kind, int blocks, hipStream_t s) {
 
 }  // namespace
 
-int gated_tiles() { return 6; }
+int gated_tiles() { return 5; }
 
 GemmTile gated_tile(int cfg) {
   switch (cfg) {
     case 0: return tile_of<Gated16>(6);
     case 1: return tile_of<Gated32>(6);
     case 2: return tile_of<Gated64>(6);
-    case 3: return tile_of<Gated128n>(8);
-    case 4: return tile_of<Gated128>(8);
+    case 3: return tile_of<Gated128>(8);
     default: return tile_of<Gated256>(16);
   }
 }
@@ -46,8 +44,7 @@ void launch_gated(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStre
     case 0: launch<Gated16>(d, kind, blocks, s); break;
     case 1: launch<Gated32>(d, kind, blocks, s); break;
     case 2: launch<Gated64>(d, kind, blocks, s); break;
-    case 3: launch<Gated128n>(d, kind, blocks, s); break;
-    case 4: launch<Gated128>(d, kind, blocks, s); break;
+    case 3: launch<Gated128>(d, kind, blocks, s); break;
     default: launch<Gated256>(d, kind, blocks, s); break;
   }
 }

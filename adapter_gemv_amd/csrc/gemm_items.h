@@ -89,11 +89,11 @@ struct GemmCfg {
   static constexpr int TAIL = RED + INFO + NW * YWAVE;  // and the rows' descriptions, when the ring is done
   static constexpr int RING = PIPE ? 5 * XBYTES : S * (STAGE + SBYTES);  // pipelined: five places of one operand's stage
   static constexpr int LDS = RING > TAIL ? RING : TAIL;
-  static constexpr int DT = NTE < 4 ? NTE : 4;         // column tiles finished at a time
+  static constexpr int DT = NTE < 4 ? NTE : Q4_ && RT >= 64 ? 2 : 4;  // column tiles finished at a time
   // Adapters whose B is in flight or in use (delta): rows of one decode tile
   // all differ, and a wave waits for each adapter in turn; the rows of a
   // prefill tile share one, which is kept from row tile to row tile instead.
-  static constexpr int AHEAD = RT >= 256 ? 1 : 4;
+  static constexpr int AHEAD = RT >= 256 ? 1 : Q4_ && RT >= 64 ? 2 : 4;
   static_assert(WL >= 1 && XI * 1024 == RT * KB && (XI < NW ? NW % XI == 0 : XL * NW == XI) && WL * NW * 1024 == WBYTES, "loads per wave");
   static_assert(!Q4_ || (SL >= 1 && SL * NW * 256 == SBYTES && KB <= 1024 && !I8_ && !PIPE_), "4-bit: scales per wave");
   static_assert(RT >= 16 || (Q4_ && WR == 1 && (RT & (RT - 1)) == 0), "fewer rows than a matrix-core tile");
@@ -150,15 +150,18 @@ struct TileOf {
   int slot, pos0, rows;  // segment's slot, first sorted row and rows
   int first, tiles;      // its first tile's number, and its tiles
 };
-template <int RT>
+// AT_ONCE: the arrays are read as far as they may reach, beside the number of
+// segments instead of after it.
+template <int RT, bool AT_ONCE>
 __device__ __forceinline__ int seg_tiles(const GemmDesc &d, int s, int nseg, int *slot, int *o0, int *len) {
   *slot = -1;
   *o0 = 0;
   *len = 0;
-  if (s >= nseg) return 0;
+  if (s >= (AT_ONCE ? d.max_seg : nseg)) return 0;
   *slot = d.seg_adapter[s];
   *o0 = d.seg_offsets[s];
   *len = d.seg_offsets[s + 1] - *o0;
+  if (AT_ONCE && s >= nseg) *len = 0;
   const bool ok = (unsigned)*slot < (unsigned)d.num_slots && *o0 >= 0 && *len > 0 && *o0 + *len <= d.num_rows;
   if (!ok) *len = 0;
   return (*len + RT - 1) / RT;
@@ -171,23 +174,23 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {  // inclusive
   }
   return v;
 }
-template <int RT>
+template <int RT, bool AT_ONCE>
 __device__ __forceinline__ int total_tiles(const GemmDesc &d, int nseg) {
   const int lane = threadIdx.x & 63;
   int total = 0;
   for (int s0 = 0; s0 < nseg; s0 += 64) {
     int slot, o0, len;
-    total += __builtin_amdgcn_readlane(wave_scan(seg_tiles<RT>(d, s0 + lane, nseg, &slot, &o0, &len), lane), 63);
+    total += __builtin_amdgcn_readlane(wave_scan(seg_tiles<RT, AT_ONCE>(d, s0 + lane, nseg, &slot, &o0, &len), lane), 63);
   }
   return total;
 }
-template <int RT>
+template <int RT, bool AT_ONCE>
 __device__ __forceinline__ bool find_tile(const GemmDesc &d, int nseg, int t, TileOf *out) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int s0 = 0; s0 < nseg; s0 += 64) {
     int slot, o0, len;
-    const int n = seg_tiles<RT>(d, s0 + lane, nseg, &slot, &o0, &len);
+    const int n = seg_tiles<RT, AT_ONCE>(d, s0 + lane, nseg, &slot, &o0, &len);
     const int upto = before + wave_scan(n, lane);
     const uint64_t hit = __ballot(t < upto && n > 0);
     if (hit) {
@@ -242,7 +245,7 @@ __device__ __forceinline__ GemmWeight load_weight(const GemmDesc &d, const GemmM
                      (uint32_t)uniform((int)(uint32_t)v));
   };
   GemmWeight r{uniform(static_cast<const uint8_t *>(raw.W)), nullptr, wide(raw.ldw), 0, false};
-  const int64_t most = (int64_t)0xFFFFFF00 / m.d_out;  // bytes of a row
+  const int64_t most = m.row_most;  // bytes of a row
   if constexpr (C::Q4) {
     r.Ws = uniform(raw.Ws);
     r.lds = wide(raw.lds);
@@ -511,6 +514,12 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   const uint8_t *W;
   const float *Ws;
   int64_t ldw, lds_ = 0;  // of W, bytes; of 4-bit scales, floats
+  constexpr int RPI = 1024 / C::KB > 0 ? 1024 / C::KB : 1;  // rows per load instruction
+  static_assert(C::KB <= 1024, "a load instruction covers whole rows");
+  const int lrow = lane / C::PIECES, lslot = lane % C::PIECES;
+  auto xload = [&](int i) { return C::XI < C::NW ? w % C::XI : i * C::NW + w; };
+  int xperm[C::XL];  // grouped: the rows that this lane loads
+  (void)xperm;
   if constexpr (GROUPED) {
     const int nseg = min(uniform(*d.num_segments), d.max_seg);
     if (blockIdx.x == 0 && w == 0)  // segments that do not fit the batch, counted once per call
@@ -521,21 +530,23 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     int rt;
     TileOf tile;
     if constexpr (C::RT >= 128) {
-      const int total = total_tiles<C::RT>(d, nseg);
+      const int total = total_tiles<C::RT, C::Q4 || C::GATED>(d, nseg);
       if (local >= total * m.n_tiles) return;
       const int lin = xcd_order(local, total * m.n_tiles);
-      if (!find_tile<C::RT>(d, nseg, lin / m.n_tiles, &tile)) return;
+      if (!find_tile<C::RT, C::Q4 || C::GATED>(d, nseg, lin / m.n_tiles, &tile)) return;
       patch_order(lin - tile.first * m.n_tiles, tile.tiles, m.n_tiles, &rt, &ct);
     } else {
       rt = local / m.n_tiles;
       ct = local - rt * m.n_tiles;
-      if (!find_tile<C::RT>(d, nseg, rt, &tile)) return;
+      if (!find_tile<C::RT, C::Q4 || C::GATED>(d, nseg, rt, &tile)) return;
       rt -= tile.first;
     }
     row0 = tile.pos0 + rt * C::RT;
     rows = min(C::RT, tile.rows - rt * C::RT);
     slot = tile.slot;
     if constexpr (C::GATED || C::Q4) {
+#pragma unroll
+      for (int i = 0; i < C::XL; ++i) xperm[i] = d.perm[row0 + min(xload(i) * RPI + lrow, rows - 1)];
       const GemmWeight own = load_weight<C>(d, m, slot, C::GATED ? gemm_desc().mod[half].col : m.col);
       bool there = own.W != nullptr, ok = own.ok;
       if constexpr (C::GATED) {  // gate and up: both or neither
@@ -638,9 +649,6 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   // the resources are written by vector instructions; the assembly that reads
   // them needs 5 wait states after those, which the compiler does not count
   asm volatile("s_nop 4" : : "s"(rx), "s"(rw));
-  constexpr int RPI = 1024 / C::KB > 0 ? 1024 / C::KB : 1;  // rows per load instruction
-  static_assert(C::KB <= 1024, "a load instruction covers whole rows");
-  const int lrow = lane / C::PIECES, lslot = lane % C::PIECES;
   constexpr int WRPI = 1024 / C::WKB;
   const int wlrow = lane / C::WPIECES, wslot = lane % C::WPIECES;
   // the row of W, in LDS, of a lane's i-th load, and where in LDS the load goes
@@ -648,13 +656,15 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   auto wload_s = [&](int i) { return C::GATED ? w * C::SL + i : i * C::NW + w; };
   auto wrow_of = [&](int i) { return wload(i) * WRPI + wlrow; };
   uint32_t xoff[C::XL], woff[C::WL];
-  auto xload = [&](int i) { return C::XI < C::NW ? w % C::XI : i * C::NW + w; };
 #pragma unroll
   for (int i = 0; i < C::XL; ++i) {
     const int r = xload(i) * RPI + lrow;
     const int rr = min(r, rows - 1);  // past the tile: its last row again (never stored)
     int b = row0 + rr;
-    if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
+    if constexpr (GROUPED && (C::Q4 || C::GATED)) {
+      b = (int)min((unsigned)xperm[i], (unsigned)(d.num_rows - 1));
+      if (m.rows_per_x > 1) b /= m.rows_per_x;
+    } else if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
     else if (d.order) b = (int)min((unsigned)d.order[b], (unsigned)(d.num_rows - 1));
     xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
     if constexpr (C::Q4 || C::GATED) xoff[i] = r < rows ? xoff[i] : kOutOfRange;  // or nothing: zeros, no fetch
@@ -964,7 +974,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   // ---- sums of the k waves; the rows' descriptions
   int et0 = 0;  // first column tile this wave finishes
   acc_t fin[C::FIN][C::MT];
-  BFrag<C::DT, DELTA ? KT : 1> ebf[C::GATED ? 2 : 1][EARLY ? C::AHEAD : 1];
+  // adapters of the rows whose B is under way (more registers for four rows: 57 -> 73 us of a token's gate and up)
+  constexpr int EA = !EARLY ? 1 : C::RT < 16 ? 2 : KT == 1 ? 8 : 4;
+  BFrag<C::DT, DELTA ? KT : 1> ebf[C::GATED ? 2 : 1][EA];
   DeltaRows erows[C::GATED ? 2 : 1];
   (void)ebf;
   (void)erows;
@@ -1104,14 +1116,23 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
           const RowInfo ru = info[C::IR + r];
           if constexpr (EARLY) {
             scale_v(vraw[0], ri, v);
-            finish_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, erows[0], ebf[0], out);
+            finish_delta<C::DT, KT, EA>(m, ri, v, nw0, erows[0], ebf[0], out);
             scale_v(vraw[1], ru, v);
-            finish_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, erows[1], ebf[1], by);
-          } else {
+            finish_delta<C::DT, KT, EA>(m, ru, v, nw0, erows[1], ebf[1], by);
+          } else if constexpr (C::AHEAD == 1) {
             load_v(m.v + (int64_t)(row0 + r) * d.rs, ri, v);
             add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bg, out);
             load_v(up.v + (int64_t)(row0 + r) * d.rs, ru, v);
             add_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, bu, by);
+          } else {  // both projections' B under way at once
+            DeltaRows rg = delta_rows(ri), rup = delta_rows(ru);
+            V8Split vu[KT];
+            load_v(m.v + (int64_t)(row0 + r) * d.rs, ri, v);
+            load_v(up.v + (int64_t)(row0 + r) * d.rs, ru, vu);
+            begin_delta(m, ri, nw0, rg, bg);
+            begin_delta(m, ru, nw0, rup, bu);
+            finish_delta(m, ri, v, nw0, rg, bg, out);
+            finish_delta(m, ru, vu, nw0, rup, bu, by);
           }
         }
 #pragma unroll
@@ -1153,7 +1174,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         V8Split v[KT];
         if constexpr (EARLY) {
           scale_v(vraw[0], ri, v);
-          finish_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, erows[0], ebf[0], out);
+          finish_delta<C::DT, KT, EA>(m, ri, v, nw0, erows[0], ebf[0], out);
         } else {
           load_v(m.v + (int64_t)(C::Q4 ? row0 + r : ri.b) * d.rs, ri, v);
           add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);

@@ -219,6 +219,7 @@ struct GemmModule {
   int32_t block_base;   // first block of this module
   int32_t rows_per_x;   // grouped: rows of the batch that share one row of x
   int32_t group_log;    // 4-bit: log2 of the inputs that share a scale
+  uint32_t row_most;    // grouped, not int8: bytes of a row of W that keep it below 4 GiB
   int64_t ldws;         // 4-bit: floats per row of Ws [d_out][ldws]
 };
 
@@ -296,10 +297,11 @@ hipError_t launch_gemm(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hi
 void launch_gated(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
 void launch_q4(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
 void launch_gated_q4(const GemmDesc &d, GemmKind kind, int cfg, int blocks, hipStream_t stream);
-// The rows' v, order and descriptions: from the shrink's partials, or (few: up to
-// kFewRows rows, in their own order) from x and the factors.
+// The rows' v, order and descriptions: from the shrink's partials, or (few: fewer
+// than kOrderRows rows, in their own order) from x and the factors, where that reads
+// at most kFewBytes (a row of A and x for every row and rank, mostly from L2).
 hipError_t launch_rows(RowsDesc &d, bool few, hipStream_t stream);
-constexpr int kFewRows = 16;
+constexpr double kFewBytes = 192e6;
 hipError_t launch_quantize(const QuantDesc &d, hipStream_t stream);
 // The same, launch_shrink_reduce of d, and (order not null) the rows by slot
 // into order[num_rows], in one launch.
