@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 import adapter_gemv_amd as lg
+from tests.ffn_cases import TILE_SLOTS, TILES, tile_of
 from tests.test_dense_abi import ALIGN, BIG, MODULE, NULL, OK, P, RANK, SHAPE, WS, _on_gpu, seg
 
 LIN = dict(x=P, ldx=256, Wq=P, ldwq=128, Ws=P, lds=4, y=P, ldy=128, d_in=256, d_out=128, group=64, reserved=0)
@@ -238,3 +239,22 @@ def test_grouped_calls_refuse_short_tables_and_matrices(x, y, table, fan, what):
                  lambda: lg.grouped_gated_layer_q4g(io, 4, weights, 3, _seg(), 32)):
         with pytest.raises(ValueError, match=what):
             call()
+
+
+@pytest.mark.parametrize("kind,tile,rows,d_in,d_out", TILES)
+def test_batches_take_their_tile(kind, tile, rows, d_in, d_out):
+    most = rows if isinstance(rows, int) else max(rows)
+    if isinstance(rows, int):
+        assert tile_of(kind, rows, TILE_SLOTS, [(d_in, d_out)]) == tile
+    else:
+        assert tile_of(kind, sum(rows), len(rows), [(d_in, d_out)]) == tile
+    assert most > tile[0] and most % tile[0] and d_out > tile[1] and d_out % tile[1]
+
+
+def test_every_tile_has_a_batch():
+    bf16 = [(16, 32), (32, 32), (64, 32), (128, 64), (256, 128)]
+    q4 = [(4, 32), (4, 64), (16, 64), (16, 128), (32, 128), (64, 256), (256, 256)]
+    want = {"gated": bf16, "grouped_gated": bf16, "linear_q4g": q4, "grouped_q4g": q4}
+    want["gated_q4g"] = want["grouped_gated_q4g"] = [(r, c // 2) for r, c in q4]
+    for kind, tiles in want.items():
+        assert sorted(c[1] for c in TILES if c[0] == kind) == tiles, kind

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests.dense_cases import MODS, bf16, close, delta, gen, grouped_bf16, ids_of
-from tests.ffn_cases import ACTS, GROUPS, gated, q4_sums, q4_weight
+from tests.ffn_cases import ACTS, GROUPS, TILE_SLOTS, TILES, gated, q4_sums, q4_weight
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -182,6 +182,31 @@ def one(d_in, d_out):
                                         (260, 3), (700, 9), (300, 150)])
 def test_rows(form, rows, slots):
     Run(form, rows, slots, one(264, 136), [5, 16, 0, 32], seed=rows).check()
+
+
+@pytest.mark.parametrize("group,rank", [(32, 48), (128, 16)])
+@pytest.mark.parametrize("kind,tile,rows,d_in,d_out", [c for c in TILES if not c[0].startswith("grouped")])
+def test_every_tile(kind, tile, rows, d_in, d_out, group, rank):
+    if not kind.endswith("q4g"):
+        group = 0
+    Run(("gated" in kind, group), rows, TILE_SLOTS, one(d_in, d_out), rank, seed=tile[0], fmt="both").check()
+
+
+@forms
+@pytest.mark.parametrize("rows,rank", [(15, 64), (48, 16), (63, 64), (64, 16)])
+def test_either_way_to_v(form, rows, rank):
+    # few rows without the grouped shrink, and the same sizes past its bound of work or rows
+    # (the 63 rows with the longer d_in: past 192 MB of factors and x)
+    Run(form, rows, 20, one(4104 if form[1] == 0 else 4096, 72), rank, seed=rows, fmt="both").check()
+    if rows == 63:
+        Run(form, rows, 20, one(16384, 40), rank, seed=rows, fmt="both").check()
+
+
+@pytest.mark.parametrize("is_gated,group", [(False, 32), (False, 64), (False, 128), (True, 0), (True, 32), (True, 128)])
+@pytest.mark.parametrize("rows", [1, 4, 16])
+def test_few_rows_over_a_long_input(is_gated, group, rows):
+    # blocks start at different places along k and come round; many batches of scales
+    Run((is_gated, group), rows, 3, one(8192 + (group or 8), 2056), 16, seed=rows).check()
 
 
 @forms

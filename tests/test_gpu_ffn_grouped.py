@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests.dense_cases import MODS, bf16, close, gen, grouped_bf16, ids_of
-from tests.ffn_cases import ACTS, GROUPS, gated, q4_sums, q4_weight
+from tests.ffn_cases import ACTS, GROUPS, TILES, gated, q4_sums, q4_weight
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -159,6 +159,60 @@ def test_widths(form, d_in, d_out, rows):
 def test_groups(is_gated, group, groups, rows):
     # every length of a group, widths that end inside a stage of every tile
     Run((is_gated, group), ids_of("mixed", rows, 2, groups), 2, one(group * groups, 72), seed=groups).check()
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("kind,tile,lengths,d_in,d_out", [c for c in TILES if c[0].startswith("grouped")])
+def test_every_tile(kind, tile, lengths, d_in, d_out, group):
+    if not kind.endswith("q4g"):
+        group = 0
+    Run(("gated" in kind, group), ragged(lengths, 2), len(lengths), one(d_in, d_out), seed=tile[0], act="gelu_tanh").check()
+
+
+@pytest.mark.parametrize("is_gated,group", [(True, 0), (False, 32), (True, 128)])
+@pytest.mark.parametrize("rows", [3, 40, 300])
+def test_a_weight_of_almost_4_gib(is_gated, group, rows):
+    # offsets past 2^31 and up to the last rows of W; outputs sampled
+    d_in = 8192
+    d_out = (0xFFFFFF00 // (d_in // 2 if group else 2 * d_in)) // 8 * 8
+    x = bf16(gen(1), rows, d_in)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    t = np.zeros((1, 7), lg.WEIGHT_Q4G_ENTRY_DTYPE)
+    keep, cols = {}, ("gate", "up") if is_gated else ("gate",)
+    at = torch.unique(torch.cat([torch.arange(8), torch.randint(0, d_out, (40,), generator=gen(2)),
+                                 torch.arange(d_out - 24, d_out), torch.tensor([d_out // 2 - 1, d_out // 2])]))
+    for c in cols:
+        k = MODS.index(c)
+        if group:
+            W = torch.randint(0, 256, (d_out, d_in // 2), generator=g, device="cuda", dtype=torch.uint8)
+            S = torch.rand(d_out, d_in // group, generator=g, device="cuda") * 0.3 * d_in ** -0.5
+            t["Ws"][0, k], t["lds"][0, k] = S.data_ptr(), S.stride(0)
+            w = W[at.cuda()].cpu().to(torch.int32)
+            q = torch.stack([w & 15, w >> 4], -1).view(len(at), -1)
+            q = torch.where(q > 7, q - 16, q)
+            s = S[at.cuda()].cpu()
+            keep[c] = (W, S, (q.double() * s.double().repeat_interleave(group, 1), s, group))
+        else:
+            W = torch.empty(d_out, d_in, dtype=torch.bfloat16, device="cuda").normal_(0, d_in ** -0.5, generator=g)
+            keep[c] = (W, None, (W[at.cuda()].cpu(),))
+        t["W"][0, k], t["ldw"][0, k] = W.data_ptr(), W.stride(0)
+    table = torch.from_numpy(t.view(np.uint8).reshape(-1).copy()).cuda()
+    y = torch.zeros(rows, d_out, dtype=torch.bfloat16, device="cuda")
+    seg, ws = lg.Segments(rows, max_segments=1), torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    lg.build_segments(torch.zeros(rows, dtype=torch.int32, device="cuda"), 1, seg, ws)
+    io = lg.GroupedIO(x.cuda(), y)
+    if not is_gated:
+        lg.grouped_layer_q4g({"gate": io}, rows, table, 1, seg, group)
+    elif group:
+        lg.grouped_gated_layer_q4g(io, rows, table, 1, seg, group)
+    else:
+        lg.grouped_gated_layer(io, rows, table, 1, seg)
+    torch.cuda.synchronize()
+    assert int(seg.status.item()) == 0
+    sums = [(q4_sums if group else grouped_bf16)(x, *keep[c][2]) for c in cols]
+    ref, slack = gated("silu", *sums[0], *sums[1]) if is_gated else sums[0]
+    close(y[:, at.cuda()], ref, slack, "sampled outputs")
 
 
 @forms
