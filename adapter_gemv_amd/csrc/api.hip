@@ -741,6 +741,12 @@ int pick_gemm(GemmKind kind, int64_t rows, int64_t groups, int adapters, const G
     }
     const double fill = blocks / (kComputeUnits * t.per_unit);  // rounds; the last of many overlaps the one before
     double us = std::max(longest, sum / blocks * (fill <= 2 ? std::ceil(fill) : fill + 0.4));
+    // Blocks of a longer d_in than the others' go on when those are done, with the
+    // unit to themselves (16 rows on a whole layer, whose down projection is 3.5
+    // times as long as the rest: 150 us with 64 columns, four blocks a unit; 162
+    // with 128, two).
+    const double others = sum / (kComputeUnits * t.per_unit);
+    if (q4 && longest > 1.5 * sum / blocks && longest > others) us = others + (longest - others) / share;
     if (q4) {  // W read again for every row tile, at 5.5 TB/s: what few rows wait for
       double bytes = 0;
       for (int i = 0; i < n; ++i) bytes += rt * m[i].d_out * (double)m[i].kbytes / 4 * (is_gated(kind) ? 2 : 1);

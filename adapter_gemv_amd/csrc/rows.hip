@@ -105,12 +105,17 @@ __global__ __launch_bounds__(256) void few_rows_kernel(RowsDesc r) {
   const int module = (int)blockIdx.x / per, rest = (int)blockIdx.x - module * per;
   const int b = rest / d.max_rank, j = rest - b * d.max_rank;
   const ModuleDesc m = kernel_desc().mod[module];
+  // ids and number of segments; then the entry, the last segment and x; then A: what
+  // can be read at once is asked for at once
   const int a = uniform(r.ids[b]);
-  const int last = uniform(last_slot(d));
+  const int nseg = min(uniform(*d.num_segments), d.max_seg);
+  const bool valid = (unsigned)a < (unsigned)d.num_slots;
+  const lora_adapter_entry_t raw = d.table[(int64_t)(valid ? a : 0) * d.table_cols + m.col];
+  int last = nseg > 0 ? uniform(d.seg_adapter[nseg - 1]) : -1;
+  if (nseg > 0 && uniform(d.seg_offsets[nseg]) > d.num_rows) last = uniform(last_slot(d));  // built for more rows
   const bool on = has_segment(d, a, last);
   lora_adapter_entry_t e{};
   if (on) {
-    const lora_adapter_entry_t raw = d.table[(int64_t)a * d.table_cols + m.col];
     e.A = uniform(raw.A);
     e.B = uniform(raw.B);
     e.rank = uniform(raw.rank);
@@ -118,7 +123,6 @@ __global__ __launch_bounds__(256) void few_rows_kernel(RowsDesc r) {
     e.format = uniform(raw.format);
   }
   if (blockIdx.x == 0 && w == 0) {  // segments that do not fit the batch, once a call
-    const int nseg = min(*d.num_segments, d.max_seg);
     for (int s = lane; s < nseg; s += 64) {
       const int o0 = d.seg_offsets[s], o1 = d.seg_offsets[s + 1];
       if ((unsigned)d.seg_adapter[s] >= (unsigned)d.num_slots || o0 < 0 || o1 <= o0 || o1 > d.num_rows) atomicAdd(d.status, 1);
