@@ -718,9 +718,16 @@ int pick_gemm(GemmKind kind, int64_t rows, int64_t groups, int adapters, const G
   // of x's k (fitted to blocks of 8192 inputs: 256 x 256 391 us, 128 x 128 by
   // two 219, 64 x 256 by two 244, 32 x 128 by two 74, 16 x 64 by four 45)
   const bool q4 = is_q4(kind);
-  auto work = [&](const GemmTile &t, double kbytes) {
-    if (!q4) return (t.rows + t.wcols) * kbytes / kUnitBytesPerUs;
-    return (0.4 * (t.rows + 0.25 * t.wcols) / kUnitBytesPerUs + 0.32e-6 * std::max(t.rows, 16) * t.wcols) * kbytes;
+  // A stage of a block alone on its unit takes a chain of waits (memory, barrier,
+  // LDS, products) whatever it holds: shorter in a deeper ring, which leaves no room
+  // for other blocks (28672 inputs, 8192 outputs, a block or less a unit: one row 46
+  // and 37 us with 2 and 4 stages, 16 rows 89 and 56 with 2 and, on half the
+  // columns, 8).
+  auto work = [&](const GemmTile &t, double share, double kbytes) {
+    if (!q4) return share * (t.rows + t.wcols) * kbytes / kUnitBytesPerUs;
+    return std::max(kbytes / t.stage_bytes * t.stage_us,
+                    share * (0.4 * (t.rows + 0.25 * t.wcols) / kUnitBytesPerUs + 0.32e-6 * std::max(t.rows, 16) * t.wcols) *
+                        kbytes);
   };
   int fit = 0;
   while (fit + 1 < tiles && gemm_tile(kind, fit).rows < per) ++fit;
@@ -735,7 +742,7 @@ int pick_gemm(GemmKind kind, int64_t rows, int64_t groups, int adapters, const G
     const double share = std::min((double)t.per_unit, std::ceil(blocks / kComputeUnits));
     double sum = 0, longest = 0;
     for (int i = 0; i < n; ++i) {
-      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + share * work(t, (double)m[i].kbytes);
+      const double one = t.fixed + t.per_adapter * std::min(adapters, 16) + work(t, share, (double)m[i].kbytes);
       sum += rt * ((m[i].d_out + t.cols - 1) / t.cols) * one;
       longest = std::max(longest, one);
     }

@@ -106,7 +106,7 @@ struct GemmCfg {
 // What the account of the tiles (api.hip) knows of one.
 template <class C>
 constexpr GemmTile tile_of(double fixed) {
-  return {C::RT, C::HC, C::NC, 160 * 1024 / C::LDS, fixed, 0.3 * C::MT * C::NTE / C::DT * (C::GATED ? 2 : 1)};
+  return {C::RT, C::HC, C::NC, 160 * 1024 / C::LDS, fixed, C::KB, C::Q4 ? (C::S > 4 ? 0.5 : C::S > 2 ? 0.65 : 0.78) : 0., 0.3 * C::MT * C::NTE / C::DT * (C::GATED ? 2 : 1)};
 }
 
 __device__ __forceinline__ const GemmDesc &gemm_desc() {

@@ -277,6 +277,8 @@ struct GemmTile {
   int wcols;       // rows of W (gated: of both)
   int per_unit;   // blocks that a compute unit holds (their LDS)
   double fixed;   // us from a block's start to its first product, and of its end
+  int stage_bytes;  // 4-bit: bytes of x's k in a stage,
+  double stage_us;  // and the least time of one
   double per_adapter;  // us of its end for each adapter among 16 rows (its waves' row tiles in turn)
 };
 constexpr int kGemmTiles = 6;
