@@ -719,10 +719,10 @@ int pick_gemm(GemmKind kind, int64_t rows, int64_t groups, int adapters, const G
   // two 219, 64 x 256 by two 244, 32 x 128 by two 74, 16 x 64 by four 45)
   const bool q4 = is_q4(kind);
   // A stage of a block alone on its unit takes a chain of waits (memory, barrier,
-  // LDS, products) whatever it holds: shorter in a deeper ring, which leaves no room
-  // for other blocks (28672 inputs, 8192 outputs, a block or less a unit: one row 46
-  // and 37 us with 2 and 4 stages, 16 rows 89 and 56 with 2 and, on half the
-  // columns, 8).
+  // LDS, products) whatever it holds: where blocks are few, long stages on 8 waves,
+  // which leave little room for other blocks (28672 inputs, 8192 outputs, a block or
+  // less a unit: one row 46 us with 4 waves and 1024 bytes of x a stage, 30 with 8
+  // and 2048; 16 rows 89 with 512 and 64 columns, 42 with 8 waves, 1024 and 32).
   auto work = [&](const GemmTile &t, double share, double kbytes) {
     if (!q4) return share * (t.rows + t.wcols) * kbytes / kUnitBytesPerUs;
     return std::max(kbytes / t.stage_bytes * t.stage_us,

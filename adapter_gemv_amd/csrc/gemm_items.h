@@ -75,8 +75,10 @@ struct GemmCfg {
   static constexpr int WSWZ = WPIECES >= 16 ? 15 : WPIECES - 1;
   static constexpr int XI = RT * KB / 1024;            // load instructions of x per stage; fewer than waves: some twice
   static constexpr int XL = XI < NW ? 1 : XI / NW, WL = NC * WKB / 1024 / NW;  // loads per wave and stage
-  // 4-bit: the scales of 16 groups of each row of W, and the loads of them per wave.
-  static constexpr int SBYTES = Q4_ ? NC * 16 * 4 : 0, SL = SBYTES / 256 / NW;
+  // 4-bit: the scales of SG groups of each row of W (as many as a stage may have, at
+  // least 16), and the loads of them per wave.
+  static constexpr int SG = KB > 1024 ? KB / 64 : 16;
+  static constexpr int SBYTES = Q4_ ? NC * SG * 4 : 0, SL = SBYTES / 256 / NW;
   static constexpr int XBYTES = RT * KB, WBYTES = NC * WKB, STAGE = XBYTES + WBYTES;
   static constexpr int RED = WK > 1 ? NW * MT * NT * 1024 : 0;  // partial sums of the k waves
   // A wave of at least 64 finished columns turns its outputs round in LDS and
@@ -95,7 +97,7 @@ struct GemmCfg {
   // prefill tile share one, which is kept from row tile to row tile instead.
   static constexpr int AHEAD = RT >= 256 ? 1 : Q4_ && RT >= 64 ? 2 : 4;
   static_assert(WL >= 1 && XI * 1024 == RT * KB && (XI < NW ? NW % XI == 0 : XL * NW == XI) && WL * NW * 1024 == WBYTES, "loads per wave");
-  static_assert(!Q4_ || (SL >= 1 && SL * NW * 256 == SBYTES && KB <= 1024 && !I8_ && !PIPE_), "4-bit: scales per wave");
+  static_assert(!Q4_ || (SL >= 1 && SL * NW * 256 == SBYTES && !I8_ && !PIPE_), "4-bit: scales per wave");
   static_assert(RT >= 16 || (Q4_ && WR == 1 && (RT & (RT - 1)) == 0), "fewer rows than a matrix-core tile");
   static_assert(!GATED_ || (NT % 2 == 0 && NW % 2 == 0 && HC % 16 == 0 && !I8_), "gated: the waves split the halves");
   static_assert(KB % (64 * WK) == 0 && KB >= 128, "k steps per wave");
@@ -106,7 +108,7 @@ struct GemmCfg {
 // What the account of the tiles (api.hip) knows of one.
 template <class C>
 constexpr GemmTile tile_of(double fixed) {
-  return {C::RT, C::HC, C::NC, 160 * 1024 / C::LDS, fixed, C::KB, C::Q4 ? (C::S > 4 ? 0.5 : C::S > 2 ? 0.65 : 0.78) : 0., 0.3 * C::MT * C::NTE / C::DT * (C::GATED ? 2 : 1)};
+  return {C::RT, C::HC, C::NC, 160 * 1024 / C::LDS, fixed, C::KB, C::Q4 ? (C::KB > 1024 ? 1.0 : C::S > 2 ? 0.72 : 0.78) : 0., 0.3 * C::MT * C::NTE / C::DT * (C::GATED ? 2 : 1)};
 }
 
 __device__ __forceinline__ const GemmDesc &gemm_desc() {
@@ -514,10 +516,10 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   const uint8_t *W;
   const float *Ws;
   int64_t ldw, lds_ = 0;  // of W, bytes; of 4-bit scales, floats
-  constexpr int RPI = 1024 / C::KB > 0 ? 1024 / C::KB : 1;  // rows per load instruction
-  static_assert(C::KB <= 1024, "a load instruction covers whole rows");
-  const int lrow = lane / C::PIECES, lslot = lane % C::PIECES;
   auto xload = [&](int i) { return C::XI < C::NW ? w % C::XI : i * C::NW + w; };
+  // the row of x, in LDS, of a lane's i-th load, and its 16-byte place in the row
+  auto xrow_of = [&](int i) { return (C::KB > 1024 ? xload(i) * 64 + lane : lane) / C::PIECES + (C::KB > 1024 ? 0 : xload(i) * (1024 / C::KB)); };
+  auto xslot_of = [&](int i) { return (C::KB > 1024 ? xload(i) * 64 + lane : lane) % C::PIECES; };
   int xperm[C::XL];  // grouped: the rows that this lane loads
   (void)xperm;
   if constexpr (GROUPED) {
@@ -546,7 +548,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     slot = tile.slot;
     if constexpr (C::GATED || C::Q4) {
 #pragma unroll
-      for (int i = 0; i < C::XL; ++i) xperm[i] = d.perm[row0 + min(xload(i) * RPI + lrow, rows - 1)];
+      for (int i = 0; i < C::XL; ++i) xperm[i] = d.perm[row0 + min(xrow_of(i), rows - 1)];
       const GemmWeight own = load_weight<C>(d, m, slot, C::GATED ? gemm_desc().mod[half].col : m.col);
       bool there = own.W != nullptr, ok = own.ok;
       if constexpr (C::GATED) {  // gate and up: both or neither
@@ -658,7 +660,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   uint32_t xoff[C::XL], woff[C::WL];
 #pragma unroll
   for (int i = 0; i < C::XL; ++i) {
-    const int r = xload(i) * RPI + lrow;
+    const int r = xrow_of(i);
     const int rr = min(r, rows - 1);  // past the tile: its last row again (never stored)
     int b = row0 + rr;
     if constexpr (GROUPED && (C::Q4 || C::GATED)) {
@@ -666,7 +668,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       if (m.rows_per_x > 1) b /= m.rows_per_x;
     } else if constexpr (GROUPED) b = (int)min((unsigned)d.perm[b], (unsigned)(d.num_rows - 1)) / m.rows_per_x;
     else if (d.order) b = (int)min((unsigned)d.order[b], (unsigned)(d.num_rows - 1));
-    xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((lslot ^ (r & C::SWZ)) * 16);
+    xoff[i] = (uint32_t)((int64_t)b * m.ldx) + (uint32_t)((xslot_of(i) ^ (r & C::SWZ)) * 16);
     if constexpr (C::Q4 || C::GATED) xoff[i] = r < rows ? xoff[i] : kOutOfRange;  // or nothing: zeros, no fetch
   }
 #pragma unroll
@@ -675,8 +677,8 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const int n = min(n0 + r - half * C::HC, m.d_out - 1);
     woff[i] = (uint32_t)((int64_t)n * ldw) + (uint32_t)((wslot ^ (r & C::WSWZ)) * 16);
   }
-  // 4-bit: the scales of 16 groups (a batch), 64 consecutive bytes of each row of
-  // Ws; in LDS [4 rows][group][row], so that a lane reads its four outputs' in one.
+  // 4-bit: the scales of SG groups (a batch), 64 consecutive bytes or more of each
+  // row of Ws; in LDS [4 rows][group][row], so that a lane reads its four outputs' in one.
   // (A stage's own, 4 to 32 bytes of a row each time: every load instruction met
   // 64 lines, 7 to 36 us of the calls below.)
   const int glog = C::Q4 ? m.group_log : 0;
@@ -684,11 +686,12 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   if constexpr (C::Q4) asm volatile("s_nop 4" : : "s"(rsc));
   constexpr int SLN = C::SL > 0 ? C::SL : 1;
   uint32_t soffs[SLN];
-  auto sgroup = [&](int i) { return (lane >> 2) ^ (wload_s(i) & 3); };
+  auto squad = [&](int i) { return (wload_s(i) * 64 + lane) / (4 * C::SG); };  // its 4 rows
+  auto sgroup = [&](int i) { return ((wload_s(i) * 16 + (lane >> 2)) % C::SG) ^ (squad(i) & 3); };
   if constexpr (C::Q4) {
 #pragma unroll
     for (int i = 0; i < C::SL; ++i) {
-      const int n = min(n0 + wload_s(i) * 4 + (lane & 3) - half * C::HC, m.d_out - 1);
+      const int n = min(n0 + squad(i) * 4 + (lane & 3) - half * C::HC, m.d_out - 1);
       soffs[i] = (uint32_t)(((int64_t)n * lds_ + sgroup(i)) * 4);
     }
   }
@@ -708,7 +711,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     } else {
 #pragma unroll
       for (int i = 0; i < C::XL; ++i) {
-        const int piece = lslot ^ ((xload(i) * RPI + lrow) & C::SWZ);
+        const int piece = xslot_of(i) ^ (xrow_of(i) & C::SWZ);
         const bool on = piece * 16 < left && (!(C::Q4 || C::GATED) || xoff[i] != kOutOfRange);
         dma16(rx, on ? xoff[i] + soff : kOutOfRange, 0, at + (uint32_t)xload(i) * 1024);
       }
@@ -732,7 +735,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   // A stage's batch of scales goes with the first stage that needs it, before its
   // operands (loads complete in order).  A place for each of the stages under way:
   // none of them can need the batch whose place is taken.
-  auto batch_of = [&](int r) { return ((r * (C::KB / 2)) >> glog) >> 4; };
+  auto batch_of = [&](int r) { return ((r * (C::KB / 2)) >> glog) / C::SG; };
   int s_batch = -1, s_put = 0;
   auto issue_s = [&](int r) {
     const int batch = batch_of(r);
@@ -740,7 +743,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     s_batch = batch;
 #pragma unroll
     for (int i = 0; i < C::SL; ++i)
-      dma4(rsc, batch * 16 + sgroup(i) < (m.d_in >> glog) ? soffs[i] + (uint32_t)batch * 64 : kOutOfRange, 0,
+      dma4(rsc, batch * C::SG + sgroup(i) < (m.d_in >> glog) ? soffs[i] + (uint32_t)batch * C::SG * 4 : kOutOfRange, 0,
            lds_base + C::S * C::STAGE + s_put + (uint32_t)wload_s(i) * 256);
     s_put = s_put + C::SBYTES == C::S * C::SBYTES ? 0 : s_put + C::SBYTES;
   };
@@ -891,7 +894,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
           if (now >= 0) s_get = s_get + C::SBYTES == C::S * C::SBYTES ? 0 : s_get + C::SBYTES;
           now = batch_of(stage);
         }
-        return lds + C::S * C::STAGE + s_get + g * 256 + wcol * 64;
+        return lds + C::S * C::STAGE + s_get + (g * 4 + wcol) * C::SG * 4;
       };
       auto read_x = [&](const uint8_t *buf, int i, int mt) {
         return *(const u32x4 *)(buf + xrow + mt * 16 * C::KB + ((((wk * KS + i) * 4 + g) ^ (xin & C::SWZ)) * 16));
@@ -902,7 +905,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
       // steps c * CH .. of the stage in buf
       auto multiply = [&](auto chain, int c, int stage, const uint8_t *scales, const uint8_t *buf) {
         constexpr int CH = decltype(chain)::value;
-        const int grp = ((stage * (C::KB / 2) + (wk * KS + c * CH) * 32) >> glog) & 15;
+        const int grp = ((stage * (C::KB / 2) + (wk * KS + c * CH) * 32) >> glog) & (C::SG - 1);
         const uint8_t *sc_at = scales + ((grp ^ g) * 16);
         u32x4 xo[CH][C::MT];
         f32x4_t start[C::MT];
@@ -917,7 +920,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
         }
 #pragma unroll
         for (int nt = 0; nt < C::NT; ++nt) {
-          const f32x4_t sc = *(const f32x4_t *)(sc_at + wtile(nt) / C::WKB * 64);
+          const f32x4_t sc = *(const f32x4_t *)(sc_at + wtile(nt) / C::WKB * C::SG * 4);
           u32x4 wo[CH];
 #pragma unroll
           for (int i = 0; i < CH; ++i) wo[i] = q4x8_shifted(read_w(buf, c * CH + i, nt));

@@ -15,7 +15,7 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::E
 int q4_tiles() { return kQ4Tiles; }
 
 GemmTile q4_tile(bool gated, int cfg) {
-  auto of = [](auto c) { return tile_of<decltype(c)>(c.RT <= 64 ? 6 : c.RT <= 128 ? 8 : 16); };
+  auto of = [](auto c) { return tile_of<decltype(c)>(c.WK == 8 ? 9 : c.RT <= 64 ? 6 : 16); };
   return gated ? with_q4_tile<true>(cfg, of) : with_q4_tile<false>(cfg, of);
 }
 

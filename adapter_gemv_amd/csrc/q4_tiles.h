@@ -7,9 +7,9 @@ namespace lora {
 
 //                                                    I8     RT   NC  WR WC WK  KB  S EU  PIPE   Q4
 template <bool GATED> using Q4Cfg4n = GemmCfg<false, 4, 32, 1, 1, 4, 1024, 2, 2, false, true, GATED>;
-template <bool GATED> using Q4Cfg4d = GemmCfg<false, 4, 32, 1, 1, 4, 1024, 4, 2, false, true, GATED>;
+template <bool GATED> using Q4Cfg4d = GemmCfg<false, 4, 32, 1, 1, 8, 2048, 3, 2, false, true, GATED>;
 template <bool GATED> using Q4Cfg4 = GemmCfg<false, 4, 64, 1, 1, 4, 512, 2, 2, false, true, GATED>;
-template <bool GATED> using Q4Cfg16d = GemmCfg<false, 16, 32, 1, 1, 4, 512, 8, 2, false, true, GATED>;
+template <bool GATED> using Q4Cfg16d = GemmCfg<false, 16, 32, 1, 1, 8, 1024, 3, 2, false, true, GATED>;
 template <bool GATED> using Q4Cfg16 = GemmCfg<false, 16, 64, 1, 1, 4, 512, 2, 2, false, true, GATED>;
 template <bool GATED> using Q4Cfg16w = GemmCfg<false, 16, 128, 1, 1, 4, 512, 2, 2, false, true, GATED>;
 template <bool GATED> using Q4Cfg32 = GemmCfg<false, 32, 128, 1, 1, 4, 512, 2, 2, false, true, GATED>;

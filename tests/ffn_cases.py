@@ -71,56 +71,64 @@ def gated(kind, z, dz, u, du):
     return h, slack
 
 
-# The tiles (rows, columns of the output) and a batch that takes each: (kind, tile, lengths of the segments, or rows of a
-# batch over TILE_SLOTS adapters, d_in, d_out).  More than one row tile and column tile, the last of each partial, and
-# enough of k that the tile's ring is filled again.
+# A batch that takes each tile: (kind, the tile's number, its rows and columns of the output, lengths of the segments, or
+# rows of a batch over TILE_SLOTS adapters, d_in, d_out).  More than one row tile and column tile, the last of each
+# partial, and enough of k that the tile's ring is filled again.
 TILE_SLOTS = 5
 TILES = [
-    ("gated", (16, 32), 21, 1032, 40),
-    ("gated", (32, 32), 1030, 1032, 104),
-    ("gated", (64, 32), 1030, 1032, 232),
-    ("gated", (128, 64), 130, 1032, 5464),
-    ("gated", (256, 128), 260, 1032, 11048),
-    ("gated_q4g", (4, 16), 5, 1152, 24),
-    ("gated_q4g", (4, 32), 130, 1152, 120),
-    ("gated_q4g", (16, 32), 700, 1152, 40),
-    ("gated_q4g", (16, 64), 1030, 1152, 104),
-    ("gated_q4g", (32, 64), 1030, 1152, 360),
-    ("gated_q4g", (64, 128), 100, 1152, 8288),
-    ("gated_q4g", (256, 128), 1030, 2176, 4848),
-    ("grouped_gated", (16, 32), (0, 7, 33), 1032, 40),
-    ("grouped_gated", (32, 32), (520, 700, 257), 1032, 72),
-    ("grouped_gated", (64, 32), (70, 5, 3), 1032, 2088),
-    ("grouped_gated", (128, 64), (200, 15, 5), 1032, 3360),
-    ("grouped_gated", (256, 128), (0, 520, 15), 1032, 5040),
-    ("grouped_gated_q4g", (4, 16), (3, 7, 5), 1152, 24),
-    ("grouped_gated_q4g", (4, 32), (33, 257, 100), 1152, 40),
-    ("grouped_gated_q4g", (16, 32), (700, 0, 3), 1152, 40),
-    ("grouped_gated_q4g", (16, 64), (63, 700, 257), 1152, 104),
-    ("grouped_gated_q4g", (32, 64), (3, 37, 15), 1152, 4976),
-    ("grouped_gated_q4g", (64, 128), (70, 3, 0), 1152, 8952),
-    ("grouped_gated_q4g", (256, 128), (300, 127, 15), 2176, 10720),
-    ("grouped_q4g", (4, 32), (0, 1, 5), 1152, 48),
-    ("grouped_q4g", (4, 64), (37, 100, 127), 1152, 104),
-    ("grouped_q4g", (16, 64), (520, 63, 100), 1152, 72),
-    ("grouped_q4g", (16, 128), (520, 520, 0), 1152, 200),
-    ("grouped_q4g", (32, 128), (700, 520, 15), 1152, 584),
-    ("grouped_q4g", (64, 256), (1, 33, 70), 1152, 13752),
-    ("grouped_q4g", (256, 256), (129, 21, 300), 2176, 20928),
-    ("linear_q4g", (4, 32), 5, 1152, 40),
-    ("linear_q4g", (4, 64), 130, 1152, 232),
-    ("linear_q4g", (16, 64), 700, 1152, 72),
-    ("linear_q4g", (16, 128), 1030, 1152, 200),
-    ("linear_q4g", (32, 128), 1030, 1152, 712),
-    ("linear_q4g", (64, 256), 1030, 1152, 1936),
-    ("linear_q4g", (256, 256), 1030, 2176, 9880),
+    ("gated", 0, (16, 32), 21, 1032, 40),
+    ("gated", 1, (32, 32), 1030, 1032, 104),
+    ("gated", 2, (64, 32), 1030, 1032, 232),
+    ("gated", 3, (128, 64), 130, 1032, 5464),
+    ("gated", 4, (256, 128), 260, 1032, 11048),
+    ("gated_q4g", 0, (4, 16), 5, 1152, 24),
+    ("gated_q4g", 1, (4, 16), 6, 8320, 24),
+    ("gated_q4g", 2, (4, 32), 130, 1152, 616),
+    ("gated_q4g", 3, (16, 16), 700, 2176, 120),
+    ("gated_q4g", 4, (16, 32), 1030, 1152, 72),
+    ("gated_q4g", 5, (16, 64), 90, 1152, 1176),
+    ("gated_q4g", 6, (32, 64), 1030, 1152, 360),
+    ("gated_q4g", 7, (64, 128), 100, 1152, 8288),
+    ("gated_q4g", 8, (256, 128), 520, 2176, 9496),
+    ("grouped_gated", 0, (16, 32), (0, 7, 33), 1032, 40),
+    ("grouped_gated", 1, (32, 32), (520, 700, 257), 1032, 72),
+    ("grouped_gated", 2, (64, 32), (70, 5, 3), 1032, 2088),
+    ("grouped_gated", 3, (128, 64), (200, 15, 5), 1032, 3360),
+    ("grouped_gated", 4, (256, 128), (0, 520, 15), 1032, 5040),
+    ("grouped_gated_q4g", 0, (4, 16), (3, 7, 5), 1152, 24),
+    ("grouped_gated_q4g", 1, (4, 16), (15, 7, 0), 8320, 24),
+    ("grouped_gated_q4g", 2, (4, 32), (200, 21, 257), 1152, 168),
+    ("grouped_gated_q4g", 3, (16, 16), (300, 21, 70), 2176, 200),
+    ("grouped_gated_q4g", 4, (16, 32), (520, 700, 5), 1152, 72),
+    ("grouped_gated_q4g", 5, (16, 64), (100, 37, 257), 1152, 280),
+    ("grouped_gated_q4g", 6, (32, 64), (3, 37, 15), 1152, 4976),
+    ("grouped_gated_q4g", 7, (64, 128), (70, 3, 0), 1152, 8952),
+    ("grouped_gated_q4g", 8, (256, 128), (300, 129, 100), 2176, 9032),
+    ("grouped_q4g", 0, (4, 32), (5, 3, 7), 1152, 40),
+    ("grouped_q4g", 1, (4, 32), (33, 1, 15), 8320, 48),
+    ("grouped_q4g", 2, (4, 64), (129, 129, 257), 1152, 296),
+    ("grouped_q4g", 3, (16, 32), (700, 520, 127), 2176, 104),
+    ("grouped_q4g", 4, (16, 64), (300, 5, 520), 1152, 200),
+    ("grouped_q4g", 5, (16, 128), (37, 7, 129), 1152, 2224),
+    ("grouped_q4g", 6, (32, 128), (63, 33, 700), 1152, 912),
+    ("grouped_q4g", 7, (64, 256), (1, 33, 70), 1152, 13752),
+    ("grouped_q4g", 8, (256, 256), (300, 63, 70), 2176, 21648),
+    ("linear_q4g", 0, (4, 32), 5, 1152, 40),
+    ("linear_q4g", 1, (4, 32), 9, 8320, 40),
+    ("linear_q4g", 2, (4, 64), 130, 1152, 1224),
+    ("linear_q4g", 3, (16, 32), 1030, 2176, 136),
+    ("linear_q4g", 4, (16, 64), 1030, 1152, 136),
+    ("linear_q4g", 5, (16, 128), 70, 1152, 5776),
+    ("linear_q4g", 6, (32, 128), 1030, 1152, 712),
+    ("linear_q4g", 7, (64, 256), 1030, 1152, 1936),
+    ("linear_q4g", 8, (256, 256), 520, 2176, 19360),
 ]
 KINDS = ("linear_i8", "grouped", "grouped_i8", "gated", "grouped_gated", "linear_q4g", "grouped_q4g", "gated_q4g",
          "grouped_gated_q4g")
 
 
 def tile_of(kind, rows, slots, shapes, max_segments=0):
-    """(rows, columns) of the tile that the library takes for a call of `kind` with these (d_in, d_out)."""
+    """(number, rows, columns) of the tile that the library takes for a call of `kind` with these (d_in, d_out)."""
     import ctypes
 
     import adapter_gemv_amd as lg
@@ -135,4 +143,4 @@ def tile_of(kind, rows, slots, shapes, max_segments=0):
             ints(*[s[0] for s in shapes]), ints(*[s[1] for s in shapes]), ctypes.c_int32(n), ctypes.byref(rt),
             ctypes.byref(ct), ctypes.byref(us))
     assert got >= 0
-    return rt.value, ct.value
+    return got, rt.value, ct.value

@@ -241,20 +241,15 @@ def test_grouped_calls_refuse_short_tables_and_matrices(x, y, table, fan, what):
             call()
 
 
-@pytest.mark.parametrize("kind,tile,rows,d_in,d_out", TILES)
-def test_batches_take_their_tile(kind, tile, rows, d_in, d_out):
-    most = rows if isinstance(rows, int) else max(rows)
-    if isinstance(rows, int):
-        assert tile_of(kind, rows, TILE_SLOTS, [(d_in, d_out)]) == tile
-    else:
-        assert tile_of(kind, sum(rows), len(rows), [(d_in, d_out)]) == tile
-    assert most > tile[0] and most % tile[0] and d_out > tile[1] and d_out % tile[1]
+@pytest.mark.parametrize("kind,number,tile,rows,d_in,d_out", TILES)
+def test_batches_take_their_tile(kind, number, tile, rows, d_in, d_out):
+    lengths = (rows,) if isinstance(rows, int) else rows
+    slots = TILE_SLOTS if isinstance(rows, int) else len(rows)
+    assert tile_of(kind, sum(lengths), slots, [(d_in, d_out)]) == (number,) + tile
+    assert max(lengths) > tile[0] and max(lengths) % tile[0] and d_out > tile[1] and d_out % tile[1]
 
 
 def test_every_tile_has_a_batch():
-    bf16 = [(16, 32), (32, 32), (64, 32), (128, 64), (256, 128)]
-    q4 = [(4, 32), (4, 64), (16, 64), (16, 128), (32, 128), (64, 256), (256, 256)]
-    want = {"gated": bf16, "grouped_gated": bf16, "linear_q4g": q4, "grouped_q4g": q4}
-    want["gated_q4g"] = want["grouped_gated_q4g"] = [(r, c // 2) for r, c in q4]
-    for kind, tiles in want.items():
-        assert sorted(c[1] for c in TILES if c[0] == kind) == tiles, kind
+    tiles = {"gated": 5, "grouped_gated": 5, "linear_q4g": 9, "grouped_q4g": 9, "gated_q4g": 9, "grouped_gated_q4g": 9}
+    for kind, n in tiles.items():
+        assert sorted(c[1] for c in TILES if c[0] == kind) == list(range(n)), kind

@@ -185,8 +185,8 @@ def test_rows(form, rows, slots):
 
 
 @pytest.mark.parametrize("group,rank", [(32, 48), (128, 16)])
-@pytest.mark.parametrize("kind,tile,rows,d_in,d_out", [c for c in TILES if not c[0].startswith("grouped")])
-def test_every_tile(kind, tile, rows, d_in, d_out, group, rank):
+@pytest.mark.parametrize("kind,number,tile,rows,d_in,d_out", [c for c in TILES if not c[0].startswith("grouped")])
+def test_every_tile(kind, number, tile, rows, d_in, d_out, group, rank):
     if not kind.endswith("q4g"):
         group = 0
     Run(("gated" in kind, group), rows, TILE_SLOTS, one(d_in, d_out), rank, seed=tile[0], fmt="both").check()

@@ -162,8 +162,8 @@ def test_groups(is_gated, group, groups, rows):
 
 
 @pytest.mark.parametrize("group", [32, 128])
-@pytest.mark.parametrize("kind,tile,lengths,d_in,d_out", [c for c in TILES if c[0].startswith("grouped")])
-def test_every_tile(kind, tile, lengths, d_in, d_out, group):
+@pytest.mark.parametrize("kind,number,tile,lengths,d_in,d_out", [c for c in TILES if c[0].startswith("grouped")])
+def test_every_tile(kind, number, tile, lengths, d_in, d_out, group):
     if not kind.endswith("q4g"):
         group = 0
     Run(("gated" in kind, group), ragged(lengths, 2), len(lengths), one(d_in, d_out), seed=tile[0], act="gelu_tanh").check()
