@@ -11,6 +11,13 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::E
   gemm_block<C, GROUPED, KT>(d, lds);
 }
 
+// The tiles; NC counts gate's and up's columns.  One MI355X, us of a pass with the
+// adapters, gate and up of 8192 x 28672, by tile: 1 row [163], 173, 168, 177; 16
+// rows [177], 187, 185, 196; 48 rows 494, 366, [220], 222; 128 rows over 128
+// adapters of rank 16 1293, 732, 468, [262], 414 (1.18 GB with their B, 4.7 TB/s of
+// the whole call); 7637 rows 256 x 256 [5826], 128 x 128 8596 (1.22 PFLOP/s with
+// the epilogue; the matrix cores busy for 60% of the cycles).  128 rows x 96
+// columns, two blocks a unit, 343 where 128 x 128 takes 262: not kept.
 //                   I8     RT   NC  WR WC WK  KB  S EU  PIPE   Q4    GATED
 using Gated16 = GemmCfg<false, 16, 64, 1, 1, 4, 512, 2, 2, false, false, true>;
 using Gated32 = GemmCfg<false, 32, 64, 1, 1, 4, 256, 3, 2, false, false, true>;

@@ -36,10 +36,16 @@
 //     stage; with WK > 1 (few rows and columns per block, so that short
 //     batches still fill the device) the partial sums meet in LDS, added in
 //     wave order.
+//   * 4-bit W goes to LDS as it is, a quarter of the bytes, and is unpacked for the
+//     matrix cores by the wave that multiplies it: two values an operation
+//     (q4x8_shifted), 8 operations a register of 8 weights; converting them took 15
+//     and one token's q/k/v/o 46 us instead of 43.  Scales come in batches of 16
+//     groups of a row (172 -> 150 us of 16 rows on a layer).
 // int8 sums are exact in int32, bf16 sums are fp32; the order of the additions
 // is fixed, so results are bit-reproducible.
 // Bound: few rows, HBM by the weights (W once per row tile; 4.3 GB of bf16 at 16
-// rows a slot 690 us, 6.2 TB/s); many rows, the matrix cores (gemm.hip).
+// rows a slot 690 us, 6.2 TB/s; 1.1 GB of 4-bit at 4 rows a slot 207 us, 5.5 TB/s);
+// many rows, the matrix cores (gemm.hip; 4-bit: with the unpacking beside them).
 #pragma once
 
 #include <type_traits>

@@ -81,7 +81,7 @@ extern "C" {
 
 /* A flag the layer calls (lora_apply_layer and its parts, lora_decode_layer,
  * lora_apply_layer_noalloc, lora_apply_layer_stacked, lora_linear_layer and
- * its parts and their _q4 and _i8 forms) accept in module_mask beside the module
+ * its parts and their _q4, _q4g and _i8 forms) accept in module_mask beside the module
  * bits: the caller's table entries are int8 (LORA_FORMAT_INT8_ROWS), so the
  * shrink's work items take more k than a bf16 item (four times, up to 4096
  * inputs: at least as many bytes per item).  Results are the same within the tolerance with or without it and
@@ -631,10 +631,13 @@ size_t lora_linear_q4g_workspace_bytes(int32_t num_rows, int32_t num_slots,
  *     y[b] = bf16_rne( W . x[b] + scale_a * B_a . (A_a . x[b]) ).
  * Each 4-bit value is exact on the matrix cores, each group's sum meets its
  * scale once, in fp32.  Source: as lora_linear_layer_q4.  Every projection of a
- * call has the same group.  A row of x that holds an infinity or a NaN reaches
- * no other row.  Three launches on `stream`: the grouped shrink, the sum of its
- * partials, one product.  Results are bit-reproducible; the order of a sum
- * depends on the tile, so a row's bits may differ between batches.
+ * call has the same group.  A group's sum is formed from (24 + q) / 16 x less 24 /
+ * 16 of the sum of x: a row of x with magnitudes above 2^119 may give infinities
+ * or NaN before it must, and one that holds an infinity or a NaN gives NaN in all
+ * its outputs, and only there.  Two launches on `stream` for a few rows (v straight
+ * from x and the factors, then one product), else three (the grouped shrink, the
+ * sum of its partials, the product).  Results are bit-reproducible; the order of a
+ * sum depends on the tile, so a row's bits may differ between batches.
  * row_adapter and seg belong together, as for lora_linear_layer_i8.  y overlaps
  * no input.
  *
@@ -721,10 +724,10 @@ size_t lora_gated_workspace_bytes(int32_t num_rows, int32_t num_slots, int32_t m
  * Numbers" (gate, up 8192->28672 and down as three of a layer's seven
  * projections) and "6. Deep Dive A" (the base term shared by the batch, the
  * adapter term per row); the activation between them is not on the pages.
- * z = -infinity gives NaN (as -infinity times 0 does).  Three launches on
- * `stream`: the grouped shrink of both projections, the sum of its partials,
- * one product that reads each weight and x once and writes h alone.  Any batch,
- * from one decode row to a prefill: the tile follows the number of rows.
+ * z = -infinity gives NaN (as -infinity times 0 does).  Launches as for
+ * lora_linear_layer_q4g; the product reads each weight and x once (a row tile) and
+ * writes h alone.  Any batch, from one decode row to a prefill: the tile follows
+ * the number of rows.
  * Results are bit-reproducible.  row_adapter and seg belong together, as for
  * lora_linear_layer_i8.  h overlaps no input.
  *
@@ -745,7 +748,7 @@ lora_status_t lora_gated_layer(const lora_gated_io_t *io, int32_t activation, in
 
 /*
  * lora_gated_layer_q4g -- lora_gated_layer with 4-bit base weights, as in
- * lora_linear_layer_q4g.  Wgs and Wus 4-byte aligned.
+ * lora_linear_layer_q4g (the range of x too).  Wgs and Wus 4-byte aligned.
  * Errors: those of lora_gated_layer; LORA_ERR_ALIGN for a d_in that is not a
  * multiple of group or a weight's leading dimension that is not a multiple of 16
  * bytes, LORA_ERR_SHAPE for a group that is none of the three.
@@ -871,7 +874,8 @@ lora_status_t lora_grouped_layer_i8(const lora_grouped_io_t *io, uint32_t module
  * lora_grouped_layer_q4g -- lora_grouped_layer with 4-bit weights, one fp32 scale
  * per output and group of 32, 64 or 128 inputs, and bf16 rows:
  *     y[b][n] = bf16_rne( sum_k Ws_a[n][k / group] q_a[n][k] x[b / rows_per_x][k] ).
- * No workspace; one launch; Speed as for lora_grouped_layer.
+ * Arithmetic and the range of x as for lora_linear_layer_q4g.  No workspace; one
+ * launch; Speed as for lora_grouped_layer.
  *   weights  device lora_weight_q4g_entry_t [num_slots * 7]
  * Errors: those of lora_grouped_layer, LORA_ERR_SHAPE for a group that is none of
  * the three, LORA_ERR_ALIGN for a d_in that is not a multiple of group.
