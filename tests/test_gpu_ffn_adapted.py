@@ -264,8 +264,9 @@ def test_a_bound_on_the_segments(form, rows, bound):
 
 
 @forms
-def test_bad_entries_are_counted_and_get_no_delta(form):
-    r = Run(form, 60, 5, one(264, 136), 16, kind="runs", seed=4)
+@pytest.mark.parametrize("rows", [60, 90])
+def test_bad_entries_are_counted_and_get_no_delta(form, rows):
+    r = Run(form, rows, 5, one(264, 136), 16, kind="runs", seed=4)
     cols = [MODS.index(c) for c in (("gate", "up") if r.is_gated else ("gate",))]
     present = [s for s in range(5) if (r.ids == s).any()]
     for k in cols:
@@ -365,14 +366,26 @@ def test_no_rows(form):
 
 
 @forms
-def test_segments_of_a_longer_batch(form):
-    # a call for fewer rows than the segments hold: no delta for a segment that does not fit, nothing past the rows
-    r = Run(form, 100, 3, one(264, 136), 16, kind="runs", seed=5)
+@pytest.mark.parametrize("rows,fewer", [(100, 70), (100, 40)])
+def test_segments_of_a_longer_batch(form, rows, fewer):
+    # a call for fewer rows than the segments hold: no delta for a segment that does not fit, which is counted, and
+    # nothing past the rows
+    r = Run(form, rows, 3, one(264, 136), 16, kind="one", seed=5)
+    r.ids = np.sort(np.random.RandomState(3).randint(0, 3, rows)).astype(np.int32)
+    r.dids.copy_(torch.from_numpy(r.ids))
     lg.build_segments(r.dids, 3, r.seg, r.ws)
     r.out("gate").fill_(float("nan"))
-    r.call(rows=70)
+    r.call(rows=fewer)
     torch.cuda.synchronize()
-    assert bool(torch.isnan(r.out("gate")[70:]).all())
+    assert bool(torch.isnan(r.out("gate")[fewer:]).all())
+    ends = np.cumsum(np.bincount(r.ids, minlength=3))
+    out = [s for s in range(3) if ends[s] > fewer]
+    assert 0 < len(out) < 3
+    # 64 rows and more: counted by the grouped shrink, a segment of 8 rows and more by both of its parts
+    assert r.status() == len(out) if fewer < 64 else len(out) <= r.status() <= 2 * len(out)
+    r.rows, full = fewer, r.ids
+    r.ids = full[:fewer]
+    r.check({"gate": r.out("gate")}, skip=out)
 
 
 @pytest.mark.parametrize("group", [0, 64])

@@ -413,6 +413,19 @@ def test_activation_at_infinity():
         assert bool((h[3] == 0).all())
 
 
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("rows", [2, 20, 300])
+def test_large_rows_of_4_bit_products(group, rows):
+    # magnitudes up to 2^119: no sum of a group passes the end of fp32 on its way to a finite result
+    r = Run((False, group), np.zeros(rows, np.int32), 1, one(640, 72), seed=group)
+    x = r.cpu["gate"]["x"]
+    x.copy_((x.float().clamp(-4, 4) / 4 * 2.0 ** 119).to(torch.bfloat16))
+    r.dev["gate"].x.copy_(x)
+    got = r.run()
+    assert bool(torch.isfinite(got["gate"][:, :72]).all())
+    r.check(got)
+
+
 def test_experts_gate_up_and_down_together():
     """A token's two experts: gated half and way back, 4-bit and bf16, in one captured step."""
     tokens, slots, d, f, group = 24, 5, 264, 520, 64
