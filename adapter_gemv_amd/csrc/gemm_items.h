@@ -515,7 +515,7 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   const int local = (int)blockIdx.x - m.block_base;
 
   // a few rows: v and B are requested before and right behind the main loop
-  constexpr bool EARLY = DELTA && (C::Q4 || C::GATED) && C::MT == 1 && C::NTE == C::DT;
+  constexpr bool EARLY = DELTA && (C::Q4 || C::GATED) && C::MT == 1 && C::NTE == C::DT && C::WK > 1;
 
   // the block's rows and columns
   int row0, rows, ct, slot = 0;
@@ -524,7 +524,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   int64_t ldw, lds_ = 0;  // of W, bytes; of 4-bit scales, floats
   auto xload = [&](int i) { return C::XI < C::NW ? w % C::XI : i * C::NW + w; };
   // the row of x, in LDS, of a lane's i-th load, and its 16-byte place in the row
-  auto xrow_of = [&](int i) { return (C::KB > 1024 ? xload(i) * 64 + lane : lane) / C::PIECES + (C::KB > 1024 ? 0 : xload(i) * (1024 / C::KB)); };
+  auto xrow_of = [&](int i) {
+    return C::KB > 1024 ? (xload(i) * 64 + lane) / C::PIECES : lane / C::PIECES + xload(i) * (1024 / C::KB);
+  };
   auto xslot_of = [&](int i) { return (C::KB > 1024 ? xload(i) * 64 + lane : lane) % C::PIECES; };
   int xperm[C::XL];  // grouped: the rows that this lane loads
   (void)xperm;
@@ -1153,45 +1155,45 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     }
   } else {
 #pragma unroll
-  for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
-    const int nw0 = n0 + (wc * C::NT + et0 + e0) * 16;  // first column
-    f32x4_t sw[C::DT];
-    if constexpr (C::I8) {
+    for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
+      const int nw0 = n0 + (wc * C::NT + et0 + e0) * 16;  // first column
+      f32x4_t sw[C::DT];
+      if constexpr (C::I8) {
 #pragma unroll
-      for (int e = 0; e < C::DT; ++e) {
-        const int n = nw0 + e * 16 + g * 4;
-        sw[e] = n < m.d_out ? *(const f32x4_t *)(Ws + n) : f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
-    }
-    BFrag<C::DT, DELTA ? KT : 1> bf[C::AHEAD];
-    (void)bf;
-#pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt) {
-      const int r = (wr * C::MT + mt) * 16 + r_in;
-      const RowInfo ri = info[r];
-      f32x4_t out[C::DT];
-#pragma unroll
-      for (int e = 0; e < C::DT; ++e) {
-        if constexpr (C::I8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[e][i] = ldexpf((float)fin[e0 + e][mt][i] * ri.xs * sw[e][i], ri.xe);
-        } else {
-          out[e] = fin[e0 + e][mt];
+        for (int e = 0; e < C::DT; ++e) {
+          const int n = nw0 + e * 16 + g * 4;
+          sw[e] = n < m.d_out ? *(const f32x4_t *)(Ws + n) : f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
       }
-      if constexpr (DELTA) {
-        V8Split v[KT];
-        if constexpr (EARLY) {
-          scale_v(vraw[0], ri, v);
-          finish_delta<C::DT, KT, EA>(m, ri, v, nw0, erows[0], ebf[0], out);
-        } else {
-          load_v(m.v + (int64_t)(C::Q4 ? row0 + r : ri.b) * d.rs, ri, v);
-          add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
+      BFrag<C::DT, DELTA ? KT : 1> bf[C::AHEAD];
+      (void)bf;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
+        const int r = (wr * C::MT + mt) * 16 + r_in;
+        const RowInfo ri = info[r];
+        f32x4_t out[C::DT];
+#pragma unroll
+        for (int e = 0; e < C::DT; ++e) {
+          if constexpr (C::I8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[e][i] = ldexpf((float)fin[e0 + e][mt][i] * ri.xs * sw[e][i], ri.xe);
+          } else {
+            out[e] = fin[e0 + e][mt];
+          }
         }
+        if constexpr (DELTA) {
+          V8Split v[KT];
+          if constexpr (EARLY) {
+            scale_v(vraw[0], ri, v);
+            finish_delta<C::DT, KT, EA>(m, ri, v, nw0, erows[0], ebf[0], out);
+          } else {
+            load_v(m.v + (int64_t)(C::Q4 ? row0 + r : ri.b) * d.rs, ri, v);
+            add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
+          }
+        }
+        put_out(mt, e0, nw0, ri.b, out);
       }
-      put_out(mt, e0, nw0, ri.b, out);
     }
-  }
   }
   if constexpr (C::TURN) {  // the wave's own rows of LDS: no barrier
     constexpr int PPR = C::NTE * 2, STEPS = C::MT * 16 * PPR / 64;  // 16-byte pieces of a row; stores
