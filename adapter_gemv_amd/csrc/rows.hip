@@ -77,9 +77,13 @@ __device__ __forceinline__ void rows_block(const RowsDesc &r, int block) {
   __syncthreads();
   if (lane == 0) wsum[w] = __popcll(mine);
   __syncthreads();
+  const int end = nvalid + base + wsum[0] + wsum[1] + wsum[2] + wsum[3];
   for (int k = 0; k < w; ++k) base += wsum[k];
   const int at = nvalid + base + __popcll(mine & ((1ull << lane) - 1));
   if ((mine >> lane & 1) && at < d.num_rows) place_row(r, at, b, last);
+  // ids other than those that the segments were built from: places left over hold no row
+  if (block == r.rows_blocks - 1)
+    for (int p = end + t; p < d.num_rows; p += 256) place_row(r, p, -1, last);
 }
 
 __global__ __launch_bounds__(256) void rows_kernel(RowsDesc r) {

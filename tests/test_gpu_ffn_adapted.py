@@ -388,6 +388,27 @@ def test_segments_of_a_longer_batch(form, rows, fewer):
     r.check({"gate": r.out("gate")}, skip=out)
 
 
+@forms
+@pytest.mark.parametrize("rows,kept", [(90, 37), (600, 300)])
+def test_ids_other_than_the_segments(form, rows, kept):
+    # rows that get a slot after the segments were built are in no segment and not among the rows without one: they
+    # may be left unwritten, and the others keep their results
+    r = Run(form, rows, 3, one(264, 136), 16, seed=5)
+    r.ids = np.sort(np.random.RandomState(3).randint(0, 3, rows)).astype(np.int32)
+    r.ids[kept:] = -1
+    r.dids.copy_(torch.from_numpy(r.ids))
+    lg.build_segments(r.dids, 3, r.seg, r.ws)
+    r.dids[kept:] = 0
+    r.ws.fill_(0x7f)
+    r.out("gate").fill_(float("nan"))
+    r.call()
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(r.out("gate")[kept:]).all())
+    assert r.status() == 0
+    r.rows, r.ids = kept, r.ids[:kept]
+    r.check({"gate": r.out("gate")})
+
+
 @pytest.mark.parametrize("group", [0, 64])
 @pytest.mark.parametrize("act", ACTS)
 def test_activation_over_its_range(group, act):
