@@ -311,6 +311,39 @@ __device__ __forceinline__ void mma_settle(f32x4_t (&t)[N]) {
   else asm volatile("s_nop 10" : "+v"(t[0]), "+v"(t[1]), "+v"(t[2]), "+v"(t[3]));
 }
 
+// Eight fp32 values of v as bf16 vectors, the largest piece first.  Two rounded
+// pieces hold 2^-16 of a value (split_v8: the int8 base); three cut ones hold all
+// of its 24 bits: 8 a piece, each remainder exact (a value that is infinite or no
+// number is its first piece), so that a delta that cancels the base leaves what the
+// formula leaves.  It is one matrix-core step more for an adapter and 16 rows: 16
+// rows on a layer, rank 32, 149 us either way; 7637 rows of rank 64, gated 6260
+// either way, 4-bit 8460 -> 8535.
+template <int P>
+struct VPieces {
+  u32x4 p[P];
+};
+template <int P>
+__device__ __forceinline__ VPieces<P> split_v(const float *v) {
+  static_assert(P == 2 || P == 3, "pieces");
+  if constexpr (P == 2) {
+    const V8Split s = split_v8(v);
+    return VPieces<2>{{s.hi, s.lo}};
+  } else {
+    VPieces<3> r;
+    auto cut = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
+    auto both = [](float a, float b) { return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u); };
+    auto rest = [&](float f) { return fabsf(f) < INFINITY ? f - cut(f) : 0.f; };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = v[2 * i], b = v[2 * i + 1], ar = rest(a), br = rest(b);
+      r.p[0][i] = both(a, b);
+      r.p[1][i] = both(ar, br);
+      r.p[2][i] = both(ar - cut(ar), br - cut(br));
+    }
+    return r;
+  }
+}
+
 // The B of one adapter for DT column tiles: values and output scales.
 template <int DT, int KT>
 struct BFrag {
@@ -347,8 +380,8 @@ __device__ __forceinline__ void load_b(const GemmModule &m, const RowInfo &ri, i
   }
 }
 
-template <int DT, int KT>
-__device__ __forceinline__ void use_b(const RowInfo &ri, const V8Split (&v)[KT], const BFrag<DT, KT> &f,
+template <int P, int DT, int KT>
+__device__ __forceinline__ void use_b(const RowInfo &ri, const VPieces<P> (&v)[KT], const BFrag<DT, KT> &f,
                                       f32x4_t (&acc)[DT]) {
   const int g = (threadIdx.x & 63) >> 4;
   u32x4 b[DT][KT];
@@ -375,10 +408,9 @@ __device__ __forceinline__ void use_b(const RowInfo &ri, const V8Split (&v)[KT],
   for (int nt = 0; nt < DT; ++nt) {
     t[nt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < KT; ++ks) {
-      t[nt] = mma(b[nt][ks], v[ks].lo, t[nt]);
-      t[nt] = mma(b[nt][ks], v[ks].hi, t[nt]);
-    }
+    for (int ks = 0; ks < KT; ++ks)
+#pragma unroll
+      for (int k = P - 1; k >= 0; --k) t[nt] = mma(b[nt][ks], v[ks].p[k], t[nt]);
   }
   mma_settle(t);
 #pragma unroll
@@ -393,7 +425,7 @@ __device__ __forceinline__ void use_b(const RowInfo &ri, const V8Split (&v)[KT],
 // operand and all 16 rows' v the B operand; the columns of that adapter's rows
 // are then added and the others dropped (selected, not multiplied by zero: a
 // non-finite factor of one row's adapter must not reach the others).  v, fp32,
-// enters as bf16 hi + lo (2^-16 relative).  The B of the next adapters is
+// enters in bf16 pieces (VPieces).  The B of the next adapters is
 // requested before the current one's products (AHEAD).
 // An int8 B (values exact in bf16) comes in the same 16-byte loads: the piece
 // that holds a lane's 8 values, of which it keeps its half; the output scales
@@ -423,8 +455,8 @@ __device__ __forceinline__ void begin_delta(const GemmModule &m, const RowInfo &
     load_b(m, ri, l, on, n0, f[k]);
   }
 }
-template <int DT, int KT, int AHEAD>
-__device__ __forceinline__ void finish_delta(const GemmModule &m, const RowInfo &ri, const V8Split (&v)[KT], int n0,
+template <int P, int DT, int KT, int AHEAD>
+__device__ __forceinline__ void finish_delta(const GemmModule &m, const RowInfo &ri, const VPieces<P> (&v)[KT], int n0,
                                              DeltaRows &rows, BFrag<DT, KT> (&f)[AHEAD], f32x4_t (&acc)[DT]) {
   for (bool more = true; more;) {
 #pragma unroll
@@ -440,8 +472,8 @@ __device__ __forceinline__ void finish_delta(const GemmModule &m, const RowInfo 
     }
   }
 }
-template <int DT, int KT, int AHEAD>
-__device__ __forceinline__ void add_delta(const GemmModule &m, const RowInfo &ri, const V8Split (&v)[KT], int n0,
+template <int P, int DT, int KT, int AHEAD>
+__device__ __forceinline__ void add_delta(const GemmModule &m, const RowInfo &ri, const VPieces<P> (&v)[KT], int n0,
                                           BFrag<DT, KT> (&f)[AHEAD], f32x4_t (&acc)[DT]) {
   DeltaRows rows = delta_rows(ri);
   if constexpr (AHEAD == 1) {
@@ -1064,27 +1096,32 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
   uint8_t *yw = lds + C::RED + C::INFO + w * C::YWAVE;
   (void)yw;
   constexpr int WNT = C::GATED ? C::NT / 2 : C::NT;  // column tiles of a wave's output
-  // v of a row's adapter, scaled, as bf16 hi + lo
-  auto scale_v = [&](const f32x4_t (&raw)[DELTA ? KT : 1][2], const RowInfo &ri, V8Split *v) {
+  // v of a row's adapter, scaled, in bf16 pieces
+  constexpr int VP = C::I8 ? 2 : 3;
+  typedef VPieces<VP> v_t;
+  auto scale_v = [&](const f32x4_t (&raw)[DELTA ? KT : 1][2], const RowInfo &ri, v_t *v) {
 #pragma unroll
     for (int ks = 0; ks < (DELTA ? KT : 1); ++ks) {
       float vv[8];
       const int j0 = ks * 32 + g * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) vv[i] = j0 + i < ri.rank ? raw[ks][i / 4][i % 4] * ri.scale : 0.f;
-      v[ks] = split_v8(vv);
+      v[ks] = split_v<VP>(vv);
     }
   };
-  auto load_v = [&](const float *row, const RowInfo &ri, V8Split *v) {
-    constexpr int K = DELTA ? KT : 1;
+  typedef f32x4_t raw_t[DELTA ? KT : 1][2];
+  auto ask_v = [&](const float *row, const RowInfo &ri, raw_t &raw) {
     const float *src = row + g * 8;
-    f32x4_t raw[K][2];
 #pragma unroll
-    for (int ks = 0; ks < K; ++ks) {
+    for (int ks = 0; ks < (DELTA ? KT : 1); ++ks) {
       const bool von = ks * 32 + g * 8 < ri.rank;
       raw[ks][0] = von ? *(const f32x4_t *)(src + ks * 32) : f32x4_t{0.f, 0.f, 0.f, 0.f};
       raw[ks][1] = von ? *(const f32x4_t *)(src + ks * 32 + 4) : f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
+  };
+  auto load_v = [&](const float *row, const RowInfo &ri, v_t *v) {
+    raw_t raw;
+    ask_v(row, ri, raw);
     scale_v(raw, ri, v);
   };
   // DT column tiles of a row, packed and stored (TURN: put into LDS)
@@ -1109,7 +1146,9 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
 #pragma unroll
     for (int e0 = 0; e0 < C::NTE; e0 += C::DT) {
       const int nw0 = n0 + (wc * WNT + et0 + e0) * 16;
-      BFrag<C::DT, DELTA ? KT : 1> bg[C::AHEAD], bu[C::AHEAD];
+      // (with four of rank 64 the 128-row tile spills 14 registers: 128 rows over as many adapters 455 us, 415 with three)
+      constexpr int AH = C::RT == 128 && KT == 2 ? 3 : C::AHEAD;
+      BFrag<C::DT, DELTA ? KT : 1> bg[AH], bu[AH];
       (void)bg;
       (void)bu;
 #pragma unroll
@@ -1123,27 +1162,28 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
           by[e] = fin[C::NTE + e0 + e][mt];
         }
         if constexpr (DELTA) {
-          V8Split v[KT];
+          v_t v[KT];
           const RowInfo ru = info[C::IR + r];
           if constexpr (EARLY) {
             scale_v(vraw[0], ri, v);
-            finish_delta<C::DT, KT, EA>(m, ri, v, nw0, erows[0], ebf[0], out);
+            finish_delta(m, ri, v, nw0, erows[0], ebf[0], out);
             scale_v(vraw[1], ru, v);
-            finish_delta<C::DT, KT, EA>(m, ru, v, nw0, erows[1], ebf[1], by);
+            finish_delta(m, ru, v, nw0, erows[1], ebf[1], by);
           } else if constexpr (C::AHEAD == 1) {
             load_v(m.v + (int64_t)(row0 + r) * d.rs, ri, v);
-            add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bg, out);
+            add_delta(m, ri, v, nw0, bg, out);
             load_v(up.v + (int64_t)(row0 + r) * d.rs, ru, v);
-            add_delta<C::DT, KT, C::AHEAD>(m, ru, v, nw0, bu, by);
+            add_delta(m, ru, v, nw0, bu, by);
           } else {  // both projections' B under way at once
             DeltaRows rg = delta_rows(ri), rup = delta_rows(ru);
-            V8Split vu[KT];
+            raw_t raw;  // up's v: in pieces when gate's are done with (fewer registers)
             load_v(m.v + (int64_t)(row0 + r) * d.rs, ri, v);
-            load_v(up.v + (int64_t)(row0 + r) * d.rs, ru, vu);
+            ask_v(up.v + (int64_t)(row0 + r) * d.rs, ru, raw);
             begin_delta(m, ri, nw0, rg, bg);
             begin_delta(m, ru, nw0, rup, bu);
             finish_delta(m, ri, v, nw0, rg, bg, out);
-            finish_delta(m, ru, vu, nw0, rup, bu, by);
+            scale_v(raw, ru, v);
+            finish_delta(m, ru, v, nw0, rup, bu, by);
           }
         }
 #pragma unroll
@@ -1182,13 +1222,13 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
           }
         }
         if constexpr (DELTA) {
-          V8Split v[KT];
+          v_t v[KT];
           if constexpr (EARLY) {
             scale_v(vraw[0], ri, v);
-            finish_delta<C::DT, KT, EA>(m, ri, v, nw0, erows[0], ebf[0], out);
+            finish_delta(m, ri, v, nw0, erows[0], ebf[0], out);
           } else {
             load_v(m.v + (int64_t)(C::Q4 ? row0 + r : ri.b) * d.rs, ri, v);
-            add_delta<C::DT, KT, C::AHEAD>(m, ri, v, nw0, bf, out);
+            add_delta(m, ri, v, nw0, bf, out);
           }
         }
         put_out(mt, e0, nw0, ri.b, out);
