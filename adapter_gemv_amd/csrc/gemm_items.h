@@ -1298,26 +1298,36 @@ __device__ __forceinline__ u32x2 quant8(u32x4 p, QuantScale qs) {
   return u32x2{o[0], o[1]};
 }
 
-// The batch's rows by slot: first those of the segments, as the build sorted
-// them, then the rows whose id has no segment (base only, bad, dropped past the
-// caller's bound) in their own order.  A block places 256 of each; it counts
-// the rows without a segment before its own from the ids.
-__device__ __forceinline__ void order_block(const LayerDesc &d, const int32_t *ids, int32_t *order, int block) {
+// The slot up to which rows have their delta: segments come in ascending slot
+// order; later slots were dropped by the build, or their segments do not fit the
+// batch.
+__device__ __forceinline__ int last_slot(const LayerDesc &d) {
+  const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
+  return nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
+}
+__device__ __forceinline__ bool has_segment(const LayerDesc &d, int a, int last) {
+  return (unsigned)a < (unsigned)d.num_slots && a <= last;
+}
+
+// The batch's rows by slot, put(place, row): first those of the segments, as the
+// build sorted them, then the rows whose id has no segment (base only, bad, dropped
+// past the caller's bound) in their own order.  A block of 256 places as many of
+// each; it counts the rows without a segment before its own from the ids.  Places
+// that no row takes (ids other than those that the segments were built from) hold
+// row -1.
+template <typename F>
+__device__ __forceinline__ void by_slot_block(const LayerDesc &d, const int32_t *ids, int block, F put) {
   __shared__ int wsum[4];
   const int t = threadIdx.x, lane = t & 63, w = wave_id();
   const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
   const int nvalid = nseg > 0 ? min(max(d.seg_offsets[nseg], 0), d.num_rows) : 0;
-  const int last_slot = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
-  auto without = [&](int b) {
-    const int a = ids[b];
-    return !((unsigned)a < (unsigned)d.num_slots && a <= last_slot);
-  };
+  const int last = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
   const int b = block * 256 + t;
-  if (b < nvalid) order[b] = d.perm[b];
+  if (b < nvalid) put(b, d.perm[b]);
   int before = 0;
 #pragma unroll 8
-  for (int i = t; i < block * 256; i += 256) before += without(i);
-  const uint64_t mine = __ballot(b < d.num_rows && without(min(b, d.num_rows - 1)));
+  for (int i = t; i < block * 256; i += 256) before += !has_segment(d, ids[i], last);
+  const uint64_t mine = __ballot(b < d.num_rows && !has_segment(d, ids[min(b, d.num_rows - 1)], last));
 #pragma unroll
   for (int k = 32; k >= 1; k /= 2) before += __shfl_xor(before, k, 64);
   if (lane == 0) wsum[w] = before;
@@ -1326,9 +1336,15 @@ __device__ __forceinline__ void order_block(const LayerDesc &d, const int32_t *i
   __syncthreads();
   if (lane == 0) wsum[w] = __popcll(mine);
   __syncthreads();
+  const int end = nvalid + base + wsum[0] + wsum[1] + wsum[2] + wsum[3];
   for (int k = 0; k < w; ++k) base += wsum[k];
   const int at = nvalid + base + __popcll(mine & ((1ull << lane) - 1));
-  if ((mine >> lane & 1) && at < d.num_rows) order[at] = b;
+  if ((mine >> lane & 1) && at < d.num_rows) put(at, b);
+  if (block == (d.num_rows + 255) / 256 - 1)
+    for (int p = end + t; p < d.num_rows; p += 256) put(p, -1);
+}
+__device__ __forceinline__ void order_block(const LayerDesc &d, const int32_t *ids, int32_t *order, int block) {
+  by_slot_block(d, ids, block, [&](int place, int b) { order[place] = b; });
 }
 
 // `lanes` threads (a wave, or a block of 256) quantise one row, keeping REGS

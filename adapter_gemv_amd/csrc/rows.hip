@@ -10,18 +10,6 @@
 namespace lora {
 namespace {
 
-// The slot up to which rows have their delta: segments come in ascending slot
-// order; later slots were dropped by the build, or their segments do not fit the
-// batch.
-__device__ __forceinline__ int last_slot(const LayerDesc &d) {
-  const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
-  return nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
-}
-
-__device__ __forceinline__ bool has_segment(const LayerDesc &d, int a, int last) {
-  return (unsigned)a < (unsigned)d.num_slots && a <= last;
-}
-
 __device__ __forceinline__ RowInfo describe(const LayerDesc &d, int b, int a, bool on, const lora_adapter_entry_t &e) {
   RowInfo ri{};
   ri.b = b;
@@ -50,40 +38,15 @@ __device__ __forceinline__ void place_row(const RowsDesc &r, int place, int b, i
   }
 }
 
-// 256 rows.  By slot: first those of the segments, as the build sorted them, then
-// the rows without one in their own order; a block counts those before its own.
+// 256 rows.
 __device__ __forceinline__ void rows_block(const RowsDesc &r, int block) {
-  __shared__ int wsum[4];
-  const LayerDesc &d = r.L;
-  const int t = threadIdx.x, lane = t & 63, w = wave_id();
-  const int nseg = fitting_segments(d.num_segments, d.max_seg, d.seg_offsets, d.num_rows);
-  const int nvalid = nseg > 0 ? min(max(d.seg_offsets[nseg], 0), d.num_rows) : 0;
-  const int last = nseg > 0 ? d.seg_adapter[nseg - 1] : -1;
-  const int b = block * 256 + t;
-  if (!r.order) {
-    if (b < d.num_rows) place_row(r, b, b, last);
-    return;
+  const int last = last_slot(r.L);
+  if (r.order) {
+    by_slot_block(r.L, r.ids, block, [&](int place, int b) { place_row(r, place, b, last); });
+  } else {
+    const int b = block * 256 + threadIdx.x;
+    if (b < r.L.num_rows) place_row(r, b, b, last);
   }
-  if (b < nvalid) place_row(r, b, d.perm[b], last);
-  int before = 0;
-#pragma unroll 8
-  for (int i = t; i < block * 256; i += 256) before += !has_segment(d, r.ids[i], last);
-  const uint64_t mine = __ballot(b < d.num_rows && !has_segment(d, r.ids[min(b, d.num_rows - 1)], last));
-#pragma unroll
-  for (int k = 32; k >= 1; k /= 2) before += __shfl_xor(before, k, 64);
-  if (lane == 0) wsum[w] = before;
-  __syncthreads();
-  int base = wsum[0] + wsum[1] + wsum[2] + wsum[3];
-  __syncthreads();
-  if (lane == 0) wsum[w] = __popcll(mine);
-  __syncthreads();
-  const int end = nvalid + base + wsum[0] + wsum[1] + wsum[2] + wsum[3];
-  for (int k = 0; k < w; ++k) base += wsum[k];
-  const int at = nvalid + base + __popcll(mine & ((1ull << lane) - 1));
-  if ((mine >> lane & 1) && at < d.num_rows) place_row(r, at, b, last);
-  // ids other than those that the segments were built from: places left over hold no row
-  if (block == r.rows_blocks - 1)
-    for (int p = end + t; p < d.num_rows; p += 256) place_row(r, p, -1, last);
 }
 
 __global__ __launch_bounds__(256) void rows_kernel(RowsDesc r) {
