@@ -12,6 +12,7 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("no GPU", allow_module_level=True)
 
 import adapter_gemv_amd as lg  # noqa: E402
+from tests import test_gpu_ffn_adapted as adapted  # noqa: E402
 from tests import test_gpu_linear_i8 as i8  # noqa: E402
 
 
@@ -37,3 +38,44 @@ def test_int8_base_with_ids_other_than_the_segments(rows, kept):
     assert bool(torch.isnan(r.dev["q"].y[kept:]).all())
     ref, slack = r.reference("q")
     i8.close(r.out()["q"][:kept], ref[:kept], slack[:kept], "q")
+
+
+def longer(r, lengths, rows):
+    """Segments of these lengths, built for all their rows, and then a call for `rows`: the ones that do not fit."""
+    r.ids = np.repeat(np.arange(len(lengths)), lengths).astype(np.int32)
+    r.dids.copy_(torch.from_numpy(r.ids))
+    lg.build_segments(r.dids, r.slots, r.seg, r.ws)
+    return [s for s, end in enumerate(np.cumsum(lengths)) if end > rows]
+
+
+LENGTHS = [(40, 30, 20, 10), (3, 90, 4, 3), (64, 8, 7, 21)]
+
+
+@adapted.forms
+@pytest.mark.parametrize("lengths", LENGTHS)
+@pytest.mark.parametrize("rows", [20, 71, 97])
+def test_segments_of_a_longer_batch_are_counted_once(form, lengths, rows):
+    # (71 and 97 rows: by the grouped shrink, whose long segments two kinds of work items look at)
+    r = adapted.Run(form, sum(lengths), len(lengths), adapted.one(264, 136), 16)
+    out = longer(r, lengths, rows)
+    r.call(rows=rows)
+    torch.cuda.synchronize()
+    assert r.status() == len(out) > 0
+
+
+@pytest.mark.parametrize("lengths", LENGTHS)
+@pytest.mark.parametrize("rows", [20, 71, 97])
+@pytest.mark.parametrize("call", ["int8", "delta", "expand"])
+def test_older_calls_count_them_once(call, lengths, rows):
+    r = i8.Run(sum(lengths), len(lengths), {"q": (264, 136, "a")}, 16)
+    out = longer(r, lengths, rows)
+    r.rows, io = rows, r.dev["q"]
+    if call == "int8":
+        lg.linear_layer(*r.args())
+    elif call == "delta":
+        lg.apply_layer({"q": lg.ModuleIO(io.x, io.y, d_in=264, d_out=136)}, rows, r.table, r.slots, r.seg, 16, r.ws)
+    else:
+        v = torch.ones(rows, 16, device="cuda")
+        lg.expand(v, r.table, r.slots, 7, 0, r.seg, 16, io.y[:rows], r.ws)
+    torch.cuda.synchronize()
+    assert int(r.seg.status.item()) == len(out) > 0
