@@ -238,16 +238,23 @@ __device__ __forceinline__ int fitting_segments(const int32_t *num_segments, int
   return n;
 }
 
+// Whether rows [o0, o1) of slot a are a segment of this batch.  (The ends are
+// compared, not the length: o1 - o0 of damaged offsets may pass 32 bits.)
+__device__ __forceinline__ bool segment_fits(int a, int o0, int o1, int num_slots, int num_rows) {
+  return (unsigned)a < (unsigned)num_slots && o0 >= 0 && o1 > o0 && o1 <= num_rows;
+}
+
 // Validated segment of a block: slot, first sorted row and length; false
 // (and the status word counted once) when the segments do not fit this batch.
 __device__ __forceinline__ bool load_segment(const LayerDesc &d, int s, bool count, int *a, int *pos0, int *len) {
   *a = uniform(d.seg_adapter[s]);
   *pos0 = uniform(d.seg_offsets[s]);
-  *len = uniform(d.seg_offsets[s + 1]) - *pos0;
-  if ((unsigned)*a >= (unsigned)d.num_slots || *pos0 < 0 || *len <= 0 || *pos0 + *len > d.num_rows) {
+  const int end = uniform(d.seg_offsets[s + 1]);
+  if (!segment_fits(*a, *pos0, end, d.num_slots, d.num_rows)) {
     if (count && threadIdx.x == 0) atomicAdd(d.status, 1);
     return false;
   }
+  *len = end - *pos0;
   return true;
 }
 

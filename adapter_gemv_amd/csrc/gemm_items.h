@@ -168,10 +168,9 @@ __device__ __forceinline__ int seg_tiles(const GemmDesc &d, int s, int nseg, int
   if (s >= (AT_ONCE ? d.max_seg : nseg)) return 0;
   *slot = d.seg_adapter[s];
   *o0 = d.seg_offsets[s];
-  *len = d.seg_offsets[s + 1] - *o0;
-  if (AT_ONCE && s >= nseg) *len = 0;
-  const bool ok = (unsigned)*slot < (unsigned)d.num_slots && *o0 >= 0 && *len > 0 && *o0 + *len <= d.num_rows;
-  if (!ok) *len = 0;
+  const int end = d.seg_offsets[s + 1];
+  const bool ok = segment_fits(*slot, *o0, end, d.num_slots, d.num_rows) && (!AT_ONCE || s < nseg);
+  *len = ok ? end - *o0 : 0;
   return (*len + RT - 1) / RT;
 }
 __device__ __forceinline__ int wave_scan(int v, int lane) {  // inclusive
@@ -566,8 +565,8 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     const int nseg = min(uniform(*d.num_segments), d.max_seg);
     if (blockIdx.x == 0 && w == 0)  // segments that do not fit the batch, counted once per call
       for (int s = lane; s < nseg; s += 64) {
-        const int a = d.seg_adapter[s], o0 = d.seg_offsets[s], o1 = d.seg_offsets[s + 1];
-        if ((unsigned)a >= (unsigned)d.num_slots || o0 < 0 || o1 <= o0 || o1 > d.num_rows) atomicAdd(d.status, 1);
+        if (!segment_fits(d.seg_adapter[s], d.seg_offsets[s], d.seg_offsets[s + 1], d.num_slots, d.num_rows))
+          atomicAdd(d.status, 1);
       }
     int rt;
     TileOf tile;

@@ -91,8 +91,8 @@ __global__ __launch_bounds__(256) void few_rows_kernel(RowsDesc r) {
   }
   if (blockIdx.x == 0 && w == 0) {  // segments that do not fit the batch, once a call
     for (int s = lane; s < nseg; s += 64) {
-      const int o0 = d.seg_offsets[s], o1 = d.seg_offsets[s + 1];
-      if ((unsigned)d.seg_adapter[s] >= (unsigned)d.num_slots || o0 < 0 || o1 <= o0 || o1 > d.num_rows) atomicAdd(d.status, 1);
+      if (!segment_fits(d.seg_adapter[s], d.seg_offsets[s], d.seg_offsets[s + 1], d.num_slots, d.num_rows))
+        atomicAdd(d.status, 1);
     }
   }
   if (j == 0 && t == 0) {

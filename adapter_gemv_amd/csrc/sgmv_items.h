@@ -52,8 +52,9 @@ __device__ __forceinline__ bool find_long_tile(const LayerDesc &d, int tile, int
     const int s = s0 + lane;
     int tl = 0;
     if (s < nseg) {
-      const int len = d.seg_offsets[s + 1] - d.seg_offsets[s];
-      tl = len >= d.long_min ? (len + rows - 1) / rows : 0;
+      const int o0 = d.seg_offsets[s], o1 = d.seg_offsets[s + 1];
+      if (segment_fits(d.seg_adapter[s], o0, o1, d.num_slots, d.num_rows) && o1 - o0 >= d.long_min)
+        tl = (o1 - o0 + rows - 1) / rows;
     }
     int inc = tl;
 #pragma unroll

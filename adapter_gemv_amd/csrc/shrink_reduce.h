@@ -30,7 +30,8 @@ __device__ __forceinline__ void shrink_reduce(const LayerDesc &d, int block, int
   if ((unsigned)a >= (unsigned)d.num_slots) return;
   const lora_adapter_entry_t e = d.table[(int64_t)a * d.table_cols + m.col];  // varies per lane
   // a segment that does not fit the batch was skipped by the shrink: no delta
-  const bool ok = entry_ok(e, d.max_rank) && d.seg_offsets[lo + 1] <= d.num_rows;
+  const int o0 = d.seg_offsets[lo], o1 = d.seg_offsets[lo + 1];
+  const bool ok = entry_ok(e, d.max_rank) && o0 >= 0 && o0 <= p && p < o1 && o1 <= d.num_rows;
   float sum = 0.f;
   if (ok && j < e.rank)
     for (int c = 0; c < m.n_chunks; ++c) sum += d.part[((int64_t)(m.part_base + c) * d.num_rows + p) * d.rs + j];

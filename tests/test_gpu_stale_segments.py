@@ -13,6 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 import adapter_gemv_amd as lg  # noqa: E402
 from tests import test_gpu_ffn_adapted as adapted  # noqa: E402
+from tests import test_gpu_ffn_grouped as grouped  # noqa: E402
 from tests import test_gpu_linear_i8 as i8  # noqa: E402
 
 
@@ -79,3 +80,75 @@ def test_older_calls_count_them_once(call, lengths, rows):
         lg.expand(v, r.table, r.slots, 7, 0, r.seg, 16, io.y[:rows], r.ws)
     torch.cuda.synchronize()
     assert int(r.seg.status.item()) == len(out) > 0
+
+
+# An end below the smallest length's start wraps a 32-bit difference round to a large length: segment 1 is (40, END),
+# segment 2 (END, 90).
+ENDS = [-2 ** 31, -2 ** 31 + 39, -1, 0, 40, 101, 2 ** 31 - 1]
+FOUR = (40, 30, 20, 10)
+
+
+def damaged(r, end):
+    """(segments that do not fit, for each row the segments that hold it): an end of 0 or 40 makes segment 2 one that
+    fits, over rows of others."""
+    longer(r, FOUR, 100)
+    r.seg.seg_offsets[2] = end
+    offsets = [0, 40, end, 90, 100]
+    fit = [s for s in range(4) if 0 <= offsets[s] < offsets[s + 1] <= 100]
+    return [s for s in range(4) if s not in fit], [[s for s in fit if offsets[s] <= b < offsets[s + 1]] for b in range(100)]
+
+
+@adapted.forms
+@pytest.mark.parametrize("end", ENDS)
+def test_damaged_offsets_with_adapters(form, end):
+    r = adapted.Run(form, 100, 4, adapted.one(264, 136), 16, pad=8)
+    bad, _ = damaged(r, end)
+    r.out("gate").fill_(7.0)
+    r.call()
+    torch.cuda.synchronize()
+    assert r.status() == len(bad) > 0
+    y = r.out("gate")[:, :136]
+    assert bool(torch.isfinite(y).all()) and bool((r.out("gate")[:, 136:] == 7).all())
+
+
+@grouped.forms
+@pytest.mark.parametrize("end", ENDS)
+def test_damaged_offsets_by_slot(form, end):
+    r = grouped.Run(form, np.repeat(np.arange(4), FOUR), 4, grouped.one(264, 136), pad=8)
+    bad, holds = damaged(r, end)
+    r.dev["gate"].y.fill_(7.0)
+    if r.is_gated and r.group:
+        lg.grouped_gated_layer_q4g(r.dev["gate"], 100, r.table, 4, r.seg, r.group)
+    elif r.is_gated:
+        lg.grouped_gated_layer(r.dev["gate"], 100, r.table, 4, r.seg)
+    else:
+        lg.grouped_layer_q4g(r.dev, 100, r.table, 4, r.seg, r.group)
+    torch.cuda.synchronize()
+    assert r.status() == len(bad) > 0
+    y = r.dev["gate"].y
+    assert bool((y[:, 136:] == 7).all())
+    # (segments that overlap hold more rows than the batch, and more tiles than the grid has blocks for)
+    for s in range(4) if all(len(h) <= 1 for h in holds) else ():
+        at = np.array([b for b in range(100) if holds[b] == [s]], int)
+        if len(at):
+            ref, slack = r.reference("gate", s, at)
+            grouped.close(y[torch.from_numpy(at).cuda()][:, :136], ref, slack, f"segment {s}")
+    none = torch.tensor([b for b in range(100) if not holds[b]], dtype=torch.long, device="cuda")
+    assert bool((y[none] == 7).all())
+
+
+@pytest.mark.parametrize("end", ENDS)
+def test_damaged_offsets_of_the_older_calls(end):
+    r = i8.Run(100, 4, {"q": (264, 136, "a")}, 16)
+    bad, holds = damaged(r, end)
+    io = r.dev["q"]
+    io.y.fill_(7.0)
+    lg.apply_layer({"q": lg.ModuleIO(io.x, io.y, d_in=264, d_out=136)}, 100, r.table, r.slots, r.seg, 16, r.ws)
+    torch.cuda.synchronize()
+    assert int(r.seg.status.item()) == len(bad) > 0
+    same = (io.y == 7).all(1).cpu()
+    assert [bool(v) for v in same] == [not h for h in holds]
+    r.seg.status.zero_()
+    lg.linear_layer(*r.args())
+    torch.cuda.synchronize()
+    assert int(r.seg.status.item()) == len(bad) and bool(torch.isfinite(io.y).all())
