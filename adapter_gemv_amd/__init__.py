@@ -747,6 +747,8 @@ def _grouped_array(ios, num_rows, weights, num_slots, seg, what):
         yp, ldy = _rows(io.y, bf16, num_rows, io.d_out, dev, name, "y")
         _GROUPED_PACK.pack_into(arr, i * _GROUPED_PACK.size, xp, ldx, yp, ldy, io.d_in, io.d_out, fan, 0)
         mask |= 1 << i
+    if seg.perm.size(0) < num_rows:  # the kernels read the segments beside their number: as many as the rows could have
+        raise ValueError("Segments buffers too small for this batch")
     _one_device(dev, (seg.perm,), what)
     return arr, mask
 
