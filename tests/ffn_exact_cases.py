@@ -4,6 +4,12 @@ functions here).  Everything is torch on the CPU; `on_gpu` runs a case through t
 Exact cases: inputs are small whole numbers and powers of two (or scales of 10 bits), chosen so that every partial sum, in
 any order, is a multiple of one step below 2^24 of it.  fp32 then rounds nowhere, and an output is the 64-bit result
 rounded once: equal, bit for bit.  A gate of 90 and more makes both activations its own value (sigma rounds to 1).
+
+Tight cases: inputs as in use.  The error's root mean square may be 1.01 times that of rounding the 64-bit result to
+bf16 once.  That leaves what comes before the rounding 14% of its step's: about 2^-9 / sqrt(3) * 0.14 = 1.6e-4 of a value.
+Rounding errors of fp32 sums that are not of one sign make about sqrt(n) * 2^-24 of a partial sum's magnitude, which for
+the (24 + q) x of 4-bit weights of one bit (q = -1, 0, 1) is 24 / 0.8 of the sum's own: 1e-4 at n = 2^13 if every sum went
+through one chain, and 2e-5 with the group's sums apart, as they are.
 """
 from __future__ import annotations
 
@@ -61,7 +67,7 @@ def whole(kind, group, ids, slots, d_in, d_out, rank=0, seed=0, act="silu", fan=
     big = {32: 15, 64: 14, 128: 13}[G]
     if rank and n >= 4:
         e[n // 2], e[1] = big, 8
-    e[0] = 5
+    e[0] = 5 if d_in < 4096 else 6  # (gates of 90 and more: four times 7 of this size above the other columns' spread)
     x_rows = -(-c.rows // fan)
     x = ints(-1, 1, x_rows, d_in) * ints(0, 1, x_rows, d_in)
     x[:, :G] = 0
@@ -95,6 +101,47 @@ def whole(kind, group, ids, slots, d_in, d_out, rank=0, seed=0, act="silu", fan=
     return c
 
 
+def in_use(kind, group, ids, slots, d_in, d_out, rank=0, seed=0, act="silu", fan=1, low=-8, high=7):
+    """A tight case: unit normal x, weights and factors of the sizes that a layer has."""
+    c = Case(kind, group, ids, slots, d_in, d_out, rank, act, fan)
+    g = gen(seed + 99)
+    G = group or 32
+    n = -(-d_in // G)
+    c.x = torch.randn(-(-c.rows // fan), d_in, generator=g).to(torch.bfloat16)
+    for col in c.cols:
+        for s in range(1 if c.adapted else slots):
+            if group:
+                q = torch.randint(low, high + 1, (d_out, d_in), generator=g)
+                sc = (torch.rand(d_out, n, generator=g) + 0.5) * d_in ** -0.5 / max(abs(low), abs(high))
+                c.weight(col, q, sc)
+            else:
+                w = (torch.randn(d_out, d_in, generator=g) * d_in ** -0.5).to(torch.bfloat16)
+                c.weight(col, w, torch.ones(d_out, n))
+        for s in range(slots if rank else 0):
+            c.A[col].append((torch.randn(rank, d_in, generator=g) * d_in ** -0.5).to(torch.bfloat16))
+            c.B[col].append((torch.randn(d_out, rank, generator=g) * 0.5).to(torch.bfloat16))
+            c.scale[col].append(float(np.float32(0.5 + 0.3 * s)))
+    return c
+
+
+def act64(kind, z):
+    if kind == "silu":
+        return z * torch.sigmoid(z)
+    return 0.5 * z * (1 + torch.tanh((2 / np.pi) ** 0.5 * (z + 0.044715 * z ** 3)))
+
+
+def result(c, rounded=lambda col, y: y, W={}):
+    """(the call's outputs in fp64, the rows that it writes).  `rounded` and `W` plant mistakes: in a projection's sums, in
+    its weights."""
+    sums = {}
+    for col in c.cols:
+        y, on = c.sums(col, W.get(col))
+        sums[col] = rounded(col, y)
+    if not c.is_gated:
+        return sums["gate"], on
+    return act64(c.act, sums["gate"]) * sums["up"], on
+
+
 def once(c):
     """The outputs of an exact case: products of fp32 values rounded to fp32, then to bf16 (fp64 to bf16 in one step
     where nothing is multiplied).  act(g) is g."""
@@ -106,6 +153,12 @@ def once(c):
         assert torch.equal(u.float().double(), u)
         return (y.float() * u.float()).to(torch.bfloat16), on
     return y.float().to(torch.bfloat16), on
+
+
+def tight(got, ref):
+    """Whether got (bf16 or fp64) is as near to ref (fp64) as a rounding to bf16, by the root of the mean square."""
+    rms = lambda t: float(t.double().square().mean().sqrt())  # noqa: E731
+    return rms(got.double() - ref) <= 1.01 * rms(ref.to(torch.bfloat16).double() - ref)
 
 
 def packed(q, s, group, pad=0):

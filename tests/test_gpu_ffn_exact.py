@@ -1,11 +1,11 @@
-"""GPU tests of the 4-bit and gated products on inputs whose sums are exact in fp32: outputs equal the 64-bit result,
-rounded once."""
+"""GPU tests of the 4-bit and gated products that are tighter than a bound on every sum's error: on inputs whose sums are
+exact in fp32 outputs equal the 64-bit result, rounded once; on inputs as in use the error is a rounding's."""
 import numpy as np
 import pytest
 
 from tests.dense_cases import ids_of
 from tests.ffn_cases import TILE_SLOTS, TILES
-from tests.ffn_exact_cases import OnGpu, once, whole
+from tests.ffn_exact_cases import OnGpu, in_use, once, result, tight, whole
 from tests.parity import note
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +55,50 @@ def test_a_v_that_is_infinite(rows):
     assert bool((got[3:7] == float("inf")).all())
     got[3:7] = want[3:7]
     assert torch.equal(got, want)
+
+
+def batch(kind, rows):
+    """(ids, slots) of a listed tile's rows."""
+    if kind.startswith("grouped"):
+        return np.random.RandomState(1).permutation(np.repeat(np.arange(len(rows)), rows)), len(rows)
+    return ids_of("mixed", rows, TILE_SLOTS, rows), TILE_SLOTS
+
+
+# every 4-bit value; the ones whose sums are smallest beside the shift's 24; none
+@pytest.mark.parametrize("group,low,high", [(32, -8, 7), (64, -1, 1), (128, -8, 7), (128, 0, 0)])
+@pytest.mark.parametrize("kind,number,tile,rows,d_in,d_out", TILES)
+def test_scales_and_sums_in_fp32(kind, number, tile, rows, d_in, d_out, group, low, high):
+    if not kind.endswith("q4g"):
+        if group == 128:
+            return  # bf16: twice is enough
+        group = 0
+    ids, slots = batch(kind, rows)
+    equal(whole(KIND[kind], group, ids, slots, d_in, d_out, seed=number, act="gelu_tanh", low=low, high=high))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("low,high", [(-8, 7), (-1, 1)])
+@pytest.mark.parametrize("kind,number,tile,rows,d_in,d_out", TILES)
+def test_errors_are_a_roundings(kind, number, tile, rows, d_in, d_out, group, low, high):
+    if not kind.endswith("q4g"):
+        if (group, low) != (32, -8):
+            return
+        group = 0
+    ids, slots = batch(kind, rows)
+    rank = 0 if kind.startswith("grouped") else {32: 40, 64: 5, 128: 16}[group or 128]
+    c = in_use(KIND[kind], group, ids, slots, d_in, d_out, rank, seed=number, act="gelu_tanh" if number % 2 else "silu",
+               low=low, high=high)
+    ref, on = result(c)
+    got = OnGpu(c).run()
+    assert tight(got[on], ref[on])
+    assert bool(torch.isnan(got[~on]).all())
+
+
+@pytest.mark.parametrize("fan", [2, 3])
+@pytest.mark.parametrize("kind,group", [("grouped", 64), ("grouped_gated", 0), ("grouped_gated", 128)])
+def test_rows_that_share_an_x(kind, group, fan):
+    ids = ids_of("mixed", 131, 5, fan)
+    equal(whole(kind, group, ids, 5, 1152, 200, fan=fan))
+    c = in_use(kind, group, ids, 5, 1152, 200, fan=fan)
+    ref, on = result(c)
+    assert tight(OnGpu(c).run()[on], ref[on])
