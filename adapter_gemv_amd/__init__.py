@@ -362,7 +362,9 @@ class LinearQ4IO:
     """One projection for linear_layer_q4: x [rows, >= d_in] bf16, Wq uint8
     [d_out, >= d_in / 2] (packed signed 4-bit weights, the even input in the
     low nibble), Ws float32 [d_out, >= d_in / Q4_GROUP] (group scales), y
-    [rows, >= d_out] bf16 (written)."""
+    [rows, >= d_out] bf16 (written).  LinearQ4GIO with group 128 takes the same
+    weight and is faster at every batch; this one has linear_shrink and
+    linear_expand."""
 
     def __init__(self, x, Wq, Ws, y, d_in=None, d_out=None):
         self.x, self.Wq, self.Ws, self.y = x, Wq, Ws, y

@@ -17,7 +17,8 @@ __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::E
 // adapters of rank 16 1293, 732, 468, [262], 414 (1.18 GB with their B, 4.7 TB/s of
 // the whole call); 7637 rows 256 x 256 [5826], 128 x 128 8596 (1.22 PFLOP/s with
 // the epilogue; the matrix cores busy for 60% of the cycles).  128 rows x 96
-// columns, two blocks a unit, 343 where 128 x 128 takes 262: not kept.
+// columns, two blocks a unit, 343 where 128 x 128 takes 262: not kept.  Registers:
+// 256 x 256 by slot spills 2, the others none.
 //                   I8     RT   NC  WR WC WK  KB  S EU  PIPE   Q4    GATED
 using Gated16 = GemmCfg<false, 16, 64, 1, 1, 4, 512, 2, 2, false, false, true>;
 using Gated32 = GemmCfg<false, 32, 64, 1, 1, 4, 256, 3, 2, false, false, true>;

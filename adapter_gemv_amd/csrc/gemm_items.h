@@ -505,8 +505,10 @@ __device__ __forceinline__ u32x2 pack_out(f32x4_t o) {
 // (q + 8) / 16.  Two values at a time take a shift and one operation (and, then
 // exclusive or with 1.5), eight for a register; converting each value took 15.
 // The sum over them is (sum q x + 24 sum x) / 16, so it starts from -24/16 sum x,
-// one matrix-core step for every tile of the same x.  Its rounding is that of 24
-// + |q| instead of |q|, at most 39/8 times more of an fp32 sum.
+// one matrix-core step for every tile of the same x.  Its rounding is that of sums
+// of up to (|q| + 48) |x|, times the scale: 2^-24 of them an addition, far below
+// a bf16 output's own for weights of any use, but no small part of a sum that is
+// itself near 0: a group of zeros leaves up to that, where converted weights leave 0.
 constexpr uint32_t kQ4Less = 0xBFC0BFC0u;  // -24/16 twice
 __device__ __forceinline__ u32x4 q4x8_shifted(uint32_t q) {
   auto two = [](uint32_t v) { return (v & 0x00780078u) ^ 0x3FC03FC0u; };
@@ -521,8 +523,9 @@ __device__ __forceinline__ u32x4 pairs_apart(u32x4 x) {
 // act(z) = z sigma(z (c1 + c3 z^2)): SiLU with c1 = 1, c3 = 0; GELU in its tanh form
 // with c1 = 2 sqrt(2 / pi), c3 = 0.044715 c1, since (1 + tanh(t)) / 2 = sigma(2t).
 // The square is bounded so that 0 * z^2 stays 0; at 1e30 sigma is 0 or 1 already.
-// exp and the reciprocal are the hardware's, within 2^-21 relative together: a
-// 2^13th of the output's rounding.
+// exp and the reciprocal are the hardware's: a few 2^-24 relative, and |t| 2^-24
+// (1 - sigma) of t's own rounding and its product with log2 e, which is 2^-18 where
+// sigma is smallest (t = -87; below, 0): a 2^9th of the output's rounding at most.
 __device__ __forceinline__ float gate_act(float z, float c1, float c3) {
   const float t = z * fmaf(c3, fminf(z * z, 1e30f), c1);
   return z * __builtin_amdgcn_rcpf(1.f + __expf(-t));
@@ -923,9 +926,10 @@ __device__ __forceinline__ void gemm_block(const GemmDesc &d, uint8_t *lds) {
     };
     if constexpr (C::Q4) {
       // A wave multiplies CH steps of 32 inputs that share their scales, then adds
-      // the products to the sums with them: s * sum_k (q / 16) x, each product
-      // exact, the scale in fp32.  CH is as long as the group and the wave's part of
-      // a stage allow, or one step.
+      // the products to the sums with them: s * (sum_k ((24 + q) / 16) x - 24/16
+      // sum_k x), each product exact, the scale in fp32.  CH is as long as the group
+      // and the wave's part of a stage allow, or one step, so that a group's sum
+      // meets its scale in one part or two.
       const u32x4 less = u32x4{kQ4Less, kQ4Less, kQ4Less, kQ4Less};
       int now = -1, s_get = 0;  // the batch of scales in use and its place
       auto scales_of = [&](int stage) {

@@ -7,18 +7,21 @@ namespace lora {
 
 // x is bf16, so that a tile of few columns moves as much x as W: wide tiles where
 // W is wide, 4 rows of x where there are no more.  A wave splits k with three or
-// seven others up to 32 rows.  Measured on one MI355X, us of a pass:
-//  * one row, gate and up of 8192 x 28672: 4 x 32 [60], 4 x 64 [57], 16 x 64 59;
+// seven others up to 32 rows.  Measured on one MI355X, us of a pass (in brackets what
+// the rule of pick_gemm takes):
+//  * one row, gate and up of 8192 x 28672: 4 x 32 60, 4 x 64 [57], 16 x 64 59;
 //    q/k/v/o: [28], 38, 39; with 3 stages (fewer blocks a unit) 64, 4 x 64 on 1024
 //    bytes 65.
-//  * 32 slots x 4 rows of 8192 x 8192: 16 x 64 [209], 16 x 128 211, 4 x 64 255;
-//    16 x 64 with 3 stages 235.  16 rows, gate and up: 16 x 128 66, 16 x 64 83.
+//  * 32 slots x 4 rows of 8192 x 8192: 16 x 64 209, 16 x 128 [211], 4 x 64 255;
+//    16 x 64 with 3 stages 235.  16 rows, gate and up: 16 x 128 [66], 16 x 64 83.
 //  * 8 slots x 16 rows, gate and up: 32 x 128 with k by four waves [421], columns and
 //    k by two 434 to 469, columns by four 478; 16 x 128 477, 16 x 64 484; 64 rows 605.
-//  * 1024 rows, gate and up of 4096 x 8192: 64 x 256 218, 256 x 256 182, 32 x 128 269;
-//    4200 rows of 8192 x 28672: 256 x 256 [5850] (0.9 PFLOP/s; in groups of 32 6914),
+//  * 1024 rows, gate and up of 4096 x 8192: 64 x 256 218, 256 x 256 [182], 32 x 128 269;
+//    5592 rows of 8192 x 28672: 256 x 256 [5850] (0.9 PFLOP/s; in groups of 32 6914),
 //    64 x 256 7086, 256 x 256 on waves of 128 x 64 9047, 256 x 128 on four waves
 //    8158.  128 x 128 stays within 3% of 64 x 256 everywhere: not kept.
+//  * Registers: 256 x 256 spills, around its epilogue, 4 with adapters of rank up to
+//    32 (gated), 8 and 10 above; the others fit.
 //  * few blocks (4d, 16d): 8 waves on long stages, see pick_gemm.
 //                                                    I8     RT   NC  WR WC WK  KB  S EU  PIPE   Q4
 template <bool GATED> using Q4Cfg4n = GemmCfg<false, 4, 32, 1, 1, 4, 1024, 2, 2, false, true, GATED>;

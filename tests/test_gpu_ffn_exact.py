@@ -102,3 +102,24 @@ def test_rows_that_share_an_x(kind, group, fan):
     c = in_use(kind, group, ids, 5, 1152, 200, fan=fan)
     ref, on = result(c)
     assert tight(OnGpu(c).run()[on], ref[on])
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind,number,tile,rows,d_in,d_out", [c for c in TILES if c[0] in ("linear_q4g", "grouped_q4g")])
+def test_weights_of_zeros(kind, number, tile, rows, d_in, d_out, group):
+    # what the shift leaves is within the bound of the sums' errors; nothing where the scale is 0
+    ids, slots = batch(kind, rows)
+    c = in_use(KIND[kind], group, ids, slots, d_in, d_out, seed=number, low=0, high=0)
+    for col in c.cols:
+        for W, q, s in c.W[col]:
+            s.copy_(torch.rand(s.shape, generator=torch.Generator().manual_seed(1)) + 0.5)
+            s[::2] = 0
+    got = OnGpu(c).run()
+    _, on = result(c)
+    scale = torch.stack([s.double().amax(1) for _, _, s in c.W["gate"]])  # the largest of an output
+    x = c.x.double().abs().sum(1)[:, None]
+    most = scale[torch.from_numpy(np.where(c.ids < slots, np.maximum(c.ids, 0), 0) if not c.adapted else np.zeros_like(c.ids))]
+    left = got[on].double().abs()
+    assert bool((left[:, ::2] == 0).all())
+    assert bool((left <= (2 * (2 * group + 4) * 2.0 ** -24 * 48 * (1 + 2.0 ** -8)) * (x * most)[on]).all())
+    print(f"[left] {kind} {number} group {group}: {float((left / (x * most + 1e-30)[on]).max()):.3g} of the scale times sum |x|")
