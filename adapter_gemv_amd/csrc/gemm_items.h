@@ -311,7 +311,7 @@ __device__ __forceinline__ void mma_settle(f32x4_t (&t)[N]) {
 }
 
 // Eight fp32 values of v as bf16 vectors, the largest piece first.  Two rounded
-// pieces hold 2^-16 of a value (split_v8: the int8 base); three cut ones hold all
+// pieces hold it to 2^-16 (split_v8: the int8 base); three cut ones hold all
 // of its 24 bits: 8 a piece, each remainder exact (a value that is infinite or no
 // number is its first piece), so that a delta that cancels the base leaves what the
 // formula leaves.  It is one matrix-core step more for an adapter and 16 rows: 16
