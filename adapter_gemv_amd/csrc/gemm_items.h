@@ -524,8 +524,9 @@ __device__ __forceinline__ u32x4 pairs_apart(u32x4 x) {
 // with c1 = 2 sqrt(2 / pi), c3 = 0.044715 c1, since (1 + tanh(t)) / 2 = sigma(2t).
 // The square is bounded so that 0 * z^2 stays 0; at 1e30 sigma is 0 or 1 already.
 // exp and the reciprocal are the hardware's: a few 2^-24 relative, and |t| 2^-24
-// (1 - sigma) of t's own rounding and its product with log2 e, which is 2^-18 where
-// sigma is smallest (t = -87; below, 0): a 2^9th of the output's rounding at most.
+// (1 - sigma) for each rounding of t and of its product with log2 e (SiLU one, GELU
+// four): 2^-17.5 and 2^-15.5 where sigma is smallest (t = -87; below, 0), less than
+// a 100th of the output's rounding.
 __device__ __forceinline__ float gate_act(float z, float c1, float c3) {
   const float t = z * fmaf(c3, fminf(z * z, 1e30f), c1);
   return z * __builtin_amdgcn_rcpf(1.f + __expf(-t));

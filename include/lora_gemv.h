@@ -483,9 +483,9 @@ typedef struct lora_linear_q4_io {
  * adapter).  The matrix cores take each 4-bit value exactly (as bf16) and
  * each group's sum is scaled once, in fp32.  It multiplies 128 rows at a time
  * for any batch: lora_linear_layer_q4g with group 128 takes the same weight and
- * factors in a fifth of the time for one row of 8192 x 8192, 0.74 of it for 128
- * rows of a layer and 0.6 from 1024 rows.  This one has the two parts below, and
- * no bound on the magnitudes of x.
+ * factors in a fifth of the time for one row of q, k, v and o, 0.74 of it for 128
+ * rows of a layer and 0.6 or less from 1024 rows.  This one has the two parts
+ * below, and no bound on the magnitudes of x.
  *
  *   io           array of LORA_NUM_MODULES entries, read where module_mask
  *                has a bit: x, Wq, y 16-byte aligned, Ws 4-byte aligned;

@@ -193,7 +193,7 @@ class OnGpu:
                         self.keep.append(t)
                     rk[s, k], sc[s, k] = c.rank, c.scale[col][s]
             host = lg.pack_table(ptr[0], ptr[1], rk, sc)
-            w = [t for col in c.cols for t in (packed(*c.W[col][0][1:], c.group) if c.group else (c.W[col][0][0].to(torch.bfloat16).cuda(),))]
+            w = [t for col in c.cols for t in self.weight(col, 0)]
             self.rank = max(c.rank, 1)
             if not c.is_gated:
                 self.ios = {"gate": lg.LinearQ4GIO(x, *w, self.y, c.group, d_in=c.d_in)}
@@ -205,7 +205,7 @@ class OnGpu:
             ld = np.zeros((2,) + shape, np.int64)
             for col in c.cols:
                 for s in range(c.slots):
-                    w = packed(*c.W[col][s][1:], c.group) if c.group else (c.W[col][s][0].to(torch.bfloat16).cuda(),)
+                    w = self.weight(col, s)
                     self.keep.append(w)
                     for i, t in enumerate(w):
                         ptr[i, s, MODS.index(col)], ld[i, s, MODS.index(col)] = t.data_ptr(), t.stride(0)
@@ -214,6 +214,10 @@ class OnGpu:
             n = lg.workspace_bytes(c.rows, c.slots, 1, 0)
         self.table = torch.from_numpy(host.view(np.uint8).reshape(-1).copy()).cuda()
         self.ws = torch.full((max(n, 16),), 0x7f, dtype=torch.uint8, device="cuda")
+
+    def weight(self, col, s):
+        W, q, scales = self.c.W[col][s]
+        return packed(q, scales, self.c.group) if self.c.group else (W.to(torch.bfloat16).cuda(),)
 
     def call(self, rows=None):
         import adapter_gemv_amd as lg
